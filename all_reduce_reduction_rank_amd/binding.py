@@ -10,6 +10,8 @@ C names (``include/ar.h``):
     comm.allgather(send, recv, ...)
     plan_bytes(nranks, op, count, dtype, algo, proto, ...)
     select(nranks, op, count, dtype, algo="auto", proto="auto", max_line_bytes_per_rank=0)
+    gated_ffn(x, w_gate, w_up, w_down, act="silu")                           # + gated_ffn_backward
+    linear_cross_entropy(x, w, target)                                       # + linear_cross_entropy_backward
 
 ``send`` / ``recv`` are lists of N contiguous CUDA (HIP) tensors on the
 communicator's device.  If the library is missing it is built once with hipcc;
@@ -29,6 +31,7 @@ PROTOS = {"simple": 0, "ll": 1, "ll128": 2}
 ALGO_AUTO, PROTO_AUTO = 4, 3  # AR_ALGO_AUTO / AR_PROTO_AUTO: the library picks (ar_select)
 DTYPES = {"f32": 0, "bf16": 1, "i32": 2}
 ESIZE = {"f32": 4, "bf16": 2, "i32": 4}
+ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 
 STATUS = {
     0: "AR_OK", 1: "AR_ERR_INVALID", 2: "AR_ERR_UNSUPPORTED", 3: "AR_ERR_NOMEM",
@@ -41,6 +44,8 @@ SYMBOLS = (
     "ar_comm_workspace_bytes", "ar_comm_set_max_workgroups", "ar_allreduce", "ar_allreduce_rmsnorm", "ar_reduce_scatter", "ar_allgather",
     "ar_plan_bytes", "ar_select", "ar_debug_inject", "ar_debug_state", "ar_status_string",
     "ar_allreduce_noalloc", "ar_debug_calls", "ar_stream_ceiling",
+    "ar_gated_ffn_workspace", "ar_gated_ffn", "ar_gated_ffn_backward",
+    "ar_linear_cross_entropy_workspace", "ar_linear_cross_entropy", "ar_linear_cross_entropy_backward",
 )
 
 
@@ -84,10 +89,18 @@ def _declare(lib):
                               ctypes.POINTER(ctypes.c_double)]
     lib.ar_debug_inject.argtypes = [P, I, I, U64]
     lib.ar_debug_state.argtypes = [P, P, ctypes.POINTER(U64), I]
+    lib.ar_gated_ffn_workspace.argtypes = [I, S, S, S, I, I]
+    lib.ar_gated_ffn.argtypes = [I] + [PP] * 7 + [S, S, S, I, I, P, S, P]
+    lib.ar_gated_ffn_backward.argtypes = [I] + [PP] * 11 + [S, S, S, I, I, P, S, P]
+    lib.ar_linear_cross_entropy_workspace.argtypes = [I, S, S, S, I, I, S]
+    lib.ar_linear_cross_entropy.argtypes = [I, PP, PP, P, PP, PP, S, S, S, I, P, S, P]
+    lib.ar_linear_cross_entropy_backward.argtypes = [I, P, PP, PP, P, PP, PP, PP, S, S, S, I, S, P, S, P]
     lib.ar_status_string.argtypes = [I]
     lib.ar_status_string.restype = ctypes.c_char_p
     for name in SYMBOLS:
-        if name not in ("ar_comm_workspace_bytes", "ar_status_string"):
+        if name in ("ar_gated_ffn_workspace", "ar_linear_cross_entropy_workspace"):
+            getattr(lib, name).restype = S
+        elif name not in ("ar_comm_workspace_bytes", "ar_status_string"):
             getattr(lib, name).restype = I
     return lib
 
@@ -373,6 +386,241 @@ def allreduce_noalloc(send, recv=None, algo="ring", proto="simple", chunk_bytes=
     _check(_lib().ar_allreduce_noalloc(n, s, r, count, DTYPES[dt], _algo(algo), _proto(proto), chunk_bytes,
                                        _stream_handle(stream, dev)), "ar_allreduce_noalloc")
     return recv
+
+
+# ---- operators of a tensor-parallel layer ----
+
+
+def _layer_ranks(first, what):
+    """(rank count, device index, dtype name) of a layer call, from its first
+    list of rank tensors; the current device is the call's device."""
+    n = len(first)
+    if not 1 <= n <= 8:
+        raise ValueError(f"{what} holds {n} rank buffers; a call has 1 to 8 ranks")
+    return n, first[0].get_device(), _dtype_name(first[0])
+
+
+def _layer_list(ts, n, shapes, dtype, device, what):
+    """Pointer array of N rank tensors after their checks; `shapes` is one
+    shape for all ranks or a list of N."""
+    if len(ts) != n:
+        raise ValueError(f"{what} holds {len(ts)} rank buffers; the call needs {n}")
+    ptrs = []
+    for i, t in enumerate(ts):
+        shape = shapes[i] if isinstance(shapes, list) else shapes
+        if t.dtype is not dtype:
+            raise TypeError(f"{what}[{i}] is {t.dtype}; the call needs {dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{what}[{i}] has shape {tuple(t.shape)}; the call needs {tuple(shape)}")
+        if t.get_device() != device or not t.is_contiguous():
+            raise ValueError(f"{what}[{i}] must be a contiguous tensor on the call's device")
+        ptrs.append(t.data_ptr())
+    return (ctypes.c_void_p * n)(*ptrs)
+
+
+def _layer_vector(t, rows, dtype, device, what):
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} is {t.dtype}; the call needs {dtype}")
+    if t.dim() != 1 or t.numel() != rows or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous vector of {rows} elements on the call's device")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _on_device(device):
+    """The call's tensors must be device tensors on the current device."""
+    import torch
+
+    if device < 0:
+        raise ValueError("rank buffers must be contiguous device tensors")
+    if device != torch.cuda.current_device():
+        raise ValueError("rank buffers must live on the current device")
+
+
+class _Scratch:
+    """Memory a call makes for itself (workspace, results the caller gave no
+    buffers for), allocated for the stream the call runs on."""
+
+    def __init__(self, stream, device):
+        self.stream, self.device = stream, device
+
+    def empty(self, shape, dtype):
+        import torch
+
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def workspace(self, nbytes):
+        ws = self.empty((nbytes,), _torch().uint8)
+        return ws, ctypes.c_void_p(ws.data_ptr())
+
+
+def _ffn_weights(x, w_gate, w_up, w_down):
+    """(n, device, dtype, dtype name, rows, hidden, inter, pointer arrays of the four)"""
+    n, device, dt = _layer_ranks(x, "x")
+    dtype = x[0].dtype
+    if x[0].dim() != 2:
+        raise ValueError("x must be [rows, hidden] on every rank")
+    rows, hidden = x[0].shape
+    if len(w_gate) != n or w_gate[0].dim() != 2:
+        raise ValueError(f"w_gate must be {n} matrices [inter, hidden]")
+    inter = w_gate[0].shape[0]
+    ptrs = [_layer_list(x, n, (rows, hidden), dtype, device, "x"),
+            _layer_list(w_gate, n, (inter, hidden), dtype, device, "w_gate"),
+            _layer_list(w_up, n, (inter, hidden), dtype, device, "w_up"),
+            _layer_list(w_down, n, (hidden, inter), dtype, device, "w_down")]
+    return n, device, dtype, dt, rows, hidden, inter, ptrs
+
+
+def _act(name):
+    if name not in ACTS:
+        raise ValueError(f"act must be one of {', '.join(ACTS)}; got {name!r}")
+    return ACTS[name]
+
+
+def gated_ffn(x, w_gate, w_up, w_down, out=None, gate=None, up=None, act="silu", stream=None):
+    """ar_gated_ffn: out[r] = (act(x[r] w_gate[r]^T) * (x[r] w_up[r]^T)) w_down[r]^T,
+    rank r's partial sum of a gated feed-forward block split over N = len(x)
+    ranks (``Comm.allreduce`` or ``Comm.allreduce_rmsnorm`` over ``out`` completes it).
+
+    x[r]: [rows, hidden]; w_gate[r], w_up[r]: [inter, hidden]; w_down[r]:
+    [hidden, inter]; out[r]: [rows, hidden], allocated when None.  gate, up:
+    None, or N tensors [rows, inter] that receive the two projections for
+    ``gated_ffn_backward``.  act: "silu", "gelu" or "gelu_tanh".  Runs on the
+    current device; fp32 and bf16."""
+    a = _act(act)
+    n, device, dtype, dt, rows, hidden, inter, ptrs = _ffn_weights(x, w_gate, w_up, w_down)
+    if (gate is None) != (up is None):
+        raise ValueError("gate and up are given together or not at all")
+    g = _layer_list(gate, n, (rows, inter), dtype, device, "gate") if gate is not None else None
+    u = _layer_list(up, n, (rows, inter), dtype, device, "up") if up is not None else None
+    o = _layer_list(out, n, (rows, hidden), dtype, device, "out") if out is not None else None
+    _on_device(device)
+    scratch = _Scratch(stream, device)
+    if out is None:
+        out = [scratch.empty((rows, hidden), dtype) for _ in range(n)]
+        o = (ctypes.c_void_p * n)(*[t.data_ptr() for t in out])
+    nbytes = _lib().ar_gated_ffn_workspace(n, rows, hidden, inter, DTYPES[dt], 0)
+    ws, ws_ptr = scratch.workspace(nbytes)
+    _check(_lib().ar_gated_ffn(n, *ptrs, o, g, u, rows, hidden, inter, a, DTYPES[dt], ws_ptr, nbytes,
+                               _stream_handle(stream, device)), "ar_gated_ffn")
+    return out
+
+
+def gated_ffn_backward(dout, x, w_gate, w_up, w_down, gate, up, dx=None, dw_gate=None, dw_up=None, dw_down=None,
+                       act="silu", stream=None):
+    """ar_gated_ffn_backward: (dx, dw_gate, dw_up, dw_down), lists of N tensors.
+
+    dout[r]: [rows, hidden], the gradient of the block's output; gate, up:
+    what ``gated_ffn`` stored.  dx[r] is rank r's partial sum (``Comm.allreduce``
+    completes it).  Results the caller gives no tensors for are allocated;
+    given ones are overwritten."""
+    a = _act(act)
+    n, device, dtype, dt, rows, hidden, inter, ptrs = _ffn_weights(x, w_gate, w_up, w_down)
+    d = _layer_list(dout, n, (rows, hidden), dtype, device, "dout")
+    g = _layer_list(gate, n, (rows, inter), dtype, device, "gate")
+    u = _layer_list(up, n, (rows, inter), dtype, device, "up")
+    results = [("dx", dx, (rows, hidden)), ("dw_gate", dw_gate, (inter, hidden)), ("dw_up", dw_up, (inter, hidden)),
+               ("dw_down", dw_down, (hidden, inter))]
+    given = [_layer_list(t, n, shape, dtype, device, what) if t is not None else None for what, t, shape in results]
+    _on_device(device)
+    scratch = _Scratch(stream, device)
+    outs = []
+    for i, (_, t, shape) in enumerate(results):
+        if t is None:
+            t = [scratch.empty(shape, dtype) for _ in range(n)]
+            given[i] = (ctypes.c_void_p * n)(*[v.data_ptr() for v in t])
+        outs.append(t)
+    nbytes = _lib().ar_gated_ffn_workspace(n, rows, hidden, inter, DTYPES[dt], 1)
+    ws, ws_ptr = scratch.workspace(nbytes)
+    _check(_lib().ar_gated_ffn_backward(n, d, *ptrs, g, u, *given, rows, hidden, inter, a, DTYPES[dt], ws_ptr, nbytes,
+                                        _stream_handle(stream, device)), "ar_gated_ffn_backward")
+    return tuple(outs)
+
+
+def vocab_shards(vocab, nranks):
+    """Vocabulary rows each rank holds: blocks of ceil(vocab / nranks)."""
+    b = -(-vocab // nranks)
+    return [min((r + 1) * b, vocab) - min(r * b, vocab) for r in range(nranks)]
+
+
+def _xent_inputs(x, w, target):
+    """(n, device, dtype, dtype name, rows, hidden, vocab, shards, pointers of x, w and target)"""
+    torch = _torch()
+    n, device, dt = _layer_ranks(x, "x")
+    dtype = x[0].dtype
+    if x[0].dim() != 2:
+        raise ValueError("x must be [rows, hidden] on every rank")
+    rows, hidden = x[0].shape
+    if len(w) != n or any(t.dim() != 2 for t in w):
+        raise ValueError(f"w must be {n} matrices [shard, hidden]")
+    vocab = sum(t.shape[0] for t in w)
+    shards = vocab_shards(vocab, n)
+    ptrs = [_layer_list(x, n, (rows, hidden), dtype, device, "x"),
+            _layer_list(w, n, [(v, hidden) for v in shards], dtype, device, "w"),
+            _layer_vector(target, rows, torch.int64, device, "target")]
+    return n, device, dtype, dt, rows, hidden, vocab, shards, ptrs
+
+
+def linear_cross_entropy(x, w, target, loss=None, lse=None, stream=None):
+    """ar_linear_cross_entropy: (loss, lse), lists of N fp32 vectors [rows].
+
+    The softmax cross entropy of logits x W^T against `target`, without the
+    logits, the vocabulary split over N = len(x) ranks: w[r] holds rank r's
+    ``vocab_shards(vocab, N)[r]`` rows of W [vocab, hidden]; x[r]: [rows,
+    hidden], the same on every rank; target: one int64 vector [rows]; rows whose
+    target is outside [0, vocab) have loss 0.  Every rank receives the whole
+    loss = lse - logit of the target, and lse, which the backward pass needs."""
+    torch = _torch()
+    n, device, _, dt, rows, hidden, vocab, _, ptrs = _xent_inputs(x, w, target)
+    given = [_layer_list(t, n, (rows,), torch.float32, device, what) if t is not None else None
+             for what, t in (("loss", loss), ("lse", lse))]
+    _on_device(device)
+    scratch = _Scratch(stream, device)
+    outs = []
+    for i, t in enumerate((loss, lse)):
+        if t is None:
+            t = [scratch.empty((rows,), torch.float32) for _ in range(n)]
+            given[i] = (ctypes.c_void_p * n)(*[v.data_ptr() for v in t])
+        outs.append(t)
+    nbytes = _lib().ar_linear_cross_entropy_workspace(n, rows, hidden, vocab, DTYPES[dt], 0, 0)
+    ws, ws_ptr = scratch.workspace(nbytes)
+    _check(_lib().ar_linear_cross_entropy(n, *ptrs, *given, rows, hidden, vocab, DTYPES[dt], ws_ptr, nbytes,
+                                          _stream_handle(stream, device)), "ar_linear_cross_entropy")
+    return tuple(outs)
+
+
+def linear_cross_entropy_backward(grad_loss, x, w, target, lse, dx=None, dw=None, piece=0, stream=None):
+    """ar_linear_cross_entropy_backward: (dx, dw), lists of N tensors shaped
+    like x and w.
+
+    grad_loss: fp32 vector [rows], the gradient of each row's loss; lse: what
+    ``linear_cross_entropy`` returned.  dx[r] is rank r's partial sum
+    (``Comm.allreduce`` completes it).  `piece`: vocabulary rows of each rank
+    worked on at a time (0: chosen by the library), which caps the workspace."""
+    torch = _torch()
+    n, device, dtype, dt, rows, hidden, vocab, shards, ptrs = _xent_inputs(x, w, target)
+    if piece < 0:
+        raise ValueError("piece must not be negative")
+    gl = _layer_vector(grad_loss, rows, torch.float32, device, "grad_loss")
+    z = _layer_list(lse, n, (rows,), torch.float32, device, "lse")
+    results = [("dx", dx, [(rows, hidden)] * n), ("dw", dw, [(v, hidden) for v in shards])]
+    given = [_layer_list(t, n, shapes, dtype, device, what) if t is not None else None for what, t, shapes in results]
+    _on_device(device)
+    scratch = _Scratch(stream, device)
+    outs = []
+    for i, (_, t, shapes) in enumerate(results):
+        if t is None:
+            t = [scratch.empty(shape, dtype) for shape in shapes]
+            given[i] = (ctypes.c_void_p * n)(*[v.data_ptr() for v in t])
+        outs.append(t)
+    nbytes = _lib().ar_linear_cross_entropy_workspace(n, rows, hidden, vocab, DTYPES[dt], 1, piece)
+    ws, ws_ptr = scratch.workspace(nbytes)
+    _check(_lib().ar_linear_cross_entropy_backward(n, gl, *ptrs, z, *given, rows, hidden, vocab, DTYPES[dt], piece,
+                                                   ws_ptr, nbytes, _stream_handle(stream, device)),
+           "ar_linear_cross_entropy_backward")
+    return tuple(outs)
 
 
 def stream_ceiling(src, dst, sink=None, nt_loads=False, nt_stores=False, unroll=8, wg_per_cu=0, stream=None):

@@ -1,0 +1,182 @@
+// ffn.hip -- the gated feed-forward block of a tensor-parallel layer
+// (ar_gated_ffn, ar_gated_ffn_backward): the work between the all-reduces
+// that the collectives page describes (a column split of the gate and up
+// projections, a row split of the down projection, partial sums left over).
+//
+// Forward, rank r:   g = x Wg^T, u = x Wu^T, h = act(g) u, out = h Wd^T.
+//   One launch makes h: its tiles hold the same columns of g and u side by
+//   side, so the activation and the product happen in registers.  One more
+//   multiplies by Wd.
+// Backward:  dh = dout Wd;  dg = dh u act'(g), du = dh act(g);
+//            dx = dg Wg + du Wu;  dWg = dg^T x, dWu = du^T x, dWd = dout^T h.
+//   dh never reaches memory: the tile that holds it writes dg, du and the
+//   h that dWd needs (recomputed from g and u: one store instead of keeping h
+//   from the forward pass).  dx is one product with two K segments.  The
+//   three weight gradients of every rank are one launch.
+//
+// Roundings to bf16 beside the stored results: h (the down projection's
+// operand), g and u (kept for the backward pass), dg and du (operands of the
+// matrix cores).  Each is half a bf16 step of the value, as large as the
+// rounding of the inputs themselves; every sum is fp32.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "../../include/ar.h"
+#include "layer.hpp"
+#include "products.hpp"
+
+using namespace ar;
+
+namespace {
+
+struct FfnShape {
+  uint64_t rows, hidden, inter, es, pitch;  // pitch: elements per row of h, dg, du (whole chunks)
+  uint64_t mid_bytes;                       // one rank's h (dg, du)
+};
+
+FfnShape shape_of(size_t rows, size_t hidden, size_t inter, int dtype) {
+  FfnShape s;
+  s.rows = rows, s.hidden = hidden, s.inter = inter;
+  s.es = dtype == DT_BF16 ? 2 : 4;
+  s.pitch = (inter + 7) / 8 * 8;
+  s.mid_bytes = layer_align(s.rows * s.pitch * s.es);
+  return s;
+}
+
+ar_status check_shape(int n, size_t rows, size_t hidden, size_t inter, int act, int dtype) {
+  if (n < 1 || n > MAX_RANKS || dtype < 0 || dtype > 2 || act < 0 || act > 2) return AR_ERR_INVALID;
+  if (hidden < 1 || inter < 1) return AR_ERR_INVALID;
+  if (dtype == DT_I32) return AR_ERR_UNSUPPORTED;
+  if (rows > LAYER_MAX_ROWS || hidden > LAYER_MAX_WIDTH || inter > LAYER_MAX_WIDTH) return AR_ERR_TOO_LARGE;
+  return AR_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ar_gated_ffn_workspace(int nranks, size_t rows, size_t hidden, size_t inter, ar_dtype dtype, int backward) {
+  if (check_shape(nranks, rows, hidden, inter, 0, (int)dtype) != AR_OK || rows == 0) return 0;
+  return (size_t)nranks * (backward ? 3 : 1) * shape_of(rows, hidden, inter, (int)dtype).mid_bytes;
+}
+
+ar_status ar_gated_ffn(int nranks, const void* const* x, const void* const* w_gate, const void* const* w_up,
+                       const void* const* w_down, void* const* out, void* const* gate, void* const* up, size_t rows,
+                       size_t hidden, size_t inter, ar_act act, ar_dtype dtype, void* workspace,
+                       size_t workspace_bytes, ar_stream_t stream) {
+  const ar_status st = check_shape(nranks, rows, hidden, inter, (int)act, (int)dtype);
+  if (st != AR_OK) return st;
+  if (!x || !w_gate || !w_up || !w_down || !out) return AR_ERR_INVALID;
+  if (rows == 0) return AR_OK;
+  const FfnShape s = shape_of(rows, hidden, inter, (int)dtype);
+  const uint64_t xb = s.rows * s.hidden * s.es, wb = s.hidden * s.inter * s.es, gb = s.rows * s.inter * s.es;
+  const uint64_t need = (uint64_t)nranks * s.mid_bytes;
+  LayerBuffers b;
+  for (int r = 0; r < nranks; ++r) {
+    b.in(x[r], xb);
+    b.in(w_gate[r], wb);
+    b.in(w_up[r], wb);
+    b.in(w_down[r], wb);
+    b.out(out[r], xb);
+    if (gate) b.out(gate[r], gb);
+    if (up) b.out(up[r], gb);
+  }
+  b.out(workspace, need);
+  if (!b.ok()) return AR_ERR_INVALID;
+  if (workspace_bytes < need) return AR_ERR_TOO_LARGE;
+  int dev = -1;
+  if (hipGetDevice(&dev) != hipSuccess) return AR_ERR_HIP;
+  char* ws = (char*)workspace;
+  auto h = [&](int r) { return ws + (uint64_t)r * s.mid_bytes; };
+
+  ProductPlan up_plan, down_plan;
+  for (int r = 0; r < nranks; ++r) {
+    Problem* p = up_plan.add(s.rows, s.inter, s.hidden, s.hidden, s.hidden, s.pitch, s.es);
+    p->a[0] = (const char*)x[r];
+    p->b[0] = (const char*)w_gate[r];
+    p->b[1] = (const char*)w_up[r];
+    p->c[0] = h(r);
+    p->c[1] = gate ? (char*)gate[r] : nullptr;
+    p->c[2] = up ? (char*)up[r] : nullptr;
+    p->mode = (uint32_t)act;
+    p = down_plan.add(s.rows, s.hidden, s.inter, s.pitch, s.inter, s.hidden, s.es);
+    p->a[0] = h(r);
+    p->b[0] = (const char*)w_down[r];
+    p->c[0] = (char*)out[r];
+  }
+  if (launch_products(PK_GATED, (int)dtype, up_plan, dev, (hipStream_t)stream) != hipSuccess) return AR_ERR_HIP;
+  if (launch_products(PK_STORE_NT, (int)dtype, down_plan, dev, (hipStream_t)stream) != hipSuccess) return AR_ERR_HIP;
+  return AR_OK;
+}
+
+ar_status ar_gated_ffn_backward(int nranks, const void* const* dout, const void* const* x, const void* const* w_gate,
+                                const void* const* w_up, const void* const* w_down, const void* const* gate,
+                                const void* const* up, void* const* dx, void* const* dw_gate, void* const* dw_up,
+                                void* const* dw_down, size_t rows, size_t hidden, size_t inter, ar_act act,
+                                ar_dtype dtype, void* workspace, size_t workspace_bytes, ar_stream_t stream) {
+  const ar_status st = check_shape(nranks, rows, hidden, inter, (int)act, (int)dtype);
+  if (st != AR_OK) return st;
+  if (!dout || !x || !w_gate || !w_up || !w_down || !gate || !up || !dx || !dw_gate || !dw_up || !dw_down)
+    return AR_ERR_INVALID;
+  const FfnShape s = shape_of(rows, hidden, inter, (int)dtype);
+  const uint64_t xb = s.rows * s.hidden * s.es, wb = s.hidden * s.inter * s.es, gb = s.rows * s.inter * s.es;
+  const uint64_t need = (uint64_t)nranks * 3 * (rows ? s.mid_bytes : 0);
+  LayerBuffers b;
+  for (int r = 0; r < nranks; ++r) {
+    b.in(dout[r], xb);
+    b.in(x[r], xb);
+    b.in(w_gate[r], wb);
+    b.in(w_up[r], wb);
+    b.in(w_down[r], wb);
+    b.in(gate[r], gb);
+    b.in(up[r], gb);
+    b.out(dx[r], xb);
+    b.out(dw_gate[r], wb);
+    b.out(dw_up[r], wb);
+    b.out(dw_down[r], wb);
+  }
+  b.out(workspace, need);
+  if (!b.ok()) return AR_ERR_INVALID;
+  if (workspace_bytes < need) return AR_ERR_TOO_LARGE;
+  int dev = -1;
+  if (hipGetDevice(&dev) != hipSuccess) return AR_ERR_HIP;
+  char* ws = (char*)workspace;
+  auto mid = [&](int r, int i) { return ws + ((uint64_t)r * 3 + i) * s.mid_bytes; };  // dg, du, h
+
+  // With no rows every weight gradient is a product with k = 0: zeros.
+  ProductPlan mid_plan, dx_plan, dw_plan;
+  dx_plan.a.nseg = 2;
+  for (int r = 0; r < nranks; ++r) {
+    Problem* p = mid_plan.add(s.rows, s.inter, s.hidden, s.hidden, s.inter, s.pitch, s.es);
+    p->a[0] = (const char*)dout[r];
+    p->b[0] = (const char*)w_down[r];
+    p->e[0] = (const char*)gate[r];
+    p->e[1] = (const char*)up[r];
+    for (int i = 0; i < 3; ++i) p->c[i] = mid(r, i);
+    p->mode = (uint32_t)act;
+    p = dx_plan.add(s.rows, s.hidden, s.inter, s.pitch, s.hidden, s.hidden, s.es);
+    p->a[0] = mid(r, 0);
+    p->a[1] = mid(r, 1);
+    p->b[0] = (const char*)w_gate[r];
+    p->b[1] = (const char*)w_up[r];
+    p->c[0] = (char*)dx[r];
+    for (int i = 0; i < 2; ++i) {
+      p = dw_plan.add(s.inter, s.hidden, s.rows, s.pitch, s.hidden, s.hidden, s.es);
+      p->a[0] = mid(r, i);
+      p->b[0] = (const char*)x[r];
+      p->c[0] = (char*)(i ? dw_up[r] : dw_gate[r]);
+    }
+    p = dw_plan.add(s.hidden, s.inter, s.rows, s.hidden, s.pitch, s.inter, s.es);
+    p->a[0] = (const char*)dout[r];
+    p->b[0] = mid(r, 2);
+    p->c[0] = (char*)dw_down[r];
+  }
+  if (launch_products(PK_GATED_BWD, (int)dtype, mid_plan, dev, (hipStream_t)stream) != hipSuccess ||
+      launch_products(PK_STORE_NN, (int)dtype, dx_plan, dev, (hipStream_t)stream) != hipSuccess ||
+      launch_products(PK_STORE_TN, (int)dtype, dw_plan, dev, (hipStream_t)stream) != hipSuccess)
+    return AR_ERR_HIP;
+  return AR_OK;
+}
+
+}  // extern "C"

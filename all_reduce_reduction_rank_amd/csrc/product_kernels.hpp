@@ -1,0 +1,235 @@
+// product_kernels.hpp -- the product kernels of the layer operators: one kernel
+// template over (type, layouts, epilogue, tile size, alignment), instantiated
+// per payload type by products_bf16.hip and products_f32.hip.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "products.hpp"
+
+namespace ar {
+
+namespace {
+
+// Value and derivative of the gate's activation, fp32.
+struct Act {
+  float v, d;
+};
+template <bool DERIV>
+__device__ __forceinline__ Act activate(float z, uint32_t act) {
+  Act r;
+  r.d = 0.f;
+  if (act == ACT_SILU) {
+    const float s = 1.0f / (1.0f + expf(-z));
+    r.v = z * s;
+    if (DERIV) r.d = s * (1.0f + z * (1.0f - s));
+  } else if (act == ACT_GELU) {
+    const float phi = 0.5f * erfcf(-0.70710678118654752f * z);  // erfc keeps the small tail's digits
+    r.v = z * phi;
+    if (DERIV) r.d = phi + z * 0.39894228040143268f * expf(-0.5f * z * z);
+  } else {
+    // tanh(y) = 2 s(2 y) - 1: (1 + tanh(y)) / 2 = s(2 y) = 1 / (1 + exp(-2 y))
+    // beyond +-64 s is 0 or 1 exactly; the clamp keeps z^3 and z^2 finite
+    const float k = 0.79788456080286536f, c = 0.044715f;
+    const float y = z > 64.f ? 64.f : z < -64.f ? -64.f : z;
+    const float s = 1.0f / (1.0f + expf(-2.0f * k * (y + c * y * y * y)));
+    r.v = z * s;
+    if (DERIV) r.d = s + 2.0f * y * s * (1.0f - s) * k * (1.0f + 3.0f * c * y * y);
+  }
+  return r;
+}
+
+// exp for probabilities.  bf16 gradients round far above the hardware
+// exponential's error (about |z| 2^-24 relative); fp32 takes the exact one.
+template <int DT>
+__device__ __forceinline__ float exp_of(float z) {
+  return DT == DT_BF16 ? __expf(z) : expf(z);
+}
+
+template <class P, int KIND>
+__global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
+  __shared__ __align__(1024) char smem[P::LDS_BYTES];
+  constexpr int DT = P::DT;
+  constexpr int ES = KElem<DT>::ES;
+  uint32_t row0, col0;
+  const Problem& p = a.p[locate<P>(a, &row0, &col0)];
+  P x;
+  x.run(p, a.nseg, row0, col0, smem);
+  const uint32_t m = p.m, n = p.n;
+  const uint64_t ldc = p.ldc;
+  const bool vec = (p.ldc & 3) == 0;
+
+  if constexpr (KIND == PK_STORE_NT || KIND == PK_STORE_NN || KIND == PK_STORE_TN) {
+    char* c = p.c[0];
+    x.visit([&](uint32_t r, uint32_t col, int i, int j) {
+      const uint64_t row = (uint64_t)row0 + r;
+      if (row >= m) return;
+      const float v[4] = {x.acc[i][j][0], x.acc[i][j][1], x.acc[i][j][2], x.acc[i][j][3]};
+      store4<DT>(c + row * ldc * ES, (uint64_t)col0 + col, n, vec, v);
+    });
+  } else if constexpr (KIND == PK_ACCUM_NN) {
+    const bool add = p.mode & ACC_ADD, last = p.mode & ACC_LAST;
+    x.visit([&](uint32_t r, uint32_t col, int i, int j) {
+      const uint64_t row = (uint64_t)row0 + r;
+      if (row >= m) return;
+      float v[4] = {x.acc[i][j][0], x.acc[i][j][1], x.acc[i][j][2], x.acc[i][j][3]};
+      char* sum = p.c[1] + row * ldc * 4;
+      if (add) {
+        float o[4];
+        load4<DT_F32>(sum, (uint64_t)col0 + col, n, vec, o);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = o[e] + v[e];
+      }
+      if (last) store4<DT>(p.c[0] + row * ldc * ES, (uint64_t)col0 + col, n, vec, v);
+      else store4<DT_F32>(sum, (uint64_t)col0 + col, n, vec, v);
+    });
+  } else if constexpr (KIND == PK_GATED) {
+    // h's storage has rows of whole chunks (ldc); g and u are n wide.
+    x.visit([&](uint32_t r, uint32_t col, int i, int j) {
+      const uint64_t row = (uint64_t)row0 + r;
+      if (row >= m) return;
+      float g[4], u[4], h[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        g[e] = x.acc[i][j][e];
+        u[e] = x.acc[i][j + P::TN / 2][e];
+        h[e] = activate<false>(g[e], p.mode).v * u[e];
+      }
+      // columns n .. ldc of h are written too (zeros: their g and u are)
+      store4<DT>(p.c[0] + row * ldc * ES, (uint64_t)col0 + col, p.ldc, vec, h);
+      if (p.c[1]) store4<DT>(p.c[1] + row * (uint64_t)n * ES, (uint64_t)col0 + col, n, (n & 3) == 0, g);
+      if (p.c[2]) store4<DT>(p.c[2] + row * (uint64_t)n * ES, (uint64_t)col0 + col, n, (n & 3) == 0, u);
+    });
+  } else if constexpr (KIND == PK_GATED_BWD) {
+    x.visit([&](uint32_t r, uint32_t col, int i, int j) {
+      const uint64_t row = (uint64_t)row0 + r;
+      if (row >= m) return;
+      float g[4], u[4], dg[4], du[4], h[4];
+      load4<DT>(p.e[0] + row * (uint64_t)n * ES, (uint64_t)col0 + col, n, (n & 3) == 0, g);
+      load4<DT>(p.e[1] + row * (uint64_t)n * ES, (uint64_t)col0 + col, n, (n & 3) == 0, u);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float dh = x.acc[i][j][e];
+        const Act f = activate<true>(g[e], p.mode);
+        dg[e] = dh * u[e] * f.d;
+        du[e] = dh * f.v;
+        h[e] = f.v * u[e];
+      }
+      store4<DT>(p.c[0] + row * ldc * ES, (uint64_t)col0 + col, p.ldc, vec, dg);
+      store4<DT>(p.c[1] + row * ldc * ES, (uint64_t)col0 + col, p.ldc, vec, du);
+      store4<DT>(p.c[2] + row * ldc * ES, (uint64_t)col0 + col, p.ldc, vec, h);
+    });
+  } else if constexpr (KIND == PK_DLOGITS) {
+    const float* lse = (const float*)p.e[0];
+    const uint32_t lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < P::TM; ++i) {
+      const uint64_t row = (uint64_t)row0 + P::wave_row() + 16 * i + (lane & 15);
+      if (row >= m) continue;
+      const int64_t t = a.target[row];
+      const bool live = t >= 0 && (uint64_t)t < a.vocab;
+      const float g = live ? a.grad[row] : 0.f;
+      const float z = lse[row];
+      const int64_t at = t - (int64_t)p.col0;  // the target's column here, if any
+#pragma unroll
+      for (int j = 0; j < P::TN; ++j) {
+        const uint32_t col = col0 + P::wave_col() + 16 * j + 4 * (lane >> 4);
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float q = exp_of<DT>(x.acc[i][j][e] - z) - ((int64_t)(col + e) == at ? 1.0f : 0.0f);
+          v[e] = live && col + e < n ? q * g : 0.f;
+        }
+        store4<DT>(p.c[0] + row * ldc * ES, col, p.ldc, vec, v);
+      }
+    }
+  } else {  // PK_STATS
+    __syncthreads();  // every wave is done with the tiles
+    float2* part = (float2*)smem;  // [WN][BM]
+    const uint32_t lane = threadIdx.x & 63;
+    const int wn = uniform((int)(threadIdx.x / 64)) % P::WN;
+#pragma unroll
+    for (int i = 0; i < P::TM; ++i) {
+      const uint32_t r = P::wave_row() + 16 * i + (lane & 15);
+      const uint64_t row = (uint64_t)row0 + r;
+      const int64_t t = row < m ? a.target[row] : -1;
+      const int64_t at = t - (int64_t)p.col0;
+      const bool live = t >= 0 && (uint64_t)t < a.vocab;
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < P::TN; ++j) {
+        const uint32_t col = col0 + P::wave_col() + 16 * j + 4 * (lane >> 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (col + e < n) {
+            top = fmaxf(top, x.acc[i][j][e]);
+            if (live && (int64_t)(col + e) == at) ((float*)p.c[1])[row] = x.acc[i][j][e];
+          }
+        }
+      }
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float shift = stats_shift(top);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < P::TN; ++j) {
+        const uint32_t col = col0 + P::wave_col() + 16 * j + 4 * (lane >> 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (col + e < n) sum += exp_of<DT>(x.acc[i][j][e] - shift);
+      }
+      sum += __shfl_xor(sum, 16);
+      sum += __shfl_xor(sum, 32);
+      if (lane < 16) part[wn * P::BM + r] = make_float2(top, sum);
+    }
+    __syncthreads();
+    for (uint32_t r = threadIdx.x; r < (uint32_t)P::BM; r += P::NT) {
+      const uint64_t row = (uint64_t)row0 + r;
+      if (row >= m) continue;
+      float2 s = part[r];
+#pragma unroll
+      for (int w = 1; w < P::WN; ++w) s = merge_stats(s, part[w * P::BM + r]);
+      ((float2*)p.c[0])[(uint64_t)(col0 / P::COLS) * m + row] = s;
+    }
+  }
+}
+
+constexpr int layout_a(int kind) { return kind == PK_STORE_TN ? L_R : L_K; }
+constexpr int layout_b(int kind) { return kind >= PK_STORE_NN ? L_R : L_K; }
+
+template <int KIND, int DT, bool ALIGNED, class TILE>
+hipError_t launch(ProductPlan& plan, hipStream_t stream) {
+  using P = Product<DT, layout_a(KIND), layout_b(KIND), KIND == PK_GATED, ALIGNED, TILE>;
+  if (!plan.cut(P::BM, P::COLS)) return hipErrorInvalidValue;
+  if (plan.tiles == 0) return hipSuccess;
+  hipLaunchKernelGGL((product_kernel<P, KIND>), dim3((unsigned)plan.tiles), dim3(P::NT), 0, stream, plan.a);
+  return hipGetLastError();
+}
+
+template <int KIND, int DT>
+hipError_t launch_kind(ProductPlan& plan, int device, hipStream_t stream) {
+  const bool large = product_tile(KIND, plan, device).bm == (uint32_t)Large::BM;
+  if (plan.aligned) return large ? launch<KIND, DT, true, Large>(plan, stream) : launch<KIND, DT, true, Small>(plan, stream);
+  return launch<KIND, DT, false, Small>(plan, stream);
+}
+
+template <int DT>
+hipError_t launch_typed(int kind, ProductPlan& plan, int device, hipStream_t stream) {
+  switch (kind) {
+    case PK_GATED: return launch_kind<PK_GATED, DT>(plan, device, stream);
+    case PK_STORE_NT: return launch_kind<PK_STORE_NT, DT>(plan, device, stream);
+    case PK_STATS: return launch_kind<PK_STATS, DT>(plan, device, stream);
+    case PK_DLOGITS: return launch_kind<PK_DLOGITS, DT>(plan, device, stream);
+    case PK_STORE_NN: return launch_kind<PK_STORE_NN, DT>(plan, device, stream);
+    case PK_GATED_BWD: return launch_kind<PK_GATED_BWD, DT>(plan, device, stream);
+    case PK_ACCUM_NN: return launch_kind<PK_ACCUM_NN, DT>(plan, device, stream);
+    case PK_STORE_TN: return launch_kind<PK_STORE_TN, DT>(plan, device, stream);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+}  // namespace ar

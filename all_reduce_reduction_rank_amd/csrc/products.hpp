@@ -1,0 +1,55 @@
+// products.hpp -- the product kernels (products_*.hip) by layout and
+// epilogue, as the layer operators launch them.
+#pragma once
+
+#include <math.h>
+
+#include "product.hpp"
+
+namespace ar {
+
+enum ProductKind : int {
+  // A, B: L_K, L_K (x W^T)
+  PK_GATED = 0,    // paired; c = {act(g) u, g, u} (c[1], c[2] may be null)
+  PK_STORE_NT,     // c[0] = C
+  PK_STATS,        // per row: c[0] = (max, sum of exponentials) of the tile, c[1] = target's logit
+  PK_DLOGITS,      // c[0] = (exp(C - lse) - onehot(target)) * grad
+  // A, B: L_K, L_R (dy W)
+  PK_STORE_NN,     // c[0] = C (two K segments when nseg is 2)
+  PK_GATED_BWD,    // C = dh, e = {g, u}; c = {dg, du, h}
+  PK_ACCUM_NN,     // C added up over launches in fp32 (Problem::mode, ACC_*)
+  // A, B: L_R, L_R (dy^T x)
+  PK_STORE_TN,
+};
+
+// Problem::mode of PK_ACCUM_NN
+enum : uint32_t { ACC_ADD = 1 /* add the fp32 sum so far (c[1]) */, ACC_LAST = 2 /* write c[0], else c[1] */ };
+// Problem::mode of PK_GATED, PK_GATED_BWD
+enum : uint32_t { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
+
+// The (max, sum of exp(v - max)) pairs of two sets of values, joined.  An
+// infinite max shifts by 0 instead, so that a set of -inf adds nothing and
+// +inf gives an infinite sum (not inf - inf).
+__device__ __forceinline__ float stats_shift(float top) { return fabsf(top) == INFINITY ? 0.f : top; }
+__device__ __forceinline__ float2 merge_stats(float2 x, float2 y) {
+  const float top = fmaxf(x.x, y.x), shift = stats_shift(top);
+  return make_float2(top, x.y * expf(stats_shift(x.x) - shift) + y.y * expf(stats_shift(y.x) - shift));
+}
+
+struct TileShape {
+  uint32_t bm, cols;  // rows and columns of C one tile covers
+};
+
+// Tile that a launch of this plan takes (its problems are final).  PK_STATS
+// writes one partial per row and `cols` columns.
+TileShape product_tile(int kind, const ProductPlan& plan, int device);
+constexpr uint32_t MIN_TILE_COLS = 128;  // of a kind that is not paired
+
+hipError_t launch_products_bf16(int kind, ProductPlan& plan, int device, hipStream_t stream);
+hipError_t launch_products_f32(int kind, ProductPlan& plan, int device, hipStream_t stream);
+inline hipError_t launch_products(int kind, int dtype, ProductPlan& plan, int device, hipStream_t stream) {
+  return dtype == DT_BF16 ? launch_products_bf16(kind, plan, device, stream)
+                          : launch_products_f32(kind, plan, device, stream);
+}
+
+}  // namespace ar

@@ -343,6 +343,104 @@ ar_status ar_debug_calls(ar_comm_t comm, ar_call_record* out, int max, int* n_ou
 ar_status ar_stream_ceiling(int nread, const void* const* src, int nwrite, void* const* dst, size_t bytes,
                             void* sink, int flags, int unroll, int wg_per_cu, ar_stream_t stream);
 
+/* ---- Operators of a tensor-parallel layer ([Q] "Direct answer": a column
+ * split followed by a row split leaves every rank a partial sum, which an
+ * all-reduce adds, twice per layer and once more for each gradient).  They
+ * make the partial sums the collectives above add.  Like the collectives they
+ * take HOST arrays of N (1..8) DEVICE pointers, one per simulated rank, 16-byte
+ * aligned and row-major without gaps, run every rank's program on the current
+ * HIP device in order on `stream`, and allocate nothing: scratch memory is the
+ * caller's `workspace` (a 16-byte aligned DEVICE buffer of at least the bytes
+ * the matching *_workspace function returns; its contents need not be kept
+ * between calls, and calls that may overlap in time, replays of captured
+ * graphs among them, need one each).  No communicator, no device waits.
+ * dtype: AR_F32 or AR_BF16 (AR_I32 returns AR_ERR_UNSUPPORTED); every sum is
+ * fp32.  Outputs and the workspace must not overlap any other buffer of the
+ * call; inputs may be the same buffer on several ranks.  A buffer of no
+ * elements may be NULL.  hidden and inter at most 2^20, rows and vocab at most
+ * 2^30 (AR_ERR_TOO_LARGE beyond, and for a workspace that is too small).
+ * Errors of all: AR_ERR_INVALID, AR_ERR_UNSUPPORTED, AR_ERR_TOO_LARGE,
+ * AR_ERR_HIP (a launch failed). */
+
+/* Activation of the gate: z s(z) with the logistic s; z Phi(z) with the normal
+ * distribution function; its tanh form
+ * z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2. */
+typedef enum { AR_ACT_SILU = 0, AR_ACT_GELU = 1, AR_ACT_GELU_TANH = 2 } ar_act;
+
+/* Workspace bytes of ar_gated_ffn (backward 0) or ar_gated_ffn_backward
+ * (backward 1); 0 for arguments the call refuses, and for rows 0. */
+size_t ar_gated_ffn_workspace(int nranks, size_t rows, size_t hidden, size_t inter, ar_dtype dtype, int backward);
+
+/* Gated feed-forward block.  Rank r holds `inter` of the inner features:
+ *   g = x[r] w_gate[r]^T,  u = x[r] w_up[r]^T        [rows, inter]
+ *   out[r] = (act(g) * u) w_down[r]^T                 [rows, hidden]
+ * with x [rows, hidden], w_gate and w_up [inter, hidden], w_down
+ * [hidden, inter].  out[r] is rank r's partial sum: ar_allreduce (or
+ * ar_allreduce_rmsnorm) over out[0..N-1] completes the block.
+ * gate, up: NULL, or N buffers [rows, inter] that receive g and u for the
+ * backward pass.  The inner product act(g) * u is rounded to dtype before it
+ * is multiplied by w_down.  rows 0: nothing is done. */
+ar_status ar_gated_ffn(int nranks, const void* const* x, const void* const* w_gate, const void* const* w_up,
+                       const void* const* w_down, void* const* out, void* const* gate, void* const* up, size_t rows,
+                       size_t hidden, size_t inter, ar_act act, ar_dtype dtype, void* workspace,
+                       size_t workspace_bytes, ar_stream_t stream);
+
+/* Gradients of ar_gated_ffn.  dout[r] [rows, hidden]: the gradient of the
+ * block's output (the same on every rank, as the all-reduce hands it back);
+ * gate, up: what the forward pass stored.
+ *   dh = dout w_down;  dg = dh * u * act'(g);  du = dh * act(g)
+ *   dx[r] = dg w_gate + du w_up                       [rows, hidden]
+ *   dw_gate = dg^T x;  dw_up = du^T x                 [inter, hidden]
+ *   dw_down = dout^T (act(g) * u)                     [hidden, inter]
+ * dx[r] is rank r's partial sum (an all-reduce completes it); every output is
+ * overwritten, not added to.  dg, du and act(g) * u are rounded to dtype
+ * before they are multiplied.  rows 0: the weight gradients become zeros. */
+ar_status ar_gated_ffn_backward(int nranks, const void* const* dout, const void* const* x, const void* const* w_gate,
+                                const void* const* w_up, const void* const* w_down, const void* const* gate,
+                                const void* const* up, void* const* dx, void* const* dw_gate, void* const* dw_up,
+                                void* const* dw_down, size_t rows, size_t hidden, size_t inter, ar_act act,
+                                ar_dtype dtype, void* workspace, size_t workspace_bytes, ar_stream_t stream);
+
+/* Workspace bytes of ar_linear_cross_entropy (backward 0; piece unused) or
+ * ar_linear_cross_entropy_backward (backward 1) with that `piece`; 0 for
+ * arguments the call refuses, and for rows 0. */
+size_t ar_linear_cross_entropy_workspace(int nranks, size_t rows, size_t hidden, size_t vocab, ar_dtype dtype,
+                                         int backward, size_t piece);
+
+/* Softmax cross entropy of the linear layer l = x W^T [rows, vocab] without
+ * storing l.  The vocabulary is split over the ranks by the blocks of
+ * ar_allreduce without their rounding: B = ceil(vocab / N), rank r holds rows
+ * [rB, min((r+1)B, vocab)) of W as w[r] (none at all where rB >= vocab).
+ *   lse[i] = log sum_v exp(l[i][v]);  loss[i] = lse[i] - l[i][target[i]]
+ * target: one DEVICE vector of `rows` int64 shared by all ranks.  A target
+ * outside [0, vocab) marks a row without loss: loss[i] = 0 (lse is still
+ * computed).  Every rank's loss[r] and lse[r] (fp32, rows each) receive the
+ * whole result: the ranks' maxima, sums and target logits are joined inside
+ * the call.  x[r] [rows, hidden] must hold the same values on every rank.
+ * rows 0: nothing is done. */
+ar_status ar_linear_cross_entropy(int nranks, const void* const* x, const void* const* w, const int64_t* target,
+                                  float* const* loss, float* const* lse, size_t rows, size_t hidden, size_t vocab,
+                                  ar_dtype dtype, void* workspace, size_t workspace_bytes, ar_stream_t stream);
+
+/* Gradients of ar_linear_cross_entropy.  grad_loss: one DEVICE fp32 vector
+ * (rows) shared by all ranks, the gradient of each row's loss; lse[r]: what
+ * the forward pass stored.
+ *   d[i][v] = (exp(l[i][v] - lse[i]) - (v == target[i])) * grad_loss[i],
+ *   0 in rows without loss (grad_loss is not looked at there)
+ *   dx[r] = d_r w[r]  [rows, hidden];  dw[r] = d_r^T x[r]  [shard, hidden]
+ * where d_r is rank r's columns of d.  dx[r] is rank r's partial sum (an
+ * all-reduce completes it); every output is overwritten.  The logits are
+ * computed again, `piece` vocabulary rows of each rank at a time (a multiple
+ * of 256 after rounding down, at least 256; 0: as many as keep d of all ranks
+ * within 1 GiB); d is rounded to dtype before it is multiplied, and dx is
+ * added up in fp32 and rounded once.  `piece` does not change dw.  rows 0: dw
+ * becomes zeros. */
+ar_status ar_linear_cross_entropy_backward(int nranks, const float* grad_loss, const void* const* x,
+                                           const void* const* w, const int64_t* target, const float* const* lse,
+                                           void* const* dx, void* const* dw, size_t rows, size_t hidden, size_t vocab,
+                                           ar_dtype dtype, size_t piece, void* workspace, size_t workspace_bytes,
+                                           ar_stream_t stream);
+
 /* Static description of a status code. */
 const char* ar_status_string(ar_status status);
 
