@@ -486,15 +486,16 @@ def gated_ffn(x, w_gate, w_up, w_down, out=None, gate=None, up=None, act="silu",
 
     x[r]: [rows, hidden]; w_gate[r], w_up[r]: [inter, hidden]; w_down[r]:
     [hidden, inter]; out[r]: [rows, hidden], allocated when None.  gate, up:
-    None, or N tensors [rows, inter] that receive the two projections for
+    None, or N fp32 tensors [rows, inter] that receive the two projections for
     ``gated_ffn_backward``.  act: "silu", "gelu" or "gelu_tanh".  Runs on the
     current device; fp32 and bf16."""
     a = _act(act)
     n, device, dtype, dt, rows, hidden, inter, ptrs = _ffn_weights(x, w_gate, w_up, w_down)
+    f32 = _torch().float32
     if (gate is None) != (up is None):
         raise ValueError("gate and up are given together or not at all")
-    g = _layer_list(gate, n, (rows, inter), dtype, device, "gate") if gate is not None else None
-    u = _layer_list(up, n, (rows, inter), dtype, device, "up") if up is not None else None
+    g = _layer_list(gate, n, (rows, inter), f32, device, "gate") if gate is not None else None
+    u = _layer_list(up, n, (rows, inter), f32, device, "up") if up is not None else None
     o = _layer_list(out, n, (rows, hidden), dtype, device, "out") if out is not None else None
     _on_device(device)
     scratch = _Scratch(stream, device)
@@ -518,9 +519,10 @@ def gated_ffn_backward(dout, x, w_gate, w_up, w_down, gate, up, dx=None, dw_gate
     given ones are overwritten."""
     a = _act(act)
     n, device, dtype, dt, rows, hidden, inter, ptrs = _ffn_weights(x, w_gate, w_up, w_down)
+    f32 = _torch().float32
     d = _layer_list(dout, n, (rows, hidden), dtype, device, "dout")
-    g = _layer_list(gate, n, (rows, inter), dtype, device, "gate")
-    u = _layer_list(up, n, (rows, inter), dtype, device, "up")
+    g = _layer_list(gate, n, (rows, inter), f32, device, "gate")
+    u = _layer_list(up, n, (rows, inter), f32, device, "up")
     results = [("dx", dx, (rows, hidden)), ("dw_gate", dw_gate, (inter, hidden)), ("dw_up", dw_up, (inter, hidden)),
                ("dw_down", dw_down, (hidden, inter))]
     given = [_layer_list(t, n, shape, dtype, device, what) if t is not None else None for what, t, shape in results]

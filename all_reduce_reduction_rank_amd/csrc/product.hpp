@@ -80,7 +80,7 @@ struct Problem {
   uint32_t m, n, k;
   uint32_t lda, ldb, ldc;  // elements between rows of storage
   uint32_t tiles_m, tiles_n, first;
-  uint32_t mode;  // epilogue variant
+  uint32_t mode;  // accumulation over launches
 };
 
 struct ProductArgs {
@@ -89,6 +89,7 @@ struct ProductArgs {
   const float* grad;      // cross entropy: per row
   uint64_t vocab;         // cross entropy: targets outside [0, vocab) are ignored
   int32_t nprob, nseg;
+  int32_t act;     // gated kinds
   uint32_t tiles;  // of all problems
 };
 
@@ -130,13 +131,14 @@ __device__ __forceinline__ v4u descriptor(const char* p, uint32_t bytes) {
 }
 
 // 16 bytes per lane from the buffer to LDS: lane l's land at dst + 16 l.
-// `dst` is uniform over the wave.  Inline, so that the compiler does not wait
+// `dst` and `soff` (added to every lane's offset) are uniform over the wave.  Inline, so that the compiler does not wait
 // for the load before the next LDS read of another buffer (the kernels wait
 // themselves, before the barrier that publishes a buffer); there is no output
 // register a load in flight could overwrite.
-__device__ __forceinline__ void load_to_lds(v4u rsrc, uint32_t off, lds_char* dst) {
+__device__ __forceinline__ void load_to_lds(v4u rsrc, uint32_t off, uint32_t soff, lds_char* dst) {
   const uint32_t at = uniform((uint32_t)(uintptr_t)dst);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(rsrc)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(at), "v"(off),
+               "s"(rsrc), "s"(soff)
                : "m0");
 }
 
@@ -147,6 +149,8 @@ struct TileLoader {
   static constexpr int ES = KElem<DT>::ES, E = KElem<DT>::E, BK = KElem<DT>::BK;
   static constexpr int SLOTS = ROWS * 8 / NT;  // 16-byte chunks per thread
   static constexpr int CH = LAYOUT == L_K ? 8 : ROWS * ES / 16;  // chunks of an LDS row
+  // slots after which a thread's swizzle repeats (its rows are NT / CH apart)
+  static constexpr int PERIOD = LAYOUT == L_K || NT / CH >= 16 ? 1 : 16 / (NT / CH);
   static_assert(!PAIR || (LAYOUT == L_K && (ROWS / 2) % (NT / 8) == 0), "a slot's rows lie in one matrix");
   static_assert(SLOTS >= 1, "");
 
@@ -200,24 +204,19 @@ struct TileLoader {
         rsrc[h] = descriptor(base[h] + (uint64_t)k0 * ldbytes, bytes);
       }
     }
+    uint32_t off[PERIOD];
 #pragma unroll
-    for (int i = 0; i < SLOTS; ++i) {
+    for (int i = 0; i < PERIOD; ++i) {
       uint32_t row, chunk;
       slot(i, &row, &chunk);
-      int h = 0;
-      if constexpr (PAIR) {
-        if (i >= SLOTS / 2) {
-          h = 1;
-          row -= ROWS / 2;
-        }
-      }
-      uint32_t off = row * ldbytes + chunk * 16;
-      if constexpr (LAYOUT == L_K) {
-        if (k0 + chunk * E >= k) off = OUT_OF_RANGE;
-      } else {
-        if (chunk * E >= rows) off = OUT_OF_RANGE;
-      }
-      load_to_lds(rsrc[h], off, dst + ((uint32_t)i * NT + wave * 64) * 16);
+      const bool in = LAYOUT == L_K ? k0 + chunk * E < k : chunk * E < rows;
+      off[i] = in ? row * ldbytes + chunk * 16 : OUT_OF_RANGE;
+    }
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) {
+      const int h = PAIR && i >= SLOTS / 2 ? 1 : 0;
+      const uint32_t turn = (uint32_t)((h ? i - SLOTS / 2 : i) / PERIOD * PERIOD);
+      load_to_lds(rsrc[h], off[i % PERIOD], turn * (NT / CH) * ldbytes, dst + ((uint32_t)i * NT + wave * 64) * 16);
     }
   }
 
@@ -309,12 +308,12 @@ __device__ __forceinline__ v4f mma(v4u first, v4u second, v4f acc) {
   }
 }
 
-// Tile sizes.  WM x WN waves share the BM x BN tile.
-struct Large {  // 8 waves of 128 x 64
-  static constexpr int BM = 256, BN = 256, WM = 2, WN = 4;
+// Tile sizes: WM x WN waves share the BM x BN tile, STAGES K steps of it in LDS.
+struct Large {  // 8 waves of 128 x 64, 128 KB of LDS: one workgroup per CU
+  static constexpr int BM = 256, BN = 256, WM = 2, WN = 4, STAGES = 2;
 };
-struct Small {  // 4 waves of 64 x 64
-  static constexpr int BM = 128, BN = 128, WM = 2, WN = 2;
+struct Small {  // 4 waves of 64 x 64, 64 KB: two workgroups per CU
+  static constexpr int BM = 128, BN = 128, WM = 2, WN = 2, STAGES = 2;
 };
 
 template <int DT_, int LA_, int LB_, bool PAIR_, bool ALIGNED_, class TILE_>
@@ -322,15 +321,16 @@ struct Product {
   static constexpr int DT = DT_, LA = LA_, LB = LB_;
   static constexpr bool PAIR = PAIR_, ALIGNED = ALIGNED_;
   using TILE = TILE_;
-  static constexpr int BM = TILE::BM, BN = TILE::BN, WM = TILE::WM, WN = TILE::WN;
+  static constexpr int BM = TILE::BM, BN = TILE::BN, WM = TILE::WM, WN = TILE::WN, STAGES = TILE::STAGES;
   static constexpr int NT = 64 * WM * WN;
   static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 blocks per wave
   static constexpr int COLS = PAIR ? BN / 2 : BN;             // columns of C a tile covers
   static constexpr int STAGE = (BM + BN) * KBYTES;
-  static constexpr int LDS_BYTES = 2 * STAGE;
+  static constexpr int LDS_BYTES = STAGES * STAGE;
 
   using LoadA = TileLoader<DT, LA, BM, NT, false, ALIGNED>;
   using LoadB = TileLoader<DT, LB, BN, NT, PAIR, ALIGNED>;
+  static constexpr int LOADS = LoadA::SLOTS + LoadB::SLOTS;  // direct loads per thread and K step
 
   v4f acc[TM][TN];
 
@@ -346,24 +346,50 @@ struct Product {
     else return wave_col() + 16 * j;
   }
 
-  __device__ __forceinline__ void step(const lds_char* lds) {
-    const lds_char* ta = lds;
-    const lds_char* tb = lds + BM * KBYTES;
+  // Fragment i of A and its share of B's fragments, of substep s.
+  __device__ __forceinline__ static void read(const lds_char* buf, int s, v4u* fa, v4u* fb, int i) {
+    fa[i] = LoadA::fragment(buf, wave_row() + 16 * i, s);
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      v4u fb[TN], fa[TM];
+    for (int j = i * TN / TM; j < (i + 1) * TN / TM; ++j)
+      fb[j] = LoadB::fragment(buf + BM * KBYTES, block_row(j), s);
+  }
+  __device__ __forceinline__ void multiply(const v4u* fa, const v4u* fb, int i) {
 #pragma unroll
-      for (int j = 0; j < TN; ++j) fb[j] = LoadB::fragment(tb, block_row(j), s);
-#pragma unroll
-      for (int i = 0; i < TM; ++i) fa[i] = LoadA::fragment(ta, wave_row() + 16 * i, s);
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = mma<DT>(fb[j], fa[i], acc[i][j]);
+    for (int j = 0; j < TN; ++j) acc[i][j] = mma<DT>(fb[j], fa[i], acc[i][j]);
+  }
+  // Order of a half step for the compiler: the LDS reads of the next half
+  // spread evenly over the first half of the products, so that neither waits
+  // for the other.
+  static constexpr int READS_A = LA == L_K ? 1 : DT == DT_BF16 ? 2 : 4;
+  static constexpr int READS_B = LB == L_K ? 1 : DT == DT_BF16 ? 2 : 4;
+  template <int I>
+  __device__ __forceinline__ static void interleave() {
+    constexpr int R = TM * READS_A + TN * READS_B, M = TM * TN * (DT == DT_BF16 ? 1 : 4), Q = M / 2;
+    if constexpr (I < R) {
+      __builtin_amdgcn_sched_group_barrier(0x8, (I + 1) * Q / R - I * Q / R, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      interleave<I + 1>();
+    } else {
+      __builtin_amdgcn_sched_group_barrier(0x8, M - Q, 0);
     }
+  }
+  // Every load of this wave but the youngest n has landed, and so has every
+  // LDS read; then the workgroup's barrier.
+  template <int N>
+  __device__ __forceinline__ static void landed() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"(N) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
   }
 
   // Accumulate the tile at (row0, col0) of problem p.
+  //
+  // Each K step is two half steps (16-byte fragments).  A half step
+  // multiplies fragments read during the one before, while it reads the next
+  // one's, so the matrix cores never wait for an LDS read.  In the middle of
+  // step t its last reads are done and step t + 1 must have landed: one
+  // barrier there frees step t's buffer for step t + STAGES and publishes
+  // the next.
   __device__ __forceinline__ void run(const Problem& p, int nseg, uint32_t row0, uint32_t col0, char* smem) {
     lds_char* lds = (lds_char*)smem;
 #pragma unroll
@@ -379,39 +405,62 @@ struct Product {
     lb[0].init(p.b[0], p.b[1], col0, p.n, p.k, p.ldb);
     la[1].init(p.a[1], nullptr, row0, p.m, p.k, p.lda);
     lb[1].init(p.b[1], nullptr, col0, p.n, p.k, p.ldb);
-    auto start = [&](uint32_t t, lds_char* dst) {
-      const bool second = t >= per;
-      LoadA a = la[0];
-      LoadB b = lb[0];
+    // Loader of step t's segment and its first k.  A step past the last one
+    // (t up to steps + STAGES - 1) starts past k: all of it reads as zero.
+    auto at = [&](uint32_t t, LoadA* a, LoadB* b) {
+      const bool second = nseg > 1 && t >= per;
+      *a = la[0];
+      *b = lb[0];
       if (second) {
-        a.base[0] = la[1].base[0];
-        b.base[0] = lb[1].base[0];
+        a->base[0] = la[1].base[0];
+        b->base[0] = lb[1].base[0];
       }
-      const uint32_t k0 = (second ? t - per : t) * KElem<DT>::BK;
-      a.load_direct(k0, dst);
-      b.load_direct(k0, dst + BM * KBYTES);
+      return (second ? t - per : t) * KElem<DT>::BK;
     };
+    v4u fa[2][TM], fb[2][TN];
     if constexpr (ALIGNED) {
-      start(0, lds);
+      auto start = [&](uint32_t t, lds_char* dst) {
+        LoadA a;
+        LoadB b;
+        const uint32_t k0 = at(t, &a, &b);
+        a.load_direct(k0, dst);
+        b.load_direct(k0, dst + BM * KBYTES);
+      };
+#pragma unroll
+      for (int t = 0; t < STAGES; ++t) start(t, lds + t * STAGE);
+      landed<(STAGES - 1) * LOADS>();
+#pragma unroll
+      for (int i = 0; i < TM; ++i) read(lds, 0, fa[0], fb[0], i);
+      uint32_t cur = 0;  // byte offset of step t's buffer
       for (uint32_t t = 0; t < steps; ++t) {
-        // This wave's loads of step t have landed; behind the barrier
-        // everyone's have, and the other buffer is free.
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        if (t + 1 < steps) start(t + 1, lds + ((t + 1) & 1) * STAGE);
-        step(lds + (t & 1) * STAGE);
+        const uint32_t next = cur + STAGE == (uint32_t)LDS_BYTES ? 0 : cur + STAGE;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          read(lds + cur, 1, fa[1], fb[1], i);
+          multiply(fa[0], fb[0], i);
+        }
+        interleave<0>();
+        landed<(STAGES - 2) * LOADS>();
+        // with two stages the wait is for every load, and steps past the last
+        // one need not be started to keep its count
+        if (STAGES > 2 || t + STAGES < steps) start(t + STAGES, lds + cur);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          read(lds + next, 0, fa[0], fb[0], i);  // (stale after the last step, and not used)
+          multiply(fa[1], fb[1], i);
+        }
+        interleave<0>();
+        cur = next;
       }
+      landed<0>();
     } else {
+      // through registers: step t + 1's loads are in flight while t is
+      // multiplied
       v4u ra[LoadA::SLOTS], rb[LoadB::SLOTS];
       auto fetch = [&](uint32_t t) {
-        const bool second = t >= per;
-        LoadA a = la[0];
-        LoadB b = lb[0];
-        if (second) {
-          a.base[0] = la[1].base[0];
-          b.base[0] = lb[1].base[0];
-        }
-        const uint32_t k0 = (second ? t - per : t) * KElem<DT>::BK;
+        LoadA a;
+        LoadB b;
+        const uint32_t k0 = at(t, &a, &b);
         a.load_regs(k0, ra);
         b.load_regs(k0, rb);
       };
@@ -422,68 +471,130 @@ struct Product {
         lb[0].store_regs(rb, buf + BM * KBYTES);
         __syncthreads();
         if (t + 1 < steps) fetch(t + 1);
-        step(buf);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+          for (int i = 0; i < TM; ++i) read(buf, s, fa[s], fb[s], i);
+#pragma unroll
+          for (int i = 0; i < TM; ++i) multiply(fa[s], fb[s], i);
+        }
       }
     }
   }
 
-  // Visit every group of 4 consecutive columns this lane holds:
-  // f(row, col, i, j) with C's local row and first column; block j of a
-  // paired product's second half is passed as its first half's partner.
-  template <class F>
-  __device__ __forceinline__ void visit(F&& f) {
+  // Hand the finished tile out by rows: a lane of the accumulators holds 4
+  // columns of 16 different rows, so they pass through LDS (fp32, at most
+  // LDS_BYTES at a time) and every thread takes V consecutive columns at a
+  // time, a wave whole rows: 16-byte loads and stores of whole lines.
+  // (Straight from the accumulators, 32 bytes of a row per store, a
+  // 256 x 256 tile took 73 us to write.)
+  // pre(row, col) loads what f needs, for U groups at once, before any of
+  // them is stored; f(row, col, v, w, x) gets the V values (w: of the paired
+  // product) and pre's result.  Rows and columns count from the tile's corner.
+  // 16-byte chunk c of a row sits at chunk c ^ (row & 15): the 16 rows of a
+  // write and the neighbouring chunks of a read fall on different banks.
+  template <int V, int U, class PRE, class F>
+  __device__ __forceinline__ void hand_out(char* smem, PRE&& pre, F&& f) {
+    constexpr int PHASES = (BM * BN * 4 + LDS_BYTES - 1) / LDS_BYTES;
+    constexpr int PART = TM / PHASES;  // blocks of a wave per phase
+    constexpr int ROWS = PART * 16 * WM, UNITS = ROWS * (COLS / V), ROUNDS = UNITS / (NT * U);
+    static_assert(TM % PHASES == 0 && UNITS % (NT * U) == 0, "");
     const uint32_t lane = threadIdx.x & 63;
+    float4* t = (float4*)smem;
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+    for (int ph = 0; ph < PHASES; ++ph) {
+      __syncthreads();
 #pragma unroll
-      for (int j = 0; j < (PAIR ? TN / 2 : TN); ++j)
-        f((uint32_t)wave_row() + 16 * i + (lane & 15), (uint32_t)wave_col() + 16 * j + 4 * (lane >> 4), i, j);
+      for (int i = 0; i < PART; ++i) {
+        const uint32_t r = (uint32_t)(wave_row() / (16 * TM) * (16 * PART) + 16 * i) + (lane & 15);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          const v4f v = acc[ph * PART + i][j];
+          const uint32_t chunk = (uint32_t)block_row(j) / 4 + (lane >> 4);
+          t[r * (BN / 4) + (chunk ^ (r & 15))] = make_float4(v[0], v[1], v[2], v[3]);
+        }
+      }
+      __syncthreads();
+#pragma unroll 1
+      for (int round = 0; round < ROUNDS; ++round) {
+        decltype(pre(0u, 0u)) x[U];
+        uint32_t row[U], col[U], at[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const uint32_t unit = (uint32_t)((round * U + u) * NT) + threadIdx.x;
+          const uint32_t r = unit / (COLS / V);
+          at[u] = r;
+          col[u] = unit % (COLS / V) * V;
+          row[u] = r / (16 * PART) * (16 * TM) + ph * PART * 16 + r % (16 * PART);
+          x[u] = pre(row[u], col[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float v[V], w[V];
+#pragma unroll
+          for (int q = 0; q < V / 4; ++q) {
+            const uint32_t chunk = col[u] / 4 + q, s = at[u] & 15;
+            const float4 a = t[at[u] * (BN / 4) + (chunk ^ s)];
+            v[4 * q] = a.x, v[4 * q + 1] = a.y, v[4 * q + 2] = a.z, v[4 * q + 3] = a.w;
+            if constexpr (PAIR) {
+              const float4 b = t[at[u] * (BN / 4) + ((chunk + BN / 8) ^ s)];
+              w[4 * q] = b.x, w[4 * q + 1] = b.y, w[4 * q + 2] = b.z, w[4 * q + 3] = b.w;
+            }
+          }
+          f(row[u], col[u], v, w, x[u]);
+        }
+      }
+    }
   }
 };
 
-// Store 4 consecutive values of a row (n left in the row) as the payload type.
-template <int DT>
-__device__ __forceinline__ void store4(char* row, uint64_t col, uint32_t n, bool vec, const float* v) {
-  if constexpr (DT == DT_BF16) {
-    const uint32_t h[4] = {bf16_round(v[0]), bf16_round(v[1]), bf16_round(v[2]), bf16_round(v[3])};
-    if (vec && col + 4 <= n) {
-      *(uint2*)(row + col * 2) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+// Store V consecutive values of a row as DT: columns col .. col + V of a row
+// with n.  `vec`: the row's storage allows 16-byte (V * esize) stores.
+template <int DT, int V>
+__device__ __forceinline__ void store_row(char* row, uint64_t col, uint32_t n, bool vec, const float* v) {
+  constexpr int ES = KElem<DT>::ES;
+  char* p = row + col * ES;
+  if (vec && col + V <= n) {
+    if constexpr (DT == DT_BF16) {
+      uint32_t h[V / 2];
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) h[e] = bf16_round(v[2 * e]) | (bf16_round(v[2 * e + 1]) << 16);
+      if constexpr (V == 8) *(uint4*)p = make_uint4(h[0], h[1], h[2], h[3]);
+      else *(uint2*)p = make_uint2(h[0], h[1]);
     } else {
-      for (int e = 0; e < 4; ++e)
-        if (col + e < n) *(uint16_t*)(row + (col + e) * 2) = (uint16_t)h[e];
+#pragma unroll
+      for (int e = 0; e < V; e += 4) *(float4*)(p + e * 4) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
     }
   } else {
-    if (vec && col + 4 <= n) {
-      *(float4*)(row + col * 4) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
-      for (int e = 0; e < 4; ++e)
-        if (col + e < n) *(float*)(row + (col + e) * 4) = v[e];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      if (col + e >= n) break;
+      if constexpr (DT == DT_BF16) *(uint16_t*)(p + e * 2) = (uint16_t)bf16_round(v[e]);
+      else *(float*)(p + e * 4) = v[e];
     }
   }
 }
 
-// Load 4 consecutive values of a row as floats (0 beyond n).
-template <int DT>
-__device__ __forceinline__ void load4(const char* row, uint64_t col, uint32_t n, bool vec, float* v) {
-  if constexpr (DT == DT_BF16) {
-    if (vec && col + 4 <= n) {
-      const uint2 x = *(const uint2*)(row + col * 2);
-      v[0] = __uint_as_float(x.x << 16);
-      v[1] = __uint_as_float(x.x & 0xffff0000u);
-      v[2] = __uint_as_float(x.y << 16);
-      v[3] = __uint_as_float(x.y & 0xffff0000u);
-    } else {
-      for (int e = 0; e < 4; ++e)
-        v[e] = col + e < n ? __uint_as_float((uint32_t)((const uint16_t*)row)[col + e] << 16) : 0.f;
+// V consecutive fp32 values of a row (0 beyond n).
+template <int V>
+struct Floats {
+  float v[V];
+};
+template <int V>
+__device__ __forceinline__ Floats<V> load_floats(const char* row, uint64_t col, uint32_t n, bool vec) {
+  Floats<V> r;
+  const float* p = (const float*)row + col;
+  if (vec && col + V <= n) {
+#pragma unroll
+    for (int e = 0; e < V; e += 4) {
+      const float4 x = *(const float4*)(p + e);
+      r.v[e] = x.x, r.v[e + 1] = x.y, r.v[e + 2] = x.z, r.v[e + 3] = x.w;
     }
   } else {
-    if (vec && col + 4 <= n) {
-      const float4 x = *(const float4*)(row + col * 4);
-      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-    } else {
-      for (int e = 0; e < 4; ++e) v[e] = col + e < n ? ((const float*)row)[col + e] : 0.f;
-    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) r.v[e] = col + e < n ? p[e] : 0.f;
   }
+  return r;
 }
 
 // Find this workgroup's problem and tile.  Returns the problem's index.

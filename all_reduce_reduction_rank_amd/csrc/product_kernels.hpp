@@ -17,15 +17,15 @@ namespace {
 struct Act {
   float v, d;
 };
-template <bool DERIV>
-__device__ __forceinline__ Act activate(float z, uint32_t act) {
+template <uint32_t ACT, bool DERIV>
+__device__ __forceinline__ Act activate(float z) {
   Act r;
   r.d = 0.f;
-  if (act == ACT_SILU) {
+  if constexpr (ACT == ACT_SILU) {
     const float s = 1.0f / (1.0f + expf(-z));
     r.v = z * s;
     if (DERIV) r.d = s * (1.0f + z * (1.0f - s));
-  } else if (act == ACT_GELU) {
+  } else if constexpr (ACT == ACT_GELU) {
     const float phi = 0.5f * erfcf(-0.70710678118654752f * z);  // erfc keeps the small tail's digits
     r.v = z * phi;
     if (DERIV) r.d = phi + z * 0.39894228040143268f * expf(-0.5f * z * z);
@@ -48,103 +48,125 @@ __device__ __forceinline__ float exp_of(float z) {
   return DT == DT_BF16 ? __expf(z) : expf(z);
 }
 
-template <class P, int KIND>
+struct Nothing {};
+
+// ACT: the gate's activation (gated kinds).
+template <class P, int KIND, uint32_t ACT>
 __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
   __shared__ __align__(1024) char smem[P::LDS_BYTES];
   constexpr int DT = P::DT;
   constexpr int ES = KElem<DT>::ES;
+  constexpr int V = KElem<DT>::E;  // values per 16-byte vector of the payload
   uint32_t row0, col0;
   const Problem& p = a.p[locate<P>(a, &row0, &col0)];
   P x;
   x.run(p, a.nseg, row0, col0, smem);
   const uint32_t m = p.m, n = p.n;
   const uint64_t ldc = p.ldc;
-  const bool vec = (p.ldc & 3) == 0;
+  const bool vec = p.ldc % V == 0;
+  auto nothing = [](uint32_t, uint32_t) { return Nothing(); };
 
   if constexpr (KIND == PK_STORE_NT || KIND == PK_STORE_NN || KIND == PK_STORE_TN) {
     char* c = p.c[0];
-    x.visit([&](uint32_t r, uint32_t col, int i, int j) {
+    x.template hand_out<V, 2>(smem, nothing, [&](uint32_t r, uint32_t col, float* v, float*, Nothing) {
       const uint64_t row = (uint64_t)row0 + r;
-      if (row >= m) return;
-      const float v[4] = {x.acc[i][j][0], x.acc[i][j][1], x.acc[i][j][2], x.acc[i][j][3]};
-      store4<DT>(c + row * ldc * ES, (uint64_t)col0 + col, n, vec, v);
+      if (row < m) store_row<DT, V>(c + row * ldc * ES, (uint64_t)col0 + col, n, vec, v);
     });
   } else if constexpr (KIND == PK_ACCUM_NN) {
     const bool add = p.mode & ACC_ADD, last = p.mode & ACC_LAST;
-    x.visit([&](uint32_t r, uint32_t col, int i, int j) {
-      const uint64_t row = (uint64_t)row0 + r;
-      if (row >= m) return;
-      float v[4] = {x.acc[i][j][0], x.acc[i][j][1], x.acc[i][j][2], x.acc[i][j][3]};
-      char* sum = p.c[1] + row * ldc * 4;
-      if (add) {
-        float o[4];
-        load4<DT_F32>(sum, (uint64_t)col0 + col, n, vec, o);
+    const bool fvec = p.ldc % 4 == 0;
+    x.template hand_out<V, 4>(
+        smem,
+        [&](uint32_t r, uint32_t col) {
+          const uint64_t row = (uint64_t)row0 + r;
+          Floats<V> o = {};
+          if (add && row < m) o = load_floats<V>(p.c[1] + row * ldc * 4, (uint64_t)col0 + col, n, fvec);
+          return o;
+        },
+        [&](uint32_t r, uint32_t col, float* v, float*, const Floats<V>& o) {
+          const uint64_t row = (uint64_t)row0 + r;
+          if (row >= m) return;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = o[e] + v[e];
-      }
-      if (last) store4<DT>(p.c[0] + row * ldc * ES, (uint64_t)col0 + col, n, vec, v);
-      else store4<DT_F32>(sum, (uint64_t)col0 + col, n, vec, v);
-    });
+          for (int e = 0; e < V; ++e) v[e] = add ? o.v[e] + v[e] : v[e];
+          if (last) store_row<DT, V>(p.c[0] + row * ldc * ES, (uint64_t)col0 + col, n, vec, v);
+          else store_row<DT_F32, V>(p.c[1] + row * ldc * 4, (uint64_t)col0 + col, n, fvec, v);
+        });
   } else if constexpr (KIND == PK_GATED) {
-    // h's storage has rows of whole chunks (ldc); g and u are n wide.
-    x.visit([&](uint32_t r, uint32_t col, int i, int j) {
+    // h's storage has rows of whole chunks (ldc), of which the last columns
+    // come out as zeros (their g and u are); g and u are n wide, fp32.
+    x.template hand_out<V, 2>(smem, nothing, [&](uint32_t r, uint32_t col, float* g, float* u, Nothing) {
       const uint64_t row = (uint64_t)row0 + r;
       if (row >= m) return;
-      float g[4], u[4], h[4];
+      float h[V];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        g[e] = x.acc[i][j][e];
-        u[e] = x.acc[i][j + P::TN / 2][e];
-        h[e] = activate<false>(g[e], p.mode).v * u[e];
+      for (int e = 0; e < V; ++e) h[e] = activate<ACT, false>(g[e]).v * u[e];
+      store_row<DT, V>(p.c[0] + row * ldc * ES, (uint64_t)col0 + col, p.ldc, vec, h);
+      if (p.c[1]) {
+        store_row<DT_F32, V>(p.c[1] + row * (uint64_t)n * 4, (uint64_t)col0 + col, n, n % 4 == 0, g);
+        store_row<DT_F32, V>(p.c[2] + row * (uint64_t)n * 4, (uint64_t)col0 + col, n, n % 4 == 0, u);
       }
-      // columns n .. ldc of h are written too (zeros: their g and u are)
-      store4<DT>(p.c[0] + row * ldc * ES, (uint64_t)col0 + col, p.ldc, vec, h);
-      if (p.c[1]) store4<DT>(p.c[1] + row * (uint64_t)n * ES, (uint64_t)col0 + col, n, (n & 3) == 0, g);
-      if (p.c[2]) store4<DT>(p.c[2] + row * (uint64_t)n * ES, (uint64_t)col0 + col, n, (n & 3) == 0, u);
     });
   } else if constexpr (KIND == PK_GATED_BWD) {
-    x.visit([&](uint32_t r, uint32_t col, int i, int j) {
-      const uint64_t row = (uint64_t)row0 + r;
-      if (row >= m) return;
-      float g[4], u[4], dg[4], du[4], h[4];
-      load4<DT>(p.e[0] + row * (uint64_t)n * ES, (uint64_t)col0 + col, n, (n & 3) == 0, g);
-      load4<DT>(p.e[1] + row * (uint64_t)n * ES, (uint64_t)col0 + col, n, (n & 3) == 0, u);
+    struct Pre {
+      Floats<V> g, u;
+    };
+    x.template hand_out<V, 4>(
+        smem,
+        [&](uint32_t r, uint32_t col) {
+          const uint64_t row = (uint64_t)row0 + r;
+          Pre q = {};
+          if (row < m) {
+            q.g = load_floats<V>(p.e[0] + row * (uint64_t)n * 4, (uint64_t)col0 + col, n, n % 4 == 0);
+            q.u = load_floats<V>(p.e[1] + row * (uint64_t)n * 4, (uint64_t)col0 + col, n, n % 4 == 0);
+          }
+          return q;
+        },
+        [&](uint32_t r, uint32_t col, float* dh, float*, const Pre& q) {
+          const uint64_t row = (uint64_t)row0 + r;
+          if (row >= m) return;
+          float dg[V], du[V], h[V];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float dh = x.acc[i][j][e];
-        const Act f = activate<true>(g[e], p.mode);
-        dg[e] = dh * u[e] * f.d;
-        du[e] = dh * f.v;
-        h[e] = f.v * u[e];
-      }
-      store4<DT>(p.c[0] + row * ldc * ES, (uint64_t)col0 + col, p.ldc, vec, dg);
-      store4<DT>(p.c[1] + row * ldc * ES, (uint64_t)col0 + col, p.ldc, vec, du);
-      store4<DT>(p.c[2] + row * ldc * ES, (uint64_t)col0 + col, p.ldc, vec, h);
-    });
+          for (int e = 0; e < V; ++e) {
+            const Act f = activate<ACT, true>(q.g.v[e]);
+            dg[e] = dh[e] * q.u.v[e] * f.d;
+            du[e] = dh[e] * f.v;
+            h[e] = f.v * q.u.v[e];
+          }
+          store_row<DT, V>(p.c[0] + row * ldc * ES, (uint64_t)col0 + col, p.ldc, vec, dg);
+          store_row<DT, V>(p.c[1] + row * ldc * ES, (uint64_t)col0 + col, p.ldc, vec, du);
+          store_row<DT, V>(p.c[2] + row * ldc * ES, (uint64_t)col0 + col, p.ldc, vec, h);
+        });
   } else if constexpr (KIND == PK_DLOGITS) {
-    const float* lse = (const float*)p.e[0];
-    const uint32_t lane = threadIdx.x & 63;
+    struct Row {
+      int64_t at;  // the target's column in this problem, if it lies there
+      float z, g;
+      bool live;
+    };
+    x.template hand_out<V, 4>(
+        smem,
+        [&](uint32_t r, uint32_t) {
+          const uint64_t row = (uint64_t)row0 + r;
+          Row q = {-1, 0.f, 0.f, false};
+          if (row < m) {
+            const int64_t t = a.target[row];
+            q.live = t >= 0 && (uint64_t)t < a.vocab;
+            q.at = t - (int64_t)p.col0;
+            q.z = ((const float*)p.e[0])[row];
+            q.g = a.grad[row];
+          }
+          return q;
+        },
+        [&](uint32_t r, uint32_t col, float* v, float*, const Row& q) {
+          const uint64_t row = (uint64_t)row0 + r;
+          if (row >= m) return;
 #pragma unroll
-    for (int i = 0; i < P::TM; ++i) {
-      const uint64_t row = (uint64_t)row0 + P::wave_row() + 16 * i + (lane & 15);
-      if (row >= m) continue;
-      const int64_t t = a.target[row];
-      const bool live = t >= 0 && (uint64_t)t < a.vocab;
-      const float g = live ? a.grad[row] : 0.f;
-      const float z = lse[row];
-      const int64_t at = t - (int64_t)p.col0;  // the target's column here, if any
-#pragma unroll
-      for (int j = 0; j < P::TN; ++j) {
-        const uint32_t col = col0 + P::wave_col() + 16 * j + 4 * (lane >> 4);
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float q = exp_of<DT>(x.acc[i][j][e] - z) - ((int64_t)(col + e) == at ? 1.0f : 0.0f);
-          v[e] = live && col + e < n ? q * g : 0.f;
-        }
-        store4<DT>(p.c[0] + row * ldc * ES, col, p.ldc, vec, v);
-      }
-    }
+          for (int e = 0; e < V; ++e) {
+            const uint32_t c = col0 + col + e;
+            const float d = (exp_of<DT>(v[e] - q.z) - ((int64_t)c == q.at ? 1.0f : 0.0f)) * q.g;
+            v[e] = q.live && c < n ? d : 0.f;  // columns n .. ldc: zeros
+          }
+          store_row<DT, V>(p.c[0] + row * ldc * ES, (uint64_t)col0 + col, p.ldc, vec, v);
+        });
   } else {  // PK_STATS
     __syncthreads();  // every wave is done with the tiles
     float2* part = (float2*)smem;  // [WN][BM]
@@ -199,31 +221,41 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
 constexpr int layout_a(int kind) { return kind == PK_STORE_TN ? L_R : L_K; }
 constexpr int layout_b(int kind) { return kind >= PK_STORE_NN ? L_R : L_K; }
 
-template <int KIND, int DT, bool ALIGNED, class TILE>
+template <int KIND, int DT, bool ALIGNED, class TILE, uint32_t ACT>
 hipError_t launch(ProductPlan& plan, hipStream_t stream) {
   using P = Product<DT, layout_a(KIND), layout_b(KIND), KIND == PK_GATED, ALIGNED, TILE>;
   if (!plan.cut(P::BM, P::COLS)) return hipErrorInvalidValue;
   if (plan.tiles == 0) return hipSuccess;
-  hipLaunchKernelGGL((product_kernel<P, KIND>), dim3((unsigned)plan.tiles), dim3(P::NT), 0, stream, plan.a);
+  hipLaunchKernelGGL((product_kernel<P, KIND, ACT>), dim3((unsigned)plan.tiles), dim3(P::NT), 0, stream, plan.a);
   return hipGetLastError();
 }
 
-template <int KIND, int DT>
+template <int KIND, int DT, uint32_t ACT = ACT_SILU>
 hipError_t launch_kind(ProductPlan& plan, int device, hipStream_t stream) {
   const bool large = product_tile(KIND, plan, device).bm == (uint32_t)Large::BM;
-  if (plan.aligned) return large ? launch<KIND, DT, true, Large>(plan, stream) : launch<KIND, DT, true, Small>(plan, stream);
-  return launch<KIND, DT, false, Small>(plan, stream);
+  if (!plan.aligned) return launch<KIND, DT, false, Small, ACT>(plan, stream);
+  return large ? launch<KIND, DT, true, Large, ACT>(plan, stream) : launch<KIND, DT, true, Small, ACT>(plan, stream);
+}
+
+template <int KIND, int DT>
+hipError_t launch_gated(ProductPlan& plan, int device, hipStream_t stream) {
+  switch (plan.a.act) {
+    case ACT_SILU: return launch_kind<KIND, DT, ACT_SILU>(plan, device, stream);
+    case ACT_GELU: return launch_kind<KIND, DT, ACT_GELU>(plan, device, stream);
+    case ACT_GELU_TANH: return launch_kind<KIND, DT, ACT_GELU_TANH>(plan, device, stream);
+  }
+  return hipErrorInvalidValue;
 }
 
 template <int DT>
 hipError_t launch_typed(int kind, ProductPlan& plan, int device, hipStream_t stream) {
   switch (kind) {
-    case PK_GATED: return launch_kind<PK_GATED, DT>(plan, device, stream);
+    case PK_GATED: return launch_gated<PK_GATED, DT>(plan, device, stream);
     case PK_STORE_NT: return launch_kind<PK_STORE_NT, DT>(plan, device, stream);
     case PK_STATS: return launch_kind<PK_STATS, DT>(plan, device, stream);
     case PK_DLOGITS: return launch_kind<PK_DLOGITS, DT>(plan, device, stream);
     case PK_STORE_NN: return launch_kind<PK_STORE_NN, DT>(plan, device, stream);
-    case PK_GATED_BWD: return launch_kind<PK_GATED_BWD, DT>(plan, device, stream);
+    case PK_GATED_BWD: return launch_gated<PK_GATED_BWD, DT>(plan, device, stream);
     case PK_ACCUM_NN: return launch_kind<PK_ACCUM_NN, DT>(plan, device, stream);
     case PK_STORE_TN: return launch_kind<PK_STORE_TN, DT>(plan, device, stream);
   }

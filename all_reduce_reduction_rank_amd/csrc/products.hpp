@@ -24,7 +24,7 @@ enum ProductKind : int {
 
 // Problem::mode of PK_ACCUM_NN
 enum : uint32_t { ACC_ADD = 1 /* add the fp32 sum so far (c[1]) */, ACC_LAST = 2 /* write c[0], else c[1] */ };
-// Problem::mode of PK_GATED, PK_GATED_BWD
+// ProductArgs::act
 enum : uint32_t { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
 
 // The (max, sum of exp(v - max)) pairs of two sets of values, joined.  An

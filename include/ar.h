@@ -377,8 +377,9 @@ size_t ar_gated_ffn_workspace(int nranks, size_t rows, size_t hidden, size_t int
  * with x [rows, hidden], w_gate and w_up [inter, hidden], w_down
  * [hidden, inter].  out[r] is rank r's partial sum: ar_allreduce (or
  * ar_allreduce_rmsnorm) over out[0..N-1] completes the block.
- * gate, up: NULL, or N buffers [rows, inter] that receive g and u for the
- * backward pass.  The inner product act(g) * u is rounded to dtype before it
+ * gate, up: both NULL, or N fp32 buffers [rows, inter] each that receive g and
+ * u for the backward pass (fp32 for either dtype: rounded to bf16 they would
+ * add two roundings to every gradient).  The inner product act(g) * u is rounded to dtype before it
  * is multiplied by w_down.  rows 0: nothing is done. */
 ar_status ar_gated_ffn(int nranks, const void* const* x, const void* const* w_gate, const void* const* w_up,
                        const void* const* w_down, void* const* out, void* const* gate, void* const* up, size_t rows,

@@ -81,7 +81,7 @@ def gated_ffn(x, wg, wu, wd, name, dt):
     h = a * u
     _, eh = rounded(h, ea * (np.abs(u) + eu) + np.abs(a) * eu + E * np.abs(h), dt)
     out, eo = product(h, wd, eh)
-    return {"gate": rounded(g, eg, dt), "up": rounded(u, eu, dt), "out": rounded(out, eo, dt)}
+    return {"gate": (g, eg), "up": (u, eu), "out": rounded(out, eo, dt)}
 
 
 def gated_ffn_backward(dout, x, wg, wu, wd, g, u, name, dt):

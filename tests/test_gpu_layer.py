@@ -58,8 +58,8 @@ def run_ffn(n, rows, hidden, inter, dt, act, backward=True, seed=0, ranks=None):
     _say("ffn", n, rows, hidden, inter, dt, act)
     x, wg, wu, wd, dout = ffn_inputs(n, rows, hidden, inter, dt, seed)
     _poison()
-    gate = [torch.full((rows, inter), float("nan"), dtype=TORCH[dt], device="cuda") for _ in range(n)]
-    up = [torch.full((rows, inter), float("nan"), dtype=TORCH[dt], device="cuda") for _ in range(n)]
+    gate = [torch.full((rows, inter), float("nan"), device="cuda") for _ in range(n)]
+    up = [torch.full((rows, inter), float("nan"), device="cuda") for _ in range(n)]
     out = ar.gated_ffn(x, wg, wu, wd, gate=gate, up=up, act=act)
     plain = ar.gated_ffn(x, wg, wu, wd, act=act)  # without keeping g and u: the same bits
     torch.cuda.synchronize()
