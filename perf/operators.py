@@ -222,8 +222,8 @@ def _own_ffn(state):
     if not case["train"]:
         return {"out": ar.gated_ffn(x, wg, wu, wd, act=case["act"])}
     shape = (case["rows"], case["size"])
-    gate = [torch.empty(shape, dtype=t.dtype, device=t.device) for t in x]
-    up = [torch.empty(shape, dtype=t.dtype, device=t.device) for t in x]
+    gate = [torch.empty(shape, dtype=torch.float32, device=t.device) for t in x]
+    up = [torch.empty(shape, dtype=torch.float32, device=t.device) for t in x]
     out = ar.gated_ffn(x, wg, wu, wd, gate=gate, up=up, act=case["act"])
     dx, dwg, dwu, dwd = ar.gated_ffn_backward(state["dout"], x, wg, wu, wd, gate, up, act=case["act"])
     return {"out": out, "dx": dx, "dw_gate": dwg, "dw_up": dwu, "dw_down": dwd}
