@@ -8,16 +8,19 @@
 //   L_R: rows run fastest (row-major [k, rows]); a product that sums over
 //        the tokens or over the output features reads its operand this way,
 //        so no transposed copy is made.
-// A tile of either operand takes BM (BN) x 128 bytes of LDS: 64 k of bf16 or
-// 32 k of fp32.  Two buffers alternate: while the waves multiply one, the
-// loads of the next K step land in the other.
+// A substep is 64 bytes of k, 32 bf16 or 16 fp32: one 16-byte fragment per lane
+// and 16 rows.  A tile's K step is KB bytes, one or two substeps.  A ring of
+// STAGES buffers holds K steps: the direct global -> LDS loads of the next ones
+// are in flight while the waves multiply.
 //
 // LDS layout and bank conflicts.  Tiles are written 16 bytes per lane in
 // lane order (the direct global -> LDS loads allow nothing else), so the
 // order is permuted on the global side: the 16-byte chunk at position p of
 // an LDS row holds chunk p ^ f(row) of the matrix row.
-//   L_K rows are 8 chunks; f = row & 7: the 16 rows a fragment read touches
-//       fall on all 8 chunk columns.
+//   L_K rows are 4 or 8 chunks.  Of 8, f = row & 7; of 4, f runs through
+//       0, 2, 3, 1 every 4 rows: whichever 16 lanes of a fragment read the
+//       hardware serves together (16 consecutive, or 0-3, 12-15, 20-23, 24-27)
+//       touch as many different chunks as there are (no conflicts counted).
 //   L_R rows (one k each) are BM * esize / 16 chunks.  bf16 fragments come
 //       from the transposing LDS read, whose 16-lane groups read 4 k x 32
 //       bytes; f = 2 ((k & 3) + 4 ((k >> 3) & 1)) spreads the 8 rows of two
@@ -57,7 +60,7 @@ typedef uint32_t v4u_any __attribute__((ext_vector_type(4), aligned(1)));
 
 typedef __attribute__((address_space(3))) char lds_char;
 
-constexpr int KBYTES = 128;       // bytes of k per operand row and K step
+constexpr int SUBSTEP = 64;  // bytes of k per operand row and fragment
 constexpr uint32_t OUT_OF_RANGE = 0x7fffff00u;  // beyond every descriptor (at most 2^30 bytes)
 constexpr int MAX_PROBLEMS = 3 * MAX_RANKS;
 
@@ -65,7 +68,6 @@ template <int DT>
 struct KElem {
   static constexpr int ES = DT == DT_BF16 ? 2 : 4;  // bytes of an element
   static constexpr int E = 16 / ES;                 // elements of a 16-byte chunk
-  static constexpr int BK = KBYTES / ES;            // k per step
 };
 
 // One product of a launch.  `first` .. `first` + tiles_m * tiles_n are its
@@ -143,15 +145,16 @@ __device__ __forceinline__ void load_to_lds(v4u rsrc, uint32_t off, uint32_t sof
 }
 
 // Loads one operand's tiles.  ROWS rows (of one matrix, or ROWS / 2 of each
-// of two when PAIR) by 128 bytes of k, by NT threads.
-template <int DT, int LAYOUT, int ROWS, int NT, bool PAIR, bool ALIGNED>
+// of two when PAIR) by KB bytes of k, by NT threads (thread `tid` of them).
+template <int DT, int LAYOUT, int ROWS, int NT, int KB, bool PAIR>
 struct TileLoader {
-  static constexpr int ES = KElem<DT>::ES, E = KElem<DT>::E, BK = KElem<DT>::BK;
-  static constexpr int SLOTS = ROWS * 8 / NT;  // 16-byte chunks per thread
-  static constexpr int CH = LAYOUT == L_K ? 8 : ROWS * ES / 16;  // chunks of an LDS row
+  static constexpr int ES = KElem<DT>::ES, E = KElem<DT>::E, BK = KB / ES;
+  static constexpr int SLOTS = ROWS * (KB / 16) / NT;  // 16-byte chunks per thread
+  static constexpr int CH = LAYOUT == L_K ? KB / 16 : ROWS * ES / 16;  // chunks of an LDS row
   // slots after which a thread's swizzle repeats (its rows are NT / CH apart)
-  static constexpr int PERIOD = LAYOUT == L_K || NT / CH >= 16 ? 1 : 16 / (NT / CH);
-  static_assert(!PAIR || (LAYOUT == L_K && (ROWS / 2) % (NT / 8) == 0), "a slot's rows lie in one matrix");
+  static constexpr int PERIOD = NT / CH >= 16 || SLOTS == 1 ? 1 : 16 / (NT / CH) < SLOTS ? 16 / (NT / CH) : SLOTS;
+  static_assert(SLOTS % PERIOD == 0 && (!PAIR || (SLOTS / 2) % PERIOD == 0), "");
+  static_assert(!PAIR || (LAYOUT == L_K && (ROWS / 2) % (NT / CH) == 0), "a slot's rows lie in one matrix");
   static_assert(SLOTS >= 1, "");
 
   const char* base[2];  // row0's first element (L_K), or k 0 of row0 (L_R)
@@ -160,7 +163,7 @@ struct TileLoader {
   uint32_t ldbytes;
 
   __device__ __forceinline__ static uint32_t swz(uint32_t row) {
-    if constexpr (LAYOUT == L_K) return row & 7;
+    if constexpr (LAYOUT == L_K) return KB == 128 ? row & 7 : (0x78u >> (row / 4 % 4 * 2)) & 3;
     else if constexpr (DT == DT_BF16) return (2 * ((row & 3) + 4 * ((row >> 3) & 1))) & (CH - 1);
     else return (4 * ((row >> 2) & 3)) & (CH - 1);
   }
@@ -178,14 +181,14 @@ struct TileLoader {
   // Chunk of this thread's slot i: its LDS row and the chunk of the matrix
   // row it holds.
   __device__ __forceinline__ static void slot(int i, uint32_t* row, uint32_t* chunk) {
-    const uint32_t p = (uint32_t)i * NT + threadIdx.x;
+    const uint32_t p = (uint32_t)i * NT + threadIdx.x % NT;
     *row = p / CH;
     *chunk = (p % CH) ^ swz(*row);
   }
 
   // Start the direct loads of K step k0 into LDS at `dst`.
   __device__ __forceinline__ void load_direct(uint32_t k0, lds_char* dst) const {
-    const uint32_t wave = uniform(threadIdx.x / 64);
+    const uint32_t wave = uniform(threadIdx.x % NT / 64);
     v4u rsrc[2];
 #pragma unroll
     for (int h = 0; h < (PAIR ? 2 : 1); ++h) {
@@ -263,15 +266,14 @@ struct TileLoader {
   __device__ __forceinline__ void store_regs(const v4u* r, lds_char* dst) const {
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i)
-      *(__attribute__((address_space(3))) v4u*)(dst + ((uint32_t)i * NT + threadIdx.x) * 16) = r[i];
+      *(__attribute__((address_space(3))) v4u*)(dst + ((uint32_t)i * NT + threadIdx.x % NT) * 16) = r[i];
   }
 
-  // Fragment of 16 rows from r0 on, K substep s (0, 1): 16 bytes per lane.
+  // Fragment of 16 rows from r0 on, substep s: 16 bytes per lane.
   __device__ __forceinline__ static v4u fragment(const lds_char* tile, int r0, int s) {
     const uint32_t lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
     if constexpr (LAYOUT == L_K) {
-      const uint32_t chunk = (uint32_t)(s * 4) + q;
-      return *(const __attribute__((address_space(3))) v4u*)(tile + (r0 + i) * KBYTES + ((chunk ^ (i & 7)) * 16));
+      return *(const __attribute__((address_space(3))) v4u*)(tile + (r0 + i) * KB + (((uint32_t)s * 4 + q) ^ swz(i)) * 16);
     } else if constexpr (DT == DT_BF16) {
       constexpr uint32_t RB = ROWS * 2;
       const uint32_t kr = (uint32_t)s * 32 + 8 * q + i / 4;
@@ -295,25 +297,34 @@ struct TileLoader {
   }
 };
 
+// One 16 x 16 block: acc += first second^T, element j of the fragments (fp32;
+// bf16 takes the whole fragments at once).
 template <int DT>
-__device__ __forceinline__ v4f mma(v4u first, v4u second, v4f acc) {
-  if constexpr (DT == DT_BF16) {
+__device__ __forceinline__ v4f mma(v4u first, v4u second, v4f acc, int j) {
+  if constexpr (DT == DT_BF16)
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, first), __builtin_bit_cast(v8bf, second),
                                                    acc, 0, 0, 0);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(first[j]), __uint_as_float(second[j]), acc, 0, 0, 0);
-    return acc;
-  }
+  else return __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(first[j]), __uint_as_float(second[j]), acc, 0, 0, 0);
 }
 
-// Tile sizes: WM x WN waves share the BM x BN tile, STAGES K steps of it in LDS.
+// Tile classes.  WM x WN waves share the BM x BN tile and a ring of STAGES K
+// steps of KB bytes in LDS.  With WK > 1, WK single waves take a part of K
+// each, with a ring each and no barrier, and their sums are added in LDS: few
+// rows or few tiles still have many loads in flight.
 struct Large {  // 8 waves of 128 x 64, 128 KB of LDS: one workgroup per CU
-  static constexpr int BM = 256, BN = 256, WM = 2, WN = 4, STAGES = 2;
+  static constexpr int BM = 256, BN = 256, WM = 2, WN = 4, WK = 1, KB = 128, STAGES = 2;
 };
 struct Small {  // 4 waves of 64 x 64, 64 KB: two workgroups per CU
-  static constexpr int BM = 128, BN = 128, WM = 2, WN = 2, STAGES = 2;
+  static constexpr int BM = 128, BN = 128, WM = 2, WN = 2, WK = 1, KB = 128, STAGES = 2;
+};
+struct Flat {  // 4 waves of 64 x 32, 72 KB: two workgroups per CU
+  static constexpr int BM = 64, BN = 128, WM = 1, WN = 4, WK = 1, KB = 128, STAGES = 3;
+};
+struct Split {  // 4 waves, 64 x 64 each of a quarter of K, 128 KB
+  static constexpr int BM = 64, BN = 64, WM = 1, WN = 1, WK = 4, KB = 128, STAGES = 2;
+};
+struct Thin {  // 4 waves, 16 x 32 each of a quarter of K, 72 KB: two workgroups per CU
+  static constexpr int BM = 16, BN = 32, WM = 1, WN = 1, WK = 4, KB = 128, STAGES = 3;
 };
 
 template <int DT_, int LA_, int LB_, bool PAIR_, bool ALIGNED_, class TILE_>
@@ -321,15 +332,17 @@ struct Product {
   static constexpr int DT = DT_, LA = LA_, LB = LB_;
   static constexpr bool PAIR = PAIR_, ALIGNED = ALIGNED_;
   using TILE = TILE_;
-  static constexpr int BM = TILE::BM, BN = TILE::BN, WM = TILE::WM, WN = TILE::WN, STAGES = TILE::STAGES;
-  static constexpr int NT = 64 * WM * WN;
+  static constexpr int BM = TILE::BM, BN = TILE::BN, WM = TILE::WM, WN = TILE::WN;
+  static constexpr int WK = TILE::WK, KB = TILE::KB, STAGES = TILE::STAGES, SUBS = KB / SUBSTEP;
+  static_assert(WK == 1 || WM * WN == 1, "waves that split K work alone");
+  static constexpr int GROUP = 64 * WM * WN, NT = GROUP * WK;  // threads of a ring, of the workgroup
   static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 blocks per wave
   static constexpr int COLS = PAIR ? BN / 2 : BN;             // columns of C a tile covers
-  static constexpr int STAGE = (BM + BN) * KBYTES;
-  static constexpr int LDS_BYTES = STAGES * STAGE;
+  static constexpr int STAGE = (BM + BN) * KB, RING = STAGES * STAGE;
+  static constexpr int LDS_BYTES = WK * RING;
 
-  using LoadA = TileLoader<DT, LA, BM, NT, false, ALIGNED>;
-  using LoadB = TileLoader<DT, LB, BN, NT, PAIR, ALIGNED>;
+  using LoadA = TileLoader<DT, LA, BM, GROUP, KB, false>;
+  using LoadB = TileLoader<DT, LB, BN, GROUP, KB, PAIR>;
   static constexpr int LOADS = LoadA::SLOTS + LoadB::SLOTS;  // direct loads per thread and K step
 
   v4f acc[TM][TN];
@@ -337,9 +350,9 @@ struct Product {
   // This wave's first row in the A tile / its block j's first row in the B
   // tile.  A paired tile holds BN / 2 rows of b[0], then BN / 2 of b[1];
   // blocks j and j + TN / 2 of a wave are the same columns of the two.
-  __device__ __forceinline__ static int wave_row() { return uniform((int)(threadIdx.x / 64)) / WN * (BM / WM); }
+  __device__ __forceinline__ static int wave_row() { return WM == 1 ? 0 : uniform((int)(threadIdx.x / 64)) / WN * (BM / WM); }
   __device__ __forceinline__ static int wave_col() {
-    return uniform((int)(threadIdx.x / 64)) % WN * ((PAIR ? BN / 2 : BN) / WN);
+    return WN == 1 ? 0 : uniform((int)(threadIdx.x / 64)) % WN * ((PAIR ? BN / 2 : BN) / WN);
   }
   __device__ __forceinline__ static int block_row(int j) {
     if constexpr (PAIR) return j < TN / 2 ? wave_col() + 16 * j : BN / 2 + wave_col() + 16 * (j - TN / 2);
@@ -350,14 +363,15 @@ struct Product {
   __device__ __forceinline__ static void read(const lds_char* buf, int s, v4u* fa, v4u* fb, int i) {
     fa[i] = LoadA::fragment(buf, wave_row() + 16 * i, s);
 #pragma unroll
-    for (int j = i * TN / TM; j < (i + 1) * TN / TM; ++j)
-      fb[j] = LoadB::fragment(buf + BM * KBYTES, block_row(j), s);
+    for (int j = i * TN / TM; j < (i + 1) * TN / TM; ++j) fb[j] = LoadB::fragment(buf + BM * KB, block_row(j), s);
   }
   __device__ __forceinline__ void multiply(const v4u* fa, const v4u* fb, int i) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = mma<DT>(fb[j], fa[i], acc[i][j]);
+    for (int e = 0; e < (DT == DT_BF16 ? 1 : 4); ++e)  // outermost: no product waits for the one before it
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = mma<DT>(fb[j], fa[i], acc[i][j], e);
   }
-  // Order of a half step for the compiler: the LDS reads of the next half
+  // Order of a step for the compiler: the LDS reads of the next step
   // spread evenly over the first half of the products, so that neither waits
   // for the other.
   static constexpr int READS_A = LA == L_K ? 1 : DT == DT_BF16 ? 2 : 4;
@@ -374,30 +388,37 @@ struct Product {
     }
   }
   // Every load of this wave but the youngest n has landed, and so has every
-  // LDS read; then the workgroup's barrier.
+  // LDS read; then the barrier of the waves that share the ring.
   template <int N>
   __device__ __forceinline__ static void landed() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"(N) : "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    if constexpr (WK == 1) {
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    }
   }
 
   // Accumulate the tile at (row0, col0) of problem p.
   //
-  // Each K step is two half steps (16-byte fragments).  A half step
-  // multiplies fragments read during the one before, while it reads the next
-  // one's, so the matrix cores never wait for an LDS read.  In the middle of
-  // step t its last reads are done and step t + 1 must have landed: one
-  // barrier there frees step t's buffer for step t + STAGES and publishes
-  // the next.
+  // A substep multiplies fragments that were read from LDS during the one
+  // before, while it reads the next one's, so the matrix cores never wait for
+  // an LDS read.  Before the last substep of step t every wave has read all
+  // of t, and step t + 1 must have landed: one barrier there frees step t's
+  // buffer for step t + STAGES and publishes t + 1.
   __device__ __forceinline__ void run(const Problem& p, int nseg, uint32_t row0, uint32_t col0, char* smem) {
-    lds_char* lds = (lds_char*)smem;
+    const int wk = WK == 1 ? 0 : uniform((int)(threadIdx.x / GROUP));
+    lds_char* lds = (lds_char*)smem + wk * RING;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-    const uint32_t per = (p.k + KElem<DT>::BK - 1) / KElem<DT>::BK;
-    const uint32_t steps = per * (uint32_t)nseg;
+    constexpr uint32_t BK = LoadA::BK;
+    const uint32_t per = (p.k + BK - 1) / BK;
+    const uint32_t all = per * (uint32_t)nseg;
+    // this wave's part of the steps
+    const uint32_t part = (all + WK - 1) / WK;
+    const uint32_t first = (uint32_t)wk * part;
+    const uint32_t steps = first >= all ? 0 : all - first < part ? all - first : part;
     if (steps == 0) return;
     LoadA la[2];
     LoadB lb[2];
@@ -406,16 +427,17 @@ struct Product {
     la[1].init(p.a[1], nullptr, row0, p.m, p.k, p.lda);
     lb[1].init(p.b[1], nullptr, col0, p.n, p.k, p.ldb);
     // Loader of step t's segment and its first k.  A step past the last one
-    // (t up to steps + STAGES - 1) starts past k: all of it reads as zero.
+    // (t up to steps + STAGES - 1) is put past k: all of it reads as zero.
     auto at = [&](uint32_t t, LoadA* a, LoadB* b) {
-      const bool second = nseg > 1 && t >= per;
+      const uint32_t u = first + t;
+      const bool second = nseg > 1 && u >= per;
       *a = la[0];
       *b = lb[0];
       if (second) {
         a->base[0] = la[1].base[0];
         b->base[0] = lb[1].base[0];
       }
-      return (second ? t - per : t) * KElem<DT>::BK;
+      return (t >= steps ? per : second ? u - per : u) * BK;
     };
     v4u fa[2][TM], fb[2][TN];
     if constexpr (ALIGNED) {
@@ -424,7 +446,7 @@ struct Product {
         LoadB b;
         const uint32_t k0 = at(t, &a, &b);
         a.load_direct(k0, dst);
-        b.load_direct(k0, dst + BM * KBYTES);
+        b.load_direct(k0, dst + BM * KB);
       };
 #pragma unroll
       for (int t = 0; t < STAGES; ++t) start(t, lds + t * STAGE);
@@ -432,25 +454,28 @@ struct Product {
 #pragma unroll
       for (int i = 0; i < TM; ++i) read(lds, 0, fa[0], fb[0], i);
       uint32_t cur = 0;  // byte offset of step t's buffer
-      for (uint32_t t = 0; t < steps; ++t) {
-        const uint32_t next = cur + STAGE == (uint32_t)LDS_BYTES ? 0 : cur + STAGE;
+      // two substeps a turn, so that the fragment sets alternate by name (an
+      // odd count of single-substep steps ends with one of zeros)
+      for (uint32_t t = 0; t < steps; t += 2 / SUBS) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-          read(lds + cur, 1, fa[1], fb[1], i);
-          multiply(fa[0], fb[0], i);
-        }
-        interleave<0>();
-        landed<(STAGES - 2) * LOADS>();
-        // with two stages the wait is for every load, and steps past the last
-        // one need not be started to keep its count
-        if (STAGES > 2 || t + STAGES < steps) start(t + STAGES, lds + cur);
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t next = cur + STAGE == (uint32_t)RING ? 0 : cur + STAGE;
+          const bool last = SUBS == 1 || h == 1;  // of the step's substeps
+          if (last) {
+            landed<(STAGES - 2) * LOADS>();
+            // with two stages the wait is for every load: steps past the
+            // last one need not be started to keep its count
+            const uint32_t u = t + (SUBS == 1 ? h : 0) + STAGES;
+            if (STAGES > 2 || u < steps) start(u, lds + cur);
+          }
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-          read(lds + next, 0, fa[0], fb[0], i);  // (stale after the last step, and not used)
-          multiply(fa[1], fb[1], i);
+          for (int i = 0; i < TM; ++i) {
+            read(lds + (last ? next : cur), last ? 0 : 1, fa[1 - h], fb[1 - h], i);
+            multiply(fa[h], fb[h], i);
+          }
+          interleave<0>();
+          if (last) cur = next;
         }
-        interleave<0>();
-        cur = next;
       }
       landed<0>();
     } else {
@@ -468,15 +493,15 @@ struct Product {
       for (uint32_t t = 0; t < steps; ++t) {
         lds_char* buf = lds + (t & 1) * STAGE;
         la[0].store_regs(ra, buf);
-        lb[0].store_regs(rb, buf + BM * KBYTES);
-        __syncthreads();
+        lb[0].store_regs(rb, buf + BM * KB);
+        if constexpr (WK == 1) __syncthreads();
         if (t + 1 < steps) fetch(t + 1);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
+        for (int u = 0; u < SUBS; ++u) {
 #pragma unroll
-          for (int i = 0; i < TM; ++i) read(buf, s, fa[s], fb[s], i);
+          for (int i = 0; i < TM; ++i) read(buf, u, fa[u], fb[u], i);
 #pragma unroll
-          for (int i = 0; i < TM; ++i) multiply(fa[s], fb[s], i);
+          for (int i = 0; i < TM; ++i) multiply(fa[u], fb[u], i);
         }
       }
     }
@@ -495,11 +520,13 @@ struct Product {
   // write and the neighbouring chunks of a read fall on different banks.
   template <int V, int U, class PRE, class F>
   __device__ __forceinline__ void hand_out(char* smem, PRE&& pre, F&& f) {
-    constexpr int PHASES = (BM * BN * 4 + LDS_BYTES - 1) / LDS_BYTES;
+    constexpr int PHASES = (BM * BN * 4 * WK + LDS_BYTES - 1) / LDS_BYTES;
     constexpr int PART = TM / PHASES;  // blocks of a wave per phase
-    constexpr int ROWS = PART * 16 * WM, UNITS = ROWS * (COLS / V), ROUNDS = UNITS / (NT * U);
-    static_assert(TM % PHASES == 0 && UNITS % (NT * U) == 0, "");
+    constexpr int ROWS = PART * 16 * WM, UNITS = ROWS * (COLS / V), ROUNDS = (UNITS + NT * U - 1) / (NT * U);
+    constexpr int SWZ = BN / 4 < 16 ? BN / 4 - 1 : 15;
+    static_assert(TM % PHASES == 0 && (PHASES == 1 || WK == 1), "");
     const uint32_t lane = threadIdx.x & 63;
+    const uint32_t wk = WK == 1 ? 0 : threadIdx.x / GROUP;
     float4* t = (float4*)smem;
 #pragma unroll
     for (int ph = 0; ph < PHASES; ++ph) {
@@ -511,7 +538,7 @@ struct Product {
         for (int j = 0; j < TN; ++j) {
           const v4f v = acc[ph * PART + i][j];
           const uint32_t chunk = (uint32_t)block_row(j) / 4 + (lane >> 4);
-          t[r * (BN / 4) + (chunk ^ (r & 15))] = make_float4(v[0], v[1], v[2], v[3]);
+          t[(wk * ROWS + r) * (BN / 4) + (chunk ^ (r & SWZ))] = make_float4(v[0], v[1], v[2], v[3]);
         }
       }
       __syncthreads();
@@ -526,18 +553,29 @@ struct Product {
           at[u] = r;
           col[u] = unit % (COLS / V) * V;
           row[u] = r / (16 * PART) * (16 * TM) + ph * PART * 16 + r % (16 * PART);
-          x[u] = pre(row[u], col[u]);
+          if (UNITS % (NT * U) == 0 || unit < (uint32_t)UNITS) x[u] = pre(row[u], col[u]);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+          if (UNITS % (NT * U) != 0 && at[u] >= (uint32_t)ROWS) continue;
           float v[V], w[V];
 #pragma unroll
           for (int q = 0; q < V / 4; ++q) {
-            const uint32_t chunk = col[u] / 4 + q, s = at[u] & 15;
-            const float4 a = t[at[u] * (BN / 4) + (chunk ^ s)];
+            const uint32_t chunk = col[u] / 4 + q, s = at[u] & SWZ;
+            // the parts of K, added in order
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+#pragma unroll
+            for (int z = 0; z < WK; ++z) {
+              const float4 y = t[(z * ROWS + at[u]) * (BN / 4) + (chunk ^ s)];
+              a.x += y.x, a.y += y.y, a.z += y.z, a.w += y.w;
+            }
             v[4 * q] = a.x, v[4 * q + 1] = a.y, v[4 * q + 2] = a.z, v[4 * q + 3] = a.w;
             if constexpr (PAIR) {
-              const float4 b = t[at[u] * (BN / 4) + ((chunk + BN / 8) ^ s)];
+#pragma unroll
+              for (int z = 0; z < WK; ++z) {
+                const float4 y = t[(z * ROWS + at[u]) * (BN / 4) + ((chunk + BN / 8) ^ s)];
+                b.x += y.x, b.y += y.y, b.z += y.z, b.w += y.w;
+              }
               w[4 * q] = b.x, w[4 * q + 1] = b.y, w[4 * q + 2] = b.z, w[4 * q + 3] = b.w;
             }
           }

@@ -167,6 +167,35 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
           }
           store_row<DT, V>(p.c[0] + row * ldc * ES, (uint64_t)col0 + col, p.ldc, vec, v);
         });
+  } else if constexpr (P::WK > 1) {  // PK_STATS, K split over the waves
+    float* at_target = (float*)p.c[1];
+    x.template hand_out<V, 1>(
+        smem,
+        [&](uint32_t r, uint32_t) {
+          const uint64_t row = (uint64_t)row0 + r;
+          const int64_t t = row < m ? a.target[row] : -1;
+          return t >= 0 && (uint64_t)t < a.vocab ? t - (int64_t)p.col0 : (int64_t)-1;
+        },
+        [&](uint32_t r, uint32_t col, float* v, float*, int64_t at) {
+          // the COLS / V threads of a row are neighbours in a wave
+          const uint64_t row = (uint64_t)row0 + r;
+          float top = -INFINITY, sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const uint32_t c = col0 + col + e;
+            if (c < n) top = fmaxf(top, v[e]);
+            if (c < n && (int64_t)c == at && row < m) at_target[row] = v[e];
+          }
+#pragma unroll
+          for (int o = 1; o < P::COLS / V; o *= 2) top = fmaxf(top, __shfl_xor(top, o));
+          const float shift = stats_shift(top);
+#pragma unroll
+          for (int e = 0; e < V; ++e)
+            if (col0 + col + e < n) sum += exp_of<DT>(v[e] - shift);
+#pragma unroll
+          for (int o = 1; o < P::COLS / V; o *= 2) sum += __shfl_xor(sum, o);
+          if (col == 0 && row < m) ((float2*)p.c[0])[(uint64_t)(col0 / P::COLS) * m + row] = make_float2(top, sum);
+        });
   } else {  // PK_STATS
     __syncthreads();  // every wave is done with the tiles
     float2* part = (float2*)smem;  // [WN][BM]
@@ -230,11 +259,25 @@ hipError_t launch(ProductPlan& plan, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <int KIND, int DT, bool ALIGNED, uint32_t ACT>
+hipError_t launch_tile(int tile, ProductPlan& plan, hipStream_t stream) {
+  switch (tile) {
+    case TILE_LARGE:
+      if constexpr (ALIGNED && DT == DT_BF16) return launch<KIND, DT, true, Large, ACT>(plan, stream);
+      else return hipErrorInvalidValue;  // product_tile takes it for neither
+    case TILE_SMALL: return launch<KIND, DT, ALIGNED, Small, ACT>(plan, stream);
+    case TILE_FLAT: return launch<KIND, DT, ALIGNED, Flat, ACT>(plan, stream);
+    case TILE_SPLIT: return launch<KIND, DT, ALIGNED, Split, ACT>(plan, stream);
+    case TILE_THIN: return launch<KIND, DT, ALIGNED, Thin, ACT>(plan, stream);
+  }
+  return hipErrorInvalidValue;
+}
+
 template <int KIND, int DT, uint32_t ACT = ACT_SILU>
 hipError_t launch_kind(ProductPlan& plan, int device, hipStream_t stream) {
-  const bool large = product_tile(KIND, plan, device).bm == (uint32_t)Large::BM;
-  if (!plan.aligned) return launch<KIND, DT, false, Small, ACT>(plan, stream);
-  return large ? launch<KIND, DT, true, Large, ACT>(plan, stream) : launch<KIND, DT, true, Small, ACT>(plan, stream);
+  const int tile = product_tile(KIND, DT, plan, device);
+  return plan.aligned ? launch_tile<KIND, DT, true, ACT>(tile, plan, stream)
+                      : launch_tile<KIND, DT, false, ACT>(tile, plan, stream);
 }
 
 template <int KIND, int DT>

@@ -1,4 +1,22 @@
 // products.hip -- tile choice of the product kernels.
+//
+// A launch takes the tile class with the smallest estimated time.  A
+// workgroup of class c takes fixed + steps x (alone | full) us, a step being
+// 128 bytes of k (of each wave's part of K): `alone` while its CU runs no
+// other, `full` with as many as fit.  Measured on bf16 products of 8 ranks
+// [m, 5120] x [1728 pairs, 5120] (80 steps) and [m, 1728] x [5120, 1728] (27):
+//
+//   us            m = 64   128   256   512  1024 |   64   128   256   512  1024
+//   Large            143   150   172   171   302 |   51    55    60   111   162
+//   Small             96   110   125   218   373 |   39    46    76   106   174
+//   Flat              65    99   157   247   490 |   38    47    67   119   214
+//   Split             73   116   185   347   687 |   42    60   108   205   377
+//   Thin (m = 1)      55                         |   31
+//
+// One small product, [512, 4096] x [1024, 4096]: 83, 50, 31, 16 us.  Thin is
+// for 16 rows at most: with more it reads the weights again for every 16.
+// fp32 runs 16 times as many instructions per byte, so its steps cost what
+// its matrix instructions do.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -6,17 +24,69 @@
 
 namespace ar {
 
-TileShape product_tile(int kind, const ProductPlan& plan, int device) {
-  int cus = 0;
-  if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device) != hipSuccess || cus < 1) cus = 256;
+namespace {
+
+struct ClassCost {
+  uint32_t bm, bn, parts, resident;  // parts: of K; resident: workgroups per CU
+  double fixed, alone, full;         // bf16
+};
+constexpr ClassCost COST[TILE_CLASSES] = {
+    {Large::BM, Large::BN, Large::WK, 1, 9.0, 1.75, 1.75},
+    {Small::BM, Small::BN, Small::WK, 2, 4.0, 1.15, 1.35},
+    {Flat::BM, Flat::BN, Flat::WK, 2, 4.0, 0.75, 0.95},
+    {Split::BM, Split::BN, Split::WK, 1, 4.5, 1.2, 1.2},
+    {Thin::BM, Thin::BN, Thin::WK, 2, 4.5, 0.25, 0.6},
+};
+constexpr double F32_FLOPS_PER_CU_US = 0.55e6;  // of 0.61e6 (16x16x4 at 2.4 GHz)
+
+}  // namespace
+
+int product_tile(int kind, int dtype, const ProductPlan& plan, int device) {
+  int n_cu = 0;
+  if (hipDeviceGetAttribute(&n_cu, hipDeviceAttributeMultiprocessorCount, device) != hipSuccess || n_cu < 1) n_cu = 256;
+  const double cus = n_cu;
   const uint32_t half = kind == PK_GATED ? 2 : 1;
-  uint64_t tiles = 0;
-  for (int i = 0; i < plan.a.nprob; ++i) {
-    const Problem& p = plan.a.p[i];
-    tiles += (((uint64_t)p.m + 255) / 256) * (((uint64_t)p.n * half + 255) / 256);
+  const uint64_t per_step = dtype == DT_BF16 ? 64 : 32;  // k of 128 bytes
+  uint32_t max_m = 0;
+  for (int i = 0; i < plan.a.nprob; ++i) max_m = plan.a.p[i].m > max_m ? plan.a.p[i].m : max_m;
+  int best = TILE_SMALL;
+  double best_us = 1e30;
+  for (int c = 0; c < TILE_CLASSES; ++c) {
+    if (c == TILE_LARGE && (!plan.aligned || dtype != DT_BF16)) continue;
+    if (c == TILE_THIN && max_m > (uint32_t)Thin::BM) continue;
+    const ClassCost& k = COST[c];
+    double tiles = 0, work = 0, longest = 0;  // work: steps of all tiles
+    for (int i = 0; i < plan.a.nprob; ++i) {
+      const Problem& p = plan.a.p[i];
+      const double t = (double)((p.m + k.bm - 1) / k.bm) * (double)(((uint64_t)p.n * half + k.bn - 1) / k.bn);
+      const uint64_t steps = (uint64_t)plan.a.nseg * ((p.k + per_step - 1) / per_step);
+      const double s = (double)((steps + k.parts - 1) / k.parts);
+      tiles += t;
+      work += t * s;
+      if (t > 0 && s > longest) longest = s;
+    }
+    if (tiles == 0) continue;
+    double alone = k.alone, full = k.full;
+    if (dtype != DT_BF16) {
+      const double mm = 2.0 * k.bm * k.bn * per_step * k.parts / F32_FLOPS_PER_CU_US;
+      alone = mm > alone ? mm : alone;
+      full = mm * k.resident > full ? mm * k.resident : full;
+    }
+    if (!plan.aligned) {  // through registers
+      alone *= 1.6;
+      full *= 1.6;
+    }
+    const double slots = cus * k.resident;
+    const double rounds = (double)(uint64_t)(tiles / slots);
+    const double rest = tiles - rounds * slots;
+    double us = rounds * (k.fixed + work / tiles * full);
+    if (rest > 0) us += k.fixed + longest * (rest <= cus ? alone : full);
+    if (us < best_us) {
+      best_us = us;
+      best = c;
+    }
   }
-  const bool large = plan.aligned && tiles >= (uint64_t)cus;
-  return large ? TileShape{256, 256 / half} : TileShape{128, 128 / half};
+  return best;
 }
 
 }  // namespace ar

@@ -36,14 +36,16 @@ __device__ __forceinline__ float2 merge_stats(float2 x, float2 y) {
   return make_float2(top, x.y * expf(stats_shift(x.x) - shift) + y.y * expf(stats_shift(y.x) - shift));
 }
 
-struct TileShape {
-  uint32_t bm, cols;  // rows and columns of C one tile covers
-};
-
-// Tile that a launch of this plan takes (its problems are final).  PK_STATS
-// writes one partial per row and `cols` columns.
-TileShape product_tile(int kind, const ProductPlan& plan, int device);
-constexpr uint32_t MIN_TILE_COLS = 128;  // of a kind that is not paired
+// Tile class that a launch of this plan takes (its problems are final).
+enum TileClass : int { TILE_LARGE = 0, TILE_SMALL, TILE_FLAT, TILE_SPLIT, TILE_THIN, TILE_CLASSES };
+int product_tile(int kind, int dtype, const ProductPlan& plan, int device);
+// Columns of C a tile of a class that is not paired covers: PK_STATS writes
+// one partial per row and that many columns.
+constexpr uint32_t tile_cols(int tile) {
+  constexpr uint32_t cols[TILE_CLASSES] = {Large::BN, Small::BN, Flat::BN, Split::BN, Thin::BN};
+  return cols[tile];
+}
+constexpr uint32_t MIN_TILE_COLS = Thin::BN;
 
 hipError_t launch_products_bf16(int kind, ProductPlan& plan, int device, hipStream_t stream);
 hipError_t launch_products_f32(int kind, ProductPlan& plan, int device, hipStream_t stream);

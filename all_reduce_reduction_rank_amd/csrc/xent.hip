@@ -6,7 +6,7 @@
 // and sum of exponentials (and the target's logit, if it lies in the tile).
 // A second kernel joins the tiles of every rank, the all-reduce of the split
 // softmax: lse = log sum_v exp(l_v), loss = lse - l_target, stored to every
-// rank.  It reads 8 bytes per row and 128 or 256 columns.
+// rank.  It reads 8 bytes per row and tile (32 to 256 columns).
 //
 // Backward, one piece of each rank's vocabulary at a time: recompute the
 // piece's logits, store d = (exp(l - lse) - onehot) grad for the piece only,
@@ -180,8 +180,8 @@ ar_status ar_linear_cross_entropy(int nranks, const void* const* x, const void* 
     p->c[1] = ws;
     p->col0 = s.start[r];
   }
-  const TileShape tile = product_tile(PK_STATS, plan, dev);
-  for (int r = 0; r < nranks; ++r) c.tiles[r] = (uint32_t)((s.shard[r] + tile.cols - 1) / tile.cols);
+  const uint64_t cols = tile_cols(product_tile(PK_STATS, (int)dtype, plan, dev));
+  for (int r = 0; r < nranks; ++r) c.tiles[r] = (uint32_t)((s.shard[r] + cols - 1) / cols);
   c.at = (const float*)ws;
   c.target = target;
   c.vocab = s.vocab;
