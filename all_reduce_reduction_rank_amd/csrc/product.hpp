@@ -8,19 +8,17 @@
 //   L_R: rows run fastest (row-major [k, rows]); a product that sums over
 //        the tokens or over the output features reads its operand this way,
 //        so no transposed copy is made.
-// A substep is 64 bytes of k, 32 bf16 or 16 fp32: one 16-byte fragment per lane
-// and 16 rows.  A tile's K step is KB bytes, one or two substeps.  A ring of
-// STAGES buffers holds K steps: the direct global -> LDS loads of the next ones
-// are in flight while the waves multiply.
+// A K step is 128 bytes of k of every row, two substeps of 64 (32 bf16 or 16
+// fp32): one 16-byte fragment per lane and 16 rows each.  A ring of buffers
+// holds K steps: the direct global -> LDS loads of the next ones are in flight
+// while the waves multiply.
 //
 // LDS layout and bank conflicts.  Tiles are written 16 bytes per lane in
 // lane order (the direct global -> LDS loads allow nothing else), so the
 // order is permuted on the global side: the 16-byte chunk at position p of
 // an LDS row holds chunk p ^ f(row) of the matrix row.
-//   L_K rows are 4 or 8 chunks.  Of 8, f = row & 7; of 4, f runs through
-//       0, 2, 3, 1 every 4 rows: whichever 16 lanes of a fragment read the
-//       hardware serves together (16 consecutive, or 0-3, 12-15, 20-23, 24-27)
-//       touch as many different chunks as there are (no conflicts counted).
+//   L_K rows are 8 chunks; f = row & 7: the 16 rows of a fragment read touch
+//       every chunk column twice, 256 bytes apart (no conflicts counted).
 //   L_R rows (one k each) are BM * esize / 16 chunks.  bf16 fragments come
 //       from the transposing LDS read, whose 16-lane groups read 4 k x 32
 //       bytes; f = 2 ((k & 3) + 4 ((k >> 3) & 1)) spreads the 8 rows of two
@@ -60,7 +58,7 @@ typedef uint32_t v4u_any __attribute__((ext_vector_type(4), aligned(1)));
 
 typedef __attribute__((address_space(3))) char lds_char;
 
-constexpr int SUBSTEP = 64;  // bytes of k per operand row and fragment
+constexpr int KB = 128;  // bytes of k per operand row and K step: a cache line, two substeps
 constexpr uint32_t OUT_OF_RANGE = 0x7fffff00u;  // beyond every descriptor (at most 2^30 bytes)
 constexpr int MAX_PROBLEMS = 3 * MAX_RANKS;
 
@@ -146,7 +144,7 @@ __device__ __forceinline__ void load_to_lds(v4u rsrc, uint32_t off, uint32_t sof
 
 // Loads one operand's tiles.  ROWS rows (of one matrix, or ROWS / 2 of each
 // of two when PAIR) by KB bytes of k, by NT threads (thread `tid` of them).
-template <int DT, int LAYOUT, int ROWS, int NT, int KB, bool PAIR>
+template <int DT, int LAYOUT, int ROWS, int NT, bool PAIR>
 struct TileLoader {
   static constexpr int ES = KElem<DT>::ES, E = KElem<DT>::E, BK = KB / ES;
   static constexpr int SLOTS = ROWS * (KB / 16) / NT;  // 16-byte chunks per thread
@@ -163,7 +161,7 @@ struct TileLoader {
   uint32_t ldbytes;
 
   __device__ __forceinline__ static uint32_t swz(uint32_t row) {
-    if constexpr (LAYOUT == L_K) return KB == 128 ? row & 7 : (0x78u >> (row / 4 % 4 * 2)) & 3;
+    if constexpr (LAYOUT == L_K) return row & 7;
     else if constexpr (DT == DT_BF16) return (2 * ((row & 3) + 4 * ((row >> 3) & 1))) & (CH - 1);
     else return (4 * ((row >> 2) & 3)) & (CH - 1);
   }
@@ -308,23 +306,32 @@ __device__ __forceinline__ v4f mma(v4u first, v4u second, v4f acc, int j) {
 }
 
 // Tile classes.  WM x WN waves share the BM x BN tile and a ring of STAGES K
-// steps of KB bytes in LDS.  With WK > 1, WK single waves take a part of K
+// steps in LDS.  With WK > 1, WK single waves take a part of K
 // each, with a ring each and no barrier, and their sums are added in LDS: few
 // rows or few tiles still have many loads in flight.
+//
+// KB is 128, a cache line: with 64 bytes a row, weights streamed for one token
+// came at 4.3 TB/s, with lines at 5.4, and the loads alone of an 8192^3
+// product at 12.4 TB/s however many were in flight, with lines at up to 18.7.
+// What bounds the large tile is power more than any one pipe: an 8192^3
+// product's matrix instructions alone took 590 us (1.8 GHz of 2.4), its loads
+// alone 690, both with the LDS reads 840; five buffers of half steps, A one
+// step further ahead, 32 x 32 blocks, other orders of the half step and wave
+// priorities all came within 3 % of that, 4 waves of 128 x 128 at 920.
 struct Large {  // 8 waves of 128 x 64, 128 KB of LDS: one workgroup per CU
-  static constexpr int BM = 256, BN = 256, WM = 2, WN = 4, WK = 1, KB = 128, STAGES = 2;
+  static constexpr int BM = 256, BN = 256, WM = 2, WN = 4, WK = 1, STAGES = 2;
 };
 struct Small {  // 4 waves of 64 x 64, 64 KB: two workgroups per CU
-  static constexpr int BM = 128, BN = 128, WM = 2, WN = 2, WK = 1, KB = 128, STAGES = 2;
+  static constexpr int BM = 128, BN = 128, WM = 2, WN = 2, WK = 1, STAGES = 2;
 };
 struct Flat {  // 4 waves of 64 x 32, 72 KB: two workgroups per CU
-  static constexpr int BM = 64, BN = 128, WM = 1, WN = 4, WK = 1, KB = 128, STAGES = 3;
+  static constexpr int BM = 64, BN = 128, WM = 1, WN = 4, WK = 1, STAGES = 3;
 };
 struct Split {  // 4 waves, 64 x 64 each of a quarter of K, 128 KB
-  static constexpr int BM = 64, BN = 64, WM = 1, WN = 1, WK = 4, KB = 128, STAGES = 2;
+  static constexpr int BM = 64, BN = 64, WM = 1, WN = 1, WK = 4, STAGES = 2;
 };
 struct Thin {  // 4 waves, 16 x 32 each of a quarter of K, 72 KB: two workgroups per CU
-  static constexpr int BM = 16, BN = 32, WM = 1, WN = 1, WK = 4, KB = 128, STAGES = 3;
+  static constexpr int BM = 16, BN = 32, WM = 1, WN = 1, WK = 4, STAGES = 3;
 };
 
 template <int DT_, int LA_, int LB_, bool PAIR_, bool ALIGNED_, class TILE_>
@@ -333,7 +340,8 @@ struct Product {
   static constexpr bool PAIR = PAIR_, ALIGNED = ALIGNED_;
   using TILE = TILE_;
   static constexpr int BM = TILE::BM, BN = TILE::BN, WM = TILE::WM, WN = TILE::WN;
-  static constexpr int WK = TILE::WK, KB = TILE::KB, STAGES = TILE::STAGES, SUBS = KB / SUBSTEP;
+  static constexpr int WK = TILE::WK;
+  static constexpr int STAGES = TILE::STAGES;
   static_assert(WK == 1 || WM * WN == 1, "waves that split K work alone");
   static constexpr int GROUP = 64 * WM * WN, NT = GROUP * WK;  // threads of a ring, of the workgroup
   static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 blocks per wave
@@ -341,8 +349,8 @@ struct Product {
   static constexpr int STAGE = (BM + BN) * KB, RING = STAGES * STAGE;
   static constexpr int LDS_BYTES = WK * RING;
 
-  using LoadA = TileLoader<DT, LA, BM, GROUP, KB, false>;
-  using LoadB = TileLoader<DT, LB, BN, GROUP, KB, PAIR>;
+  using LoadA = TileLoader<DT, LA, BM, GROUP, false>;
+  using LoadB = TileLoader<DT, LB, BN, GROUP, PAIR>;
   static constexpr int LOADS = LoadA::SLOTS + LoadB::SLOTS;  // direct loads per thread and K step
 
   v4f acc[TM][TN];
@@ -387,11 +395,13 @@ struct Product {
       __builtin_amdgcn_sched_group_barrier(0x8, M - Q, 0);
     }
   }
-  // Every load of this wave but the youngest n has landed, and so has every
-  // LDS read; then the barrier of the waves that share the ring.
+  // Every load of this wave but the youngest N (all of them unless `more` are
+  // behind) has landed, and so has every LDS read; then the barrier of the
+  // waves that share the rings.
   template <int N>
-  __device__ __forceinline__ static void landed() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"(N) : "memory");
+  __device__ __forceinline__ static void landed(bool more) {
+    if (N > 0 && more) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"(N) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     if constexpr (WK == 1) {
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
@@ -420,84 +430,74 @@ struct Product {
     const uint32_t first = (uint32_t)wk * part;
     const uint32_t steps = first >= all ? 0 : all - first < part ? all - first : part;
     if (steps == 0) return;
-    LoadA la[2];
-    LoadB lb[2];
-    la[0].init(p.a[0], nullptr, row0, p.m, p.k, p.lda);
-    lb[0].init(p.b[0], p.b[1], col0, p.n, p.k, p.ldb);
-    la[1].init(p.a[1], nullptr, row0, p.m, p.k, p.lda);
-    lb[1].init(p.b[1], nullptr, col0, p.n, p.k, p.ldb);
-    // Loader of step t's segment and its first k.  A step past the last one
-    // (t up to steps + STAGES - 1) is put past k: all of it reads as zero.
-    auto at = [&](uint32_t t, LoadA* a, LoadB* b) {
-      const uint32_t u = first + t;
-      const bool second = nseg > 1 && u >= per;
-      *a = la[0];
-      *b = lb[0];
-      if (second) {
-        a->base[0] = la[1].base[0];
-        b->base[0] = lb[1].base[0];
-      }
-      return (t >= steps ? per : second ? u - per : u) * BK;
-    };
+    LoadA la;
+    LoadB lb;
+    la.init(p.a[0], nullptr, row0, p.m, p.k, p.lda);
+    lb.init(p.b[0], p.b[1], col0, p.n, p.k, p.ldb);
+    // the second segment's operands lie where the first's do in their matrices
+    const char* const second_a = p.a[1] + (la.base[0] - p.a[0]);
+    const char* const second_b = p.b[1] + (lb.base[0] - p.b[0]);
+    // Step t's segment, and its first k there.
+    auto in_second = [&](uint32_t t) { return nseg > 1 && first + t >= per; };
+    auto k_of = [&](uint32_t t) { return (in_second(t) ? first + t - per : first + t) * BK; };
     v4u fa[2][TM], fb[2][TN];
     if constexpr (ALIGNED) {
       auto start = [&](uint32_t t, lds_char* dst) {
-        LoadA a;
-        LoadB b;
-        const uint32_t k0 = at(t, &a, &b);
-        a.load_direct(k0, dst);
-        b.load_direct(k0, dst + BM * KB);
+        LoadA a = la;
+        LoadB b = lb;
+        a.base[0] = in_second(t) ? second_a : la.base[0];
+        b.base[0] = in_second(t) ? second_b : lb.base[0];
+        a.load_direct(k_of(t), dst);
+        b.load_direct(k_of(t), dst + BM * KB);
       };
 #pragma unroll
-      for (int t = 0; t < STAGES; ++t) start(t, lds + t * STAGE);
-      landed<(STAGES - 1) * LOADS>();
+      for (uint32_t t = 0; t < (uint32_t)STAGES; ++t)
+        if (t < steps) start(t, lds + t * STAGE);
+      landed<(STAGES - 1) * LOADS>(steps >= (uint32_t)STAGES);
 #pragma unroll
       for (int i = 0; i < TM; ++i) read(lds, 0, fa[0], fb[0], i);
       uint32_t cur = 0;  // byte offset of step t's buffer
-      // two substeps a turn, so that the fragment sets alternate by name (an
-      // odd count of single-substep steps ends with one of zeros)
-      for (uint32_t t = 0; t < steps; t += 2 / SUBS) {
+      // the two substeps' fragment sets alternate by name
+      for (uint32_t t = 0; t < steps; ++t) {
+        const uint32_t next = cur + STAGE == (uint32_t)RING ? 0 : cur + STAGE;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t next = cur + STAGE == (uint32_t)RING ? 0 : cur + STAGE;
-          const bool last = SUBS == 1 || h == 1;  // of the step's substeps
-          if (last) {
-            landed<(STAGES - 2) * LOADS>();
-            // with two stages the wait is for every load: steps past the
-            // last one need not be started to keep its count
-            const uint32_t u = t + (SUBS == 1 ? h : 0) + STAGES;
-            if (STAGES > 2 || u < steps) start(u, lds + cur);
+          if (h == 1) {
+            landed<(STAGES - 2) * LOADS>(t + STAGES <= steps);
+            if (t + STAGES < steps) start(t + STAGES, lds + cur);
           }
 #pragma unroll
           for (int i = 0; i < TM; ++i) {
-            read(lds + (last ? next : cur), last ? 0 : 1, fa[1 - h], fb[1 - h], i);
+            // (after the last step: stale, and not used)
+            read(lds + (h ? next : cur), 1 - h, fa[1 - h], fb[1 - h], i);
             multiply(fa[h], fb[h], i);
           }
           interleave<0>();
-          if (last) cur = next;
         }
+        cur = next;
       }
-      landed<0>();
+      landed<0>(false);
     } else {
       // through registers: step t + 1's loads are in flight while t is
       // multiplied
       v4u ra[LoadA::SLOTS], rb[LoadB::SLOTS];
       auto fetch = [&](uint32_t t) {
-        LoadA a;
-        LoadB b;
-        const uint32_t k0 = at(t, &a, &b);
-        a.load_regs(k0, ra);
-        b.load_regs(k0, rb);
+        LoadA a = la;
+        LoadB b = lb;
+        a.base[0] = in_second(t) ? second_a : la.base[0];
+        b.base[0] = in_second(t) ? second_b : lb.base[0];
+        a.load_regs(k_of(t), ra);
+        b.load_regs(k_of(t), rb);
       };
       fetch(0);
       for (uint32_t t = 0; t < steps; ++t) {
         lds_char* buf = lds + (t & 1) * STAGE;
-        la[0].store_regs(ra, buf);
-        lb[0].store_regs(rb, buf + BM * KB);
+        la.store_regs(ra, buf);
+        lb.store_regs(rb, buf + BM * KB);
         if constexpr (WK == 1) __syncthreads();
         if (t + 1 < steps) fetch(t + 1);
 #pragma unroll
-        for (int u = 0; u < SUBS; ++u) {
+        for (int u = 0; u < 2; ++u) {
 #pragma unroll
           for (int i = 0; i < TM; ++i) read(buf, u, fa[u], fb[u], i);
 #pragma unroll
