@@ -35,14 +35,23 @@ namespace {
 struct FfnShape {
   uint64_t rows, hidden, inter, es, pitch;  // pitch: elements per row of h, dg, du (whole chunks)
   uint64_t mid_bytes;                       // one rank's h (dg, du)
+  // one rank's copies of x (dout), of w_gate (w_up), of w_down, where their
+  // rows are not whole 16-byte chunks
+  uint64_t pack_x, pack_up, pack_down;
+  uint64_t workspace(int n, bool backward) const {
+    return (uint64_t)n * ((backward ? 3 : 1) * mid_bytes + (backward ? 2 : 1) * pack_x + 2 * pack_up + pack_down);
+  }
 };
 
 FfnShape shape_of(size_t rows, size_t hidden, size_t inter, int dtype) {
   FfnShape s;
   s.rows = rows, s.hidden = hidden, s.inter = inter;
   s.es = dtype == DT_BF16 ? 2 : 4;
-  s.pitch = (inter + 7) / 8 * 8;
+  s.pitch = Packer::pitch(inter, s.es);
   s.mid_bytes = layer_align(s.rows * s.pitch * s.es);
+  s.pack_x = Packer::bytes(rows, hidden, s.es);
+  s.pack_up = Packer::bytes(inter, hidden, s.es);
+  s.pack_down = Packer::bytes(hidden, inter, s.es);
   return s;
 }
 
@@ -60,7 +69,7 @@ extern "C" {
 
 size_t ar_gated_ffn_workspace(int nranks, size_t rows, size_t hidden, size_t inter, ar_dtype dtype, int backward) {
   if (check_shape(nranks, rows, hidden, inter, 0, (int)dtype) != AR_OK || rows == 0) return 0;
-  return (size_t)nranks * (backward ? 3 : 1) * shape_of(rows, hidden, inter, (int)dtype).mid_bytes;
+  return (size_t)shape_of(rows, hidden, inter, (int)dtype).workspace(nranks, backward != 0);
 }
 
 ar_status ar_gated_ffn(int nranks, const void* const* x, const void* const* w_gate, const void* const* w_up,
@@ -73,7 +82,7 @@ ar_status ar_gated_ffn(int nranks, const void* const* x, const void* const* w_ga
   if (rows == 0) return AR_OK;
   const FfnShape s = shape_of(rows, hidden, inter, (int)dtype);
   const uint64_t xb = s.rows * s.hidden * s.es, wb = s.hidden * s.inter * s.es, gb = s.rows * s.inter * 4;
-  const uint64_t need = (uint64_t)nranks * s.mid_bytes;
+  const uint64_t need = s.workspace(nranks, false);
   LayerBuffers b;
   for (int r = 0; r < nranks; ++r) {
     b.in(x[r], xb);
@@ -94,19 +103,23 @@ ar_status ar_gated_ffn(int nranks, const void* const* x, const void* const* w_ga
 
   ProductPlan up_plan, down_plan;
   up_plan.a.act = (int32_t)act;
+  Packer pack(ws + (uint64_t)nranks * s.mid_bytes, s.es);
   for (int r = 0; r < nranks; ++r) {
-    Problem* p = up_plan.add(s.rows, s.inter, s.hidden, s.hidden, s.hidden, s.pitch, s.es);
-    p->a[0] = (const char*)x[r];
-    p->b[0] = (const char*)w_gate[r];
-    p->b[1] = (const char*)w_up[r];
+    const Packer::Rows px = pack.rows(x[r], s.rows, s.hidden), pg = pack.rows(w_gate[r], s.inter, s.hidden),
+                       pu = pack.rows(w_up[r], s.inter, s.hidden), pd = pack.rows(w_down[r], s.hidden, s.inter);
+    Problem* p = up_plan.add(s.rows, s.inter, s.hidden, px.ld, pg.ld, s.pitch);
+    p->a[0] = px.p;
+    p->b[0] = pg.p;
+    p->b[1] = pu.p;
     p->c[0] = h(r);
     p->c[1] = gate ? (char*)gate[r] : nullptr;
     p->c[2] = up ? (char*)up[r] : nullptr;
-    p = down_plan.add(s.rows, s.hidden, s.inter, s.pitch, s.inter, s.hidden, s.es);
+    p = down_plan.add(s.rows, s.hidden, s.inter, s.pitch, pd.ld, s.hidden);
     p->a[0] = h(r);
-    p->b[0] = (const char*)w_down[r];
+    p->b[0] = pd.p;
     p->c[0] = (char*)out[r];
   }
+  if (pack.launch((hipStream_t)stream) != hipSuccess) return AR_ERR_HIP;
   if (launch_products(PK_GATED, (int)dtype, up_plan, dev, (hipStream_t)stream) != hipSuccess) return AR_ERR_HIP;
   if (launch_products(PK_STORE_NT, (int)dtype, down_plan, dev, (hipStream_t)stream) != hipSuccess) return AR_ERR_HIP;
   return AR_OK;
@@ -123,7 +136,7 @@ ar_status ar_gated_ffn_backward(int nranks, const void* const* dout, const void*
     return AR_ERR_INVALID;
   const FfnShape s = shape_of(rows, hidden, inter, (int)dtype);
   const uint64_t xb = s.rows * s.hidden * s.es, wb = s.hidden * s.inter * s.es, gb = s.rows * s.inter * 4;
-  const uint64_t need = (uint64_t)nranks * 3 * (rows ? s.mid_bytes : 0);
+  const uint64_t need = rows ? s.workspace(nranks, true) : 0;
   LayerBuffers b;
   for (int r = 0; r < nranks; ++r) {
     b.in(dout[r], xb);
@@ -150,30 +163,38 @@ ar_status ar_gated_ffn_backward(int nranks, const void* const* dout, const void*
   ProductPlan mid_plan, dx_plan, dw_plan;
   mid_plan.a.act = (int32_t)act;
   dx_plan.a.nseg = 2;
+  Packer pack(ws + (uint64_t)nranks * 3 * s.mid_bytes, s.es);
   for (int r = 0; r < nranks; ++r) {
-    Problem* p = mid_plan.add(s.rows, s.inter, s.hidden, s.hidden, s.inter, s.pitch, s.es);
-    p->a[0] = (const char*)dout[r];
-    p->b[0] = (const char*)w_down[r];
+    // (with no rows nothing is read, and nothing copied)
+    const uint64_t some = rows ? 1 : 0;
+    const Packer::Rows px = pack.rows(x[r], s.rows, s.hidden), po = pack.rows(dout[r], s.rows, s.hidden),
+                       pg = pack.rows(w_gate[r], some * s.inter, s.hidden),
+                       pu = pack.rows(w_up[r], some * s.inter, s.hidden),
+                       pd = pack.rows(w_down[r], some * s.hidden, s.inter);
+    Problem* p = mid_plan.add(s.rows, s.inter, s.hidden, po.ld, pd.ld, s.pitch);
+    p->a[0] = po.p;
+    p->b[0] = pd.p;
     p->e[0] = (const char*)gate[r];
     p->e[1] = (const char*)up[r];
     for (int i = 0; i < 3; ++i) p->c[i] = mid(r, i);
-    p = dx_plan.add(s.rows, s.hidden, s.inter, s.pitch, s.hidden, s.hidden, s.es);
+    p = dx_plan.add(s.rows, s.hidden, s.inter, s.pitch, pg.ld, s.hidden);
     p->a[0] = mid(r, 0);
     p->a[1] = mid(r, 1);
-    p->b[0] = (const char*)w_gate[r];
-    p->b[1] = (const char*)w_up[r];
+    p->b[0] = pg.p;
+    p->b[1] = pu.p;
     p->c[0] = (char*)dx[r];
     for (int i = 0; i < 2; ++i) {
-      p = dw_plan.add(s.inter, s.hidden, s.rows, s.pitch, s.hidden, s.hidden, s.es);
+      p = dw_plan.add(s.inter, s.hidden, s.rows, s.pitch, px.ld, s.hidden);
       p->a[0] = mid(r, i);
-      p->b[0] = (const char*)x[r];
+      p->b[0] = px.p;
       p->c[0] = (char*)(i ? dw_up[r] : dw_gate[r]);
     }
-    p = dw_plan.add(s.hidden, s.inter, s.rows, s.hidden, s.pitch, s.inter, s.es);
-    p->a[0] = (const char*)dout[r];
+    p = dw_plan.add(s.hidden, s.inter, s.rows, po.ld, s.pitch, s.inter);
+    p->a[0] = po.p;
     p->b[0] = mid(r, 2);
     p->c[0] = (char*)dw_down[r];
   }
+  if (pack.launch((hipStream_t)stream) != hipSuccess) return AR_ERR_HIP;
   if (launch_products(PK_GATED_BWD, (int)dtype, mid_plan, dev, (hipStream_t)stream) != hipSuccess ||
       launch_products(PK_STORE_NN, (int)dtype, dx_plan, dev, (hipStream_t)stream) != hipSuccess ||
       launch_products(PK_STORE_TN, (int)dtype, dw_plan, dev, (hipStream_t)stream) != hipSuccess)

@@ -53,8 +53,6 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-// 16 bytes at any byte address (global memory reads need no alignment)
-typedef uint32_t v4u_any __attribute__((ext_vector_type(4), aligned(1)));
 
 typedef __attribute__((address_space(3))) char lds_char;
 
@@ -221,52 +219,6 @@ struct TileLoader {
     }
   }
 
-  // Unaligned matrices (a row of partial chunks): the same chunks through
-  // registers.  Whole chunks are one 16-byte load at any address; the chunk
-  // that crosses the end of a row (of the matrix's rows, L_R) is gathered by
-  // element, so no byte outside the matrix is read.
-  __device__ __forceinline__ void load_regs(uint32_t k0, v4u* r) const {
-#pragma unroll
-    for (int i = 0; i < SLOTS; ++i) {
-      uint32_t row, chunk;
-      slot(i, &row, &chunk);
-      int h = 0;
-      if constexpr (PAIR) {
-        if (i >= SLOTS / 2) {
-          h = 1;
-          row -= ROWS / 2;
-        }
-      }
-      int valid;
-      const char* src;
-      if constexpr (LAYOUT == L_K) {
-        valid = row < rows ? (int)k - (int)(k0 + chunk * E) : 0;
-        src = base[h] + (uint64_t)row * ldbytes + (uint64_t)(k0 + chunk * E) * ES;
-      } else {
-        valid = k0 + row < k ? (int)rows - (int)(chunk * E) : 0;
-        src = base[h] + (uint64_t)(k0 + row) * ldbytes + chunk * 16;
-      }
-      v4u v = {0, 0, 0, 0};
-      if (valid >= E) {
-        v = *(const v4u_any*)src;
-      } else if (valid > 0) {
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-          if (j < valid) {
-            if constexpr (DT == DT_BF16) v[j / 2] |= (uint32_t)((const uint16_t*)src)[j] << (16 * (j % 2));
-            else v[j] = ((const uint32_t*)src)[j];
-          }
-        }
-      }
-      r[i] = v;
-    }
-  }
-  __device__ __forceinline__ void store_regs(const v4u* r, lds_char* dst) const {
-#pragma unroll
-    for (int i = 0; i < SLOTS; ++i)
-      *(__attribute__((address_space(3))) v4u*)(dst + ((uint32_t)i * NT + threadIdx.x % NT) * 16) = r[i];
-  }
-
   // Fragment of 16 rows from r0 on, substep s: 16 bytes per lane.
   __device__ __forceinline__ static v4u fragment(const lds_char* tile, int r0, int s) {
     const uint32_t lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
@@ -334,10 +286,10 @@ struct Thin {  // 4 waves, 16 x 32 each of a quarter of K, 72 KB: two workgroups
   static constexpr int BM = 16, BN = 32, WM = 1, WN = 1, WK = 4, STAGES = 3;
 };
 
-template <int DT_, int LA_, int LB_, bool PAIR_, bool ALIGNED_, class TILE_>
+template <int DT_, int LA_, int LB_, bool PAIR_, class TILE_>
 struct Product {
   static constexpr int DT = DT_, LA = LA_, LB = LB_;
-  static constexpr bool PAIR = PAIR_, ALIGNED = ALIGNED_;
+  static constexpr bool PAIR = PAIR_;
   using TILE = TILE_;
   static constexpr int BM = TILE::BM, BN = TILE::BN, WM = TILE::WM, WN = TILE::WN;
   static constexpr int WK = TILE::WK;
@@ -441,70 +393,41 @@ struct Product {
     auto in_second = [&](uint32_t t) { return nseg > 1 && first + t >= per; };
     auto k_of = [&](uint32_t t) { return (in_second(t) ? first + t - per : first + t) * BK; };
     v4u fa[2][TM], fb[2][TN];
-    if constexpr (ALIGNED) {
-      auto start = [&](uint32_t t, lds_char* dst) {
-        LoadA a = la;
-        LoadB b = lb;
-        a.base[0] = in_second(t) ? second_a : la.base[0];
-        b.base[0] = in_second(t) ? second_b : lb.base[0];
-        a.load_direct(k_of(t), dst);
-        b.load_direct(k_of(t), dst + BM * KB);
-      };
+    auto start = [&](uint32_t t, lds_char* dst) {
+      LoadA a = la;
+      LoadB b = lb;
+      a.base[0] = in_second(t) ? second_a : la.base[0];
+      b.base[0] = in_second(t) ? second_b : lb.base[0];
+      a.load_direct(k_of(t), dst);
+      b.load_direct(k_of(t), dst + BM * KB);
+    };
 #pragma unroll
-      for (uint32_t t = 0; t < (uint32_t)STAGES; ++t)
-        if (t < steps) start(t, lds + t * STAGE);
-      landed<(STAGES - 1) * LOADS>(steps >= (uint32_t)STAGES);
+    for (uint32_t t = 0; t < (uint32_t)STAGES; ++t)
+      if (t < steps) start(t, lds + t * STAGE);
+    landed<(STAGES - 1) * LOADS>(steps >= (uint32_t)STAGES);
 #pragma unroll
-      for (int i = 0; i < TM; ++i) read(lds, 0, fa[0], fb[0], i);
-      uint32_t cur = 0;  // byte offset of step t's buffer
-      // the two substeps' fragment sets alternate by name
-      for (uint32_t t = 0; t < steps; ++t) {
-        const uint32_t next = cur + STAGE == (uint32_t)RING ? 0 : cur + STAGE;
+    for (int i = 0; i < TM; ++i) read(lds, 0, fa[0], fb[0], i);
+    uint32_t cur = 0;  // byte offset of step t's buffer
+    // the two substeps' fragment sets alternate by name
+    for (uint32_t t = 0; t < steps; ++t) {
+      const uint32_t next = cur + STAGE == (uint32_t)RING ? 0 : cur + STAGE;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h == 1) {
-            landed<(STAGES - 2) * LOADS>(t + STAGES <= steps);
-            if (t + STAGES < steps) start(t + STAGES, lds + cur);
-          }
-#pragma unroll
-          for (int i = 0; i < TM; ++i) {
-            // (after the last step: stale, and not used)
-            read(lds + (h ? next : cur), 1 - h, fa[1 - h], fb[1 - h], i);
-            multiply(fa[h], fb[h], i);
-          }
-          interleave<0>();
+      for (int h = 0; h < 2; ++h) {
+        if (h == 1) {
+          landed<(STAGES - 2) * LOADS>(t + STAGES <= steps);
+          if (t + STAGES < steps) start(t + STAGES, lds + cur);
         }
-        cur = next;
-      }
-      landed<0>(false);
-    } else {
-      // through registers: step t + 1's loads are in flight while t is
-      // multiplied
-      v4u ra[LoadA::SLOTS], rb[LoadB::SLOTS];
-      auto fetch = [&](uint32_t t) {
-        LoadA a = la;
-        LoadB b = lb;
-        a.base[0] = in_second(t) ? second_a : la.base[0];
-        b.base[0] = in_second(t) ? second_b : lb.base[0];
-        a.load_regs(k_of(t), ra);
-        b.load_regs(k_of(t), rb);
-      };
-      fetch(0);
-      for (uint32_t t = 0; t < steps; ++t) {
-        lds_char* buf = lds + (t & 1) * STAGE;
-        la.store_regs(ra, buf);
-        lb.store_regs(rb, buf + BM * KB);
-        if constexpr (WK == 1) __syncthreads();
-        if (t + 1 < steps) fetch(t + 1);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-#pragma unroll
-          for (int i = 0; i < TM; ++i) read(buf, u, fa[u], fb[u], i);
-#pragma unroll
-          for (int i = 0; i < TM; ++i) multiply(fa[u], fb[u], i);
+        for (int i = 0; i < TM; ++i) {
+          // (after the last step: stale, and not used)
+          read(lds + (h ? next : cur), 1 - h, fa[1 - h], fb[1 - h], i);
+          multiply(fa[h], fb[h], i);
         }
+        interleave<0>();
       }
+      cur = next;
     }
+    landed<0>(false);
   }
 
   // Hand the finished tile out by rows: a lane of the accumulators holds 4
@@ -653,17 +576,15 @@ __device__ __forceinline__ int locate(const ProductArgs& a, uint32_t* row0, uint
 // Collects the problems of a launch.
 struct ProductPlan {
   ProductArgs a;
-  bool aligned = true;  // every operand's rows start on 16-byte boundaries
   uint64_t tiles = 0;
 
   ProductPlan() { memset(&a, 0, sizeof(a)); a.nseg = 1; }
 
-  // Operand checks of p, then a place for it; `es`: element bytes.
-  Problem* add(uint64_t m, uint64_t n, uint64_t k, uint64_t lda, uint64_t ldb, uint64_t ldc, uint64_t es) {
+  // Rows of both operands start on 16-byte boundaries (Packer).
+  Problem* add(uint64_t m, uint64_t n, uint64_t k, uint64_t lda, uint64_t ldb, uint64_t ldc) {
     Problem* p = &a.p[a.nprob++];
     p->m = (uint32_t)m, p->n = (uint32_t)n, p->k = (uint32_t)k;
     p->lda = (uint32_t)lda, p->ldb = (uint32_t)ldb, p->ldc = (uint32_t)ldc;
-    if (k && ((lda * es) % 16 || (ldb * es) % 16)) aligned = false;
     return p;
   }
   // Tiles of every problem for a kernel whose tile covers bm x cols of C.

@@ -1,5 +1,5 @@
 // product_kernels.hpp -- the product kernels of the layer operators: one kernel
-// template over (type, layouts, epilogue, tile size, alignment), instantiated
+// template over (type, layouts, epilogue, tile class), instantiated
 // per payload type by products_bf16.hip and products_f32.hip.
 #pragma once
 
@@ -250,34 +250,27 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
 constexpr int layout_a(int kind) { return kind == PK_STORE_TN ? L_R : L_K; }
 constexpr int layout_b(int kind) { return kind >= PK_STORE_NN ? L_R : L_K; }
 
-template <int KIND, int DT, bool ALIGNED, class TILE, uint32_t ACT>
+template <int KIND, int DT, class TILE, uint32_t ACT>
 hipError_t launch(ProductPlan& plan, hipStream_t stream) {
-  using P = Product<DT, layout_a(KIND), layout_b(KIND), KIND == PK_GATED, ALIGNED, TILE>;
+  using P = Product<DT, layout_a(KIND), layout_b(KIND), KIND == PK_GATED, TILE>;
   if (!plan.cut(P::BM, P::COLS)) return hipErrorInvalidValue;
   if (plan.tiles == 0) return hipSuccess;
   hipLaunchKernelGGL((product_kernel<P, KIND, ACT>), dim3((unsigned)plan.tiles), dim3(P::NT), 0, stream, plan.a);
   return hipGetLastError();
 }
 
-template <int KIND, int DT, bool ALIGNED, uint32_t ACT>
-hipError_t launch_tile(int tile, ProductPlan& plan, hipStream_t stream) {
-  switch (tile) {
-    case TILE_LARGE:
-      if constexpr (ALIGNED && DT == DT_BF16) return launch<KIND, DT, true, Large, ACT>(plan, stream);
-      else return hipErrorInvalidValue;  // product_tile takes it for neither
-    case TILE_SMALL: return launch<KIND, DT, ALIGNED, Small, ACT>(plan, stream);
-    case TILE_FLAT: return launch<KIND, DT, ALIGNED, Flat, ACT>(plan, stream);
-    case TILE_SPLIT: return launch<KIND, DT, ALIGNED, Split, ACT>(plan, stream);
-    case TILE_THIN: return launch<KIND, DT, ALIGNED, Thin, ACT>(plan, stream);
-  }
-  return hipErrorInvalidValue;
-}
-
 template <int KIND, int DT, uint32_t ACT = ACT_SILU>
 hipError_t launch_kind(ProductPlan& plan, int device, hipStream_t stream) {
-  const int tile = product_tile(KIND, DT, plan, device);
-  return plan.aligned ? launch_tile<KIND, DT, true, ACT>(tile, plan, stream)
-                      : launch_tile<KIND, DT, false, ACT>(tile, plan, stream);
+  switch (product_tile(KIND, DT, plan, device)) {
+    case TILE_LARGE:
+      if constexpr (DT == DT_BF16) return launch<KIND, DT, Large, ACT>(plan, stream);
+      else return hipErrorInvalidValue;  // product_tile does not take it
+    case TILE_SMALL: return launch<KIND, DT, Small, ACT>(plan, stream);
+    case TILE_FLAT: return launch<KIND, DT, Flat, ACT>(plan, stream);
+    case TILE_SPLIT: return launch<KIND, DT, Split, ACT>(plan, stream);
+    case TILE_THIN: return launch<KIND, DT, Thin, ACT>(plan, stream);
+  }
+  return hipErrorInvalidValue;
 }
 
 template <int KIND, int DT>

@@ -1,4 +1,5 @@
-// products.hip -- tile choice of the product kernels.
+// products.hip -- tile choice of the product kernels, and copies of matrices
+// whose rows are not whole 16-byte chunks.
 //
 // A launch takes the tile class with the smallest estimated time.  A
 // workgroup of class c takes fixed + steps x (alone | full) us, a step being
@@ -39,7 +40,70 @@ constexpr ClassCost COST[TILE_CLASSES] = {
 };
 constexpr double F32_FLOPS_PER_CU_US = 0.55e6;  // of 0.61e6 (16x16x4 at 2.4 GHz)
 
+constexpr int PACK_THREADS = 256, PACK_CHUNKS = 4;  // chunks per thread
+
+typedef uint32_t v4u_any __attribute__((ext_vector_type(4), aligned(2)));
+
+// Each thread makes 16-byte chunks of the copies: one load at any (element)
+// address for a whole chunk, element by element at a row's end, so that
+// nothing past the matrix is read.
+__global__ __launch_bounds__(PACK_THREADS) void pack_kernel(Packer::Args a) {
+  int q = 0;
+  while (q + 1 < a.n && blockIdx.x >= a.e[q + 1].first) ++q;
+  const Packer::Entry& e = a.e[q];
+  const uint64_t total = e.rows * e.chunks;
+  const uint32_t per = 16 / a.es;
+  const uint64_t base = (uint64_t)(blockIdx.x - e.first) * (PACK_THREADS * PACK_CHUNKS) + threadIdx.x;
+#pragma unroll
+  for (int i = 0; i < PACK_CHUNKS; ++i) {
+    const uint64_t t = base + (uint64_t)i * PACK_THREADS;
+    if (t >= total) break;
+    const uint64_t row = t / e.chunks;
+    const uint32_t col = (uint32_t)(t % e.chunks) * per;
+    const char* src = e.src + (row * e.cols + col) * a.es;
+    v4u v = {0, 0, 0, 0};
+    if (col + per <= e.cols) {
+      v = *(const v4u_any*)src;
+    } else if (a.es == 2) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (col + j < e.cols) v[j / 2] |= (uint32_t)((const uint16_t*)src)[j] << (16 * (j % 2));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (col + j < e.cols) v[j] = ((const uint32_t*)src)[j];
+    }
+    *(v4u*)(e.dst + t * 16) = v;
+  }
+}
+
 }  // namespace
+
+Packer::Rows Packer::rows(const void* src, uint64_t rows, uint64_t cols) {
+  if ((cols * es_) % 16 == 0 || rows == 0) return {(const char*)src, pitch(cols, es_)};
+  for (int i = 0; i < a_.n; ++i)  // the same matrix on several ranks
+    if (a_.e[i].src == (const char*)src && a_.e[i].rows == rows && a_.e[i].cols == cols)
+      return {a_.e[i].dst, pitch(cols, es_)};
+  Entry& e = a_.e[a_.n++];
+  e.src = (const char*)src;
+  e.dst = space_;
+  e.rows = rows;
+  e.cols = (uint32_t)cols;
+  e.chunks = (uint32_t)(pitch(cols, es_) * es_ / 16);
+  e.first = (uint32_t)blocks_;
+  blocks_ += (rows * e.chunks + PACK_THREADS * PACK_CHUNKS - 1) / (PACK_THREADS * PACK_CHUNKS);
+  space_ += bytes(rows, cols, es_);
+  return {e.dst, pitch(cols, es_)};
+}
+
+hipError_t Packer::launch(hipStream_t stream) const {
+  if (!blocks_) return hipSuccess;
+  if (blocks_ >= (1ull << 31)) return hipErrorInvalidValue;
+  Args a = a_;
+  a.es = (int32_t)es_;
+  hipLaunchKernelGGL(pack_kernel, dim3((unsigned)blocks_), dim3(PACK_THREADS), 0, stream, a);
+  return hipGetLastError();
+}
 
 int product_tile(int kind, int dtype, const ProductPlan& plan, int device) {
   int n_cu = 0;
@@ -52,7 +116,7 @@ int product_tile(int kind, int dtype, const ProductPlan& plan, int device) {
   int best = TILE_SMALL;
   double best_us = 1e30;
   for (int c = 0; c < TILE_CLASSES; ++c) {
-    if (c == TILE_LARGE && (!plan.aligned || dtype != DT_BF16)) continue;
+    if (c == TILE_LARGE && dtype != DT_BF16) continue;
     if (c == TILE_THIN && max_m > (uint32_t)Thin::BM) continue;
     const ClassCost& k = COST[c];
     double tiles = 0, work = 0, longest = 0;  // work: steps of all tiles
@@ -71,10 +135,6 @@ int product_tile(int kind, int dtype, const ProductPlan& plan, int device) {
       const double mm = 2.0 * k.bm * k.bn * per_step * k.parts / F32_FLOPS_PER_CU_US;
       alone = mm > alone ? mm : alone;
       full = mm * k.resident > full ? mm * k.resident : full;
-    }
-    if (!plan.aligned) {  // through registers
-      alone *= 1.6;
-      full *= 1.6;
     }
     const double slots = cus * k.resident;
     const double rounds = (double)(uint64_t)(tiles / slots);

@@ -47,6 +47,50 @@ constexpr uint32_t tile_cols(int tile) {
 }
 constexpr uint32_t MIN_TILE_COLS = Thin::BN;
 
+// Products read rows that start on 16-byte boundaries.  A matrix whose rows do
+// not (an odd width) is copied into the workspace once per call, its rows
+// padded with zeros to whole 16-byte chunks.  Measured against reading such
+// rows in place through registers, element by element at their ends: the
+// copies cost less than the products gain (cross entropy step of 611 rows,
+// width 1003, vocabulary 10007 over 3 ranks, bf16: 290 -> 131 us).
+class Packer {
+ public:
+  struct Rows {
+    const char* p;
+    uint64_t ld;
+  };
+  // Bytes of the copy of a [rows, cols] matrix; 0 if none is needed.
+  static uint64_t bytes(uint64_t rows, uint64_t cols, uint64_t es) {
+    return (cols * es) % 16 ? (rows * pitch(cols, es) * es + 255) & ~255ull : 0;
+  }
+  static uint64_t pitch(uint64_t cols, uint64_t es) { return (cols * es + 15) / 16 * 16 / es; }
+
+  Packer(char* space, uint64_t es) : space_(space), es_(es) {}
+  // A row-major [rows, cols] matrix without gaps, or its copy to be.
+  Rows rows(const void* src, uint64_t rows, uint64_t cols);
+  // Make the copies (one kernel, or none).
+  hipError_t launch(hipStream_t stream) const;
+
+  static constexpr int MAX = 5 * MAX_RANKS;
+  struct Entry {
+    const char* src;
+    char* dst;
+    uint64_t rows;
+    uint32_t cols, chunks;  // elements, 16-byte chunks of a row
+    uint32_t first;         // first workgroup
+  };
+  struct Args {
+    Entry e[MAX];
+    int32_t n, es;
+  };
+
+ private:
+  char* space_;
+  uint64_t es_;
+  Args a_ = {};
+  uint64_t blocks_ = 0;
+};
+
 hipError_t launch_products_bf16(int kind, ProductPlan& plan, int device, hipStream_t stream);
 hipError_t launch_products_f32(int kind, ProductPlan& plan, int device, hipStream_t stream);
 inline hipError_t launch_products(int kind, int dtype, ProductPlan& plan, int device, hipStream_t stream) {

@@ -29,7 +29,7 @@ struct CombineArgs {
   const float2* part[MAX_RANKS];  // [tiles of the rank][rows]
   float* loss[MAX_RANKS];
   float* lse[MAX_RANKS];
-  uint32_t tiles[MAX_RANKS];
+  uint32_t tiles[MAX_RANKS], max_tiles;
   const float* at;  // target's logit per row
   const int64_t* target;
   uint64_t vocab;
@@ -50,9 +50,17 @@ __global__ __launch_bounds__(COMBINE_THREADS) void combine_kernel(CombineArgs a,
   const uint64_t row = (uint64_t)blockIdx.x * rows_per_wg + r;
   float2 x = make_float2(-INFINITY, 0.f);
   if (row < a.rows) {
-    for (int q = 0; q < a.nranks; ++q) {
-      const float2* p = a.part[q] + row;
-      for (uint32_t t = slot; t < a.tiles[q]; t += slots) x = merge_stats(x, p[(uint64_t)t * a.rows]);
+    // one tile of every rank at a time: their loads go out together
+    for (uint32_t t = slot; t < a.max_tiles; t += slots) {
+      float2 y[MAX_RANKS];
+#pragma unroll
+      for (int q = 0; q < MAX_RANKS; ++q) {
+        y[q] = make_float2(-INFINITY, 0.f);
+        if (q < a.nranks && t < a.tiles[q]) y[q] = a.part[q][(uint64_t)t * a.rows + row];
+      }
+#pragma unroll
+      for (int q = 0; q < MAX_RANKS; ++q)
+        if (q < a.nranks) x = merge_stats(x, y[q]);
     }
   }
   s[threadIdx.x] = x;
@@ -79,6 +87,7 @@ struct XentShape {
   uint64_t rows, hidden, vocab, es;
   uint64_t shard[MAX_RANKS], start[MAX_RANKS], max_shard;
   uint64_t part_tiles;  // partials per row and rank, at the smallest tile
+  uint64_t pack_bytes;  // copies of every rank's x and w, where their rows are not whole 16-byte chunks
 };
 
 XentShape shape_of(int n, size_t rows, size_t hidden, size_t vocab, int dtype) {
@@ -92,6 +101,9 @@ XentShape shape_of(int n, size_t rows, size_t hidden, size_t vocab, int dtype) {
   }
   s.max_shard = b;
   s.part_tiles = (b + MIN_TILE_COLS - 1) / MIN_TILE_COLS;
+  s.pack_bytes = 0;
+  for (int r = 0; r < n; ++r)
+    s.pack_bytes += Packer::bytes(s.rows, s.hidden, s.es) + Packer::bytes(s.shard[r], s.hidden, s.es);
   return s;
 }
 
@@ -134,9 +146,9 @@ size_t ar_linear_cross_entropy_workspace(int nranks, size_t rows, size_t hidden,
   const XentShape s = shape_of(nranks, rows, hidden, vocab, (int)dtype);
   if (backward) {
     const BackwardSpace b = space_of(s, nranks, (int)dtype, piece);
-    return (size_t)nranks * (b.d_bytes + b.acc_bytes);
+    return (size_t)((uint64_t)nranks * (b.d_bytes + b.acc_bytes) + s.pack_bytes);
   }
-  return (size_t)(layer_align(s.rows * 4) + (uint64_t)nranks * layer_align(s.part_tiles * s.rows * 8));
+  return (size_t)(layer_align(s.rows * 4) + (uint64_t)nranks * layer_align(s.part_tiles * s.rows * 8) + s.pack_bytes);
 }
 
 ar_status ar_linear_cross_entropy(int nranks, const void* const* x, const void* const* w, const int64_t* target,
@@ -148,7 +160,7 @@ ar_status ar_linear_cross_entropy(int nranks, const void* const* x, const void* 
   if (rows == 0) return AR_OK;
   const XentShape s = shape_of(nranks, rows, hidden, vocab, (int)dtype);
   const uint64_t at_bytes = layer_align(s.rows * 4), part_bytes = layer_align(s.part_tiles * s.rows * 8);
-  const uint64_t need = at_bytes + (uint64_t)nranks * part_bytes;
+  const uint64_t need = at_bytes + (uint64_t)nranks * part_bytes + s.pack_bytes;
   LayerBuffers b;
   for (int r = 0; r < nranks; ++r) {
     b.in(x[r], s.rows * s.hidden * s.es);
@@ -168,25 +180,29 @@ ar_status ar_linear_cross_entropy(int nranks, const void* const* x, const void* 
   ProductPlan plan;
   plan.a.target = target;
   plan.a.vocab = s.vocab;
+  Packer pack(ws + at_bytes + (uint64_t)nranks * part_bytes, s.es);
   for (int r = 0; r < nranks; ++r) {
     c.part[r] = (const float2*)(ws + at_bytes + (uint64_t)r * part_bytes);
     c.loss[r] = loss[r];
     c.lse[r] = lse[r];
     if (!s.shard[r]) continue;
-    Problem* p = plan.add(s.rows, s.shard[r], s.hidden, s.hidden, s.hidden, 0, s.es);
-    p->a[0] = (const char*)x[r];
-    p->b[0] = (const char*)w[r];
+    const Packer::Rows px = pack.rows(x[r], s.rows, s.hidden), pw = pack.rows(w[r], s.shard[r], s.hidden);
+    Problem* p = plan.add(s.rows, s.shard[r], s.hidden, px.ld, pw.ld, 0);
+    p->a[0] = px.p;
+    p->b[0] = pw.p;
     p->c[0] = (char*)c.part[r];
     p->c[1] = ws;
     p->col0 = s.start[r];
   }
   const uint64_t cols = tile_cols(product_tile(PK_STATS, (int)dtype, plan, dev));
   for (int r = 0; r < nranks; ++r) c.tiles[r] = (uint32_t)((s.shard[r] + cols - 1) / cols);
+  c.max_tiles = c.tiles[0];  // the first shard is the longest
   c.at = (const float*)ws;
   c.target = target;
   c.vocab = s.vocab;
   c.rows = (uint32_t)s.rows;
   c.nranks = nranks;
+  if (pack.launch((hipStream_t)stream) != hipSuccess) return AR_ERR_HIP;
   if (launch_products(PK_STATS, (int)dtype, plan, dev, (hipStream_t)stream) != hipSuccess) return AR_ERR_HIP;
   uint32_t per = 1;
   while (per < 64 && per < s.rows) per *= 2;
@@ -205,7 +221,7 @@ ar_status ar_linear_cross_entropy_backward(int nranks, const float* grad_loss, c
   if (!x || !w || !lse || !dx || !dw) return AR_ERR_INVALID;
   const XentShape s = shape_of(nranks, rows, hidden, vocab, (int)dtype);
   const BackwardSpace sp = space_of(s, nranks, (int)dtype, piece);
-  const uint64_t need = rows ? (uint64_t)nranks * (sp.d_bytes + sp.acc_bytes) : 0;
+  const uint64_t need = rows ? (uint64_t)nranks * (sp.d_bytes + sp.acc_bytes) + s.pack_bytes : 0;
   const uint64_t xb = s.rows * s.hidden * s.es;
   LayerBuffers b;
   for (int r = 0; r < nranks; ++r) {
@@ -224,6 +240,13 @@ ar_status ar_linear_cross_entropy_backward(int nranks, const float* grad_loss, c
   if (hipGetDevice(&dev) != hipSuccess) return AR_ERR_HIP;
   char* ws = (char*)workspace;
   const uint64_t pieces = (s.max_shard + sp.piece - 1) / sp.piece;
+  Packer pack(ws + (uint64_t)nranks * (sp.d_bytes + sp.acc_bytes), s.es);
+  Packer::Rows px[MAX_RANKS], pw[MAX_RANKS];
+  for (int r = 0; r < nranks; ++r) {  // (with no rows nothing is read, and nothing copied)
+    px[r] = pack.rows(x[r], s.rows, s.hidden);
+    pw[r] = pack.rows(w[r], rows ? s.shard[r] : 0, s.hidden);
+  }
+  if (pack.launch((hipStream_t)stream) != hipSuccess) return AR_ERR_HIP;
   for (uint64_t i = 0; i < pieces; ++i) {
     ProductPlan d_plan, dx_plan, dw_plan;
     d_plan.a.target = target;
@@ -235,21 +258,21 @@ ar_status ar_linear_cross_entropy_backward(int nranks, const float* grad_loss, c
       if (first >= umax(s.shard[r], 1)) continue;
       const uint64_t len = umin(sp.piece, s.shard[r] - first);
       char* d = ws + (uint64_t)r * sp.d_bytes;
-      const char* wp = (const char*)w[r] + first * s.hidden * s.es;
+      const char* wp = pw[r].p + first * pw[r].ld * s.es;
       Problem* p;
       if (len) {
-        p = d_plan.add(s.rows, len, s.hidden, s.hidden, s.hidden, sp.piece, s.es);
-        p->a[0] = (const char*)x[r];
+        p = d_plan.add(s.rows, len, s.hidden, px[r].ld, pw[r].ld, sp.piece);
+        p->a[0] = px[r].p;
         p->b[0] = wp;
         p->c[0] = d;
         p->e[0] = (const char*)lse[r];
         p->col0 = s.start[r] + first;
-        p = dw_plan.add(len, s.hidden, s.rows, sp.piece, s.hidden, s.hidden, s.es);
+        p = dw_plan.add(len, s.hidden, s.rows, sp.piece, px[r].ld, s.hidden);
         p->a[0] = d;
-        p->b[0] = (const char*)x[r];
+        p->b[0] = px[r].p;
         p->c[0] = (char*)dw[r] + first * s.hidden * s.es;
       }
-      p = dx_plan.add(s.rows, s.hidden, len, sp.piece, s.hidden, s.hidden, s.es);
+      p = dx_plan.add(s.rows, s.hidden, len, sp.piece, pw[r].ld, s.hidden);
       p->a[0] = d;
       p->b[0] = wp;
       p->c[0] = (char*)dx[r];
