@@ -11,8 +11,8 @@
 //            dx = dg Wg + du Wu;  dWg = dg^T x, dWu = du^T x, dWd = dout^T h.
 //   dh never reaches memory: the tile that holds it writes dg, du and the
 //   h that dWd needs (recomputed from g and u: one store instead of keeping h
-//   from the forward pass).  dx is one product with two K segments.  The
-//   three weight gradients of every rank are one launch.
+//   from the forward pass).  dx is one product with two K segments.  dx and
+//   the three weight gradients of every rank are one launch.
 //
 // Roundings to bf16 beside the stored results: h, dg and du, operands of the
 // matrix cores; half a bf16 step of the value each, so that one rounding lies
@@ -160,44 +160,52 @@ ar_status ar_gated_ffn_backward(int nranks, const void* const* dout, const void*
   auto mid = [&](int r, int i) { return ws + ((uint64_t)r * 3 + i) * s.mid_bytes; };  // dg, du, h
 
   // With no rows every weight gradient is a product with k = 0: zeros.
-  ProductPlan mid_plan, dx_plan, dw_plan;
+  ProductPlan mid_plan, grads;
   mid_plan.a.act = (int32_t)act;
-  dx_plan.a.nseg = 2;
   Packer pack(ws + (uint64_t)nranks * 3 * s.mid_bytes, s.es);
+  Packer::Rows px[MAX_RANKS], po[MAX_RANKS];
   for (int r = 0; r < nranks; ++r) {
     // (with no rows nothing is read, and nothing copied)
     const uint64_t some = rows ? 1 : 0;
-    const Packer::Rows px = pack.rows(x[r], s.rows, s.hidden), po = pack.rows(dout[r], s.rows, s.hidden),
-                       pg = pack.rows(w_gate[r], some * s.inter, s.hidden),
+    px[r] = pack.rows(x[r], s.rows, s.hidden);
+    po[r] = pack.rows(dout[r], s.rows, s.hidden);
+    const Packer::Rows pg = pack.rows(w_gate[r], some * s.inter, s.hidden),
                        pu = pack.rows(w_up[r], some * s.inter, s.hidden),
                        pd = pack.rows(w_down[r], some * s.hidden, s.inter);
-    Problem* p = mid_plan.add(s.rows, s.inter, s.hidden, po.ld, pd.ld, s.pitch);
-    p->a[0] = po.p;
+    Problem* p = mid_plan.add(s.rows, s.inter, s.hidden, po[r].ld, pd.ld, s.pitch);
+    p->a[0] = po[r].p;
     p->b[0] = pd.p;
-    p->e[0] = (const char*)gate[r];
-    p->e[1] = (const char*)up[r];
+    p->a[1] = (const char*)gate[r];
+    p->b[1] = (const char*)up[r];
     for (int i = 0; i < 3; ++i) p->c[i] = mid(r, i);
-    p = dx_plan.add(s.rows, s.hidden, s.inter, s.pitch, pg.ld, s.hidden);
+    p = grads.add(s.rows, s.hidden, s.inter, s.pitch, pg.ld, s.hidden);
+    p->nseg = 2;
     p->a[0] = mid(r, 0);
     p->a[1] = mid(r, 1);
     p->b[0] = pg.p;
     p->b[1] = pu.p;
     p->c[0] = (char*)dx[r];
+  }
+  grads.head = nranks;
+  // With no rows every weight gradient is a product with k = 0: zeros.
+  for (int r = 0; r < nranks; ++r) {
+    Problem* p;
     for (int i = 0; i < 2; ++i) {
-      p = dw_plan.add(s.inter, s.hidden, s.rows, s.pitch, px.ld, s.hidden);
+      p = grads.add(s.inter, s.hidden, s.rows, s.pitch, px[r].ld, s.hidden);
       p->a[0] = mid(r, i);
-      p->b[0] = px.p;
+      p->b[0] = px[r].p;
       p->c[0] = (char*)(i ? dw_up[r] : dw_gate[r]);
+      p->mode = GRAD_TN;
     }
-    p = dw_plan.add(s.hidden, s.inter, s.rows, po.ld, s.pitch, s.inter);
-    p->a[0] = po.p;
+    p = grads.add(s.hidden, s.inter, s.rows, po[r].ld, s.pitch, s.inter);
+    p->a[0] = po[r].p;
     p->b[0] = mid(r, 2);
     p->c[0] = (char*)dw_down[r];
+    p->mode = GRAD_TN;
   }
-  if (pack.launch((hipStream_t)stream) != hipSuccess) return AR_ERR_HIP;
-  if (launch_products(PK_GATED_BWD, (int)dtype, mid_plan, dev, (hipStream_t)stream) != hipSuccess ||
-      launch_products(PK_STORE_NN, (int)dtype, dx_plan, dev, (hipStream_t)stream) != hipSuccess ||
-      launch_products(PK_STORE_TN, (int)dtype, dw_plan, dev, (hipStream_t)stream) != hipSuccess)
+  if (pack.launch((hipStream_t)stream) != hipSuccess ||
+      launch_products(PK_GATED_BWD, (int)dtype, mid_plan, dev, (hipStream_t)stream) != hipSuccess ||
+      launch_products(PK_GRADS, (int)dtype, grads, dev, (hipStream_t)stream) != hipSuccess)
     return AR_ERR_HIP;
   return AR_OK;
 }

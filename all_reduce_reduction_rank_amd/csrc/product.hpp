@@ -58,7 +58,7 @@ typedef __attribute__((address_space(3))) char lds_char;
 
 constexpr int KB = 128;  // bytes of k per operand row and K step: a cache line, two substeps
 constexpr uint32_t OUT_OF_RANGE = 0x7fffff00u;  // beyond every descriptor (at most 2^30 bytes)
-constexpr int MAX_PROBLEMS = 3 * MAX_RANKS;
+constexpr int MAX_PROBLEMS = 4 * MAX_RANKS;
 
 template <int DT>
 struct KElem {
@@ -68,28 +68,32 @@ struct KElem {
 
 // One product of a launch.  `first` .. `first` + tiles_m * tiles_n are its
 // tiles in the launch.  With two K segments, C = a[0] b[0]^T + a[1] b[1]^T;
-// a paired product has b[0] and b[1] side by side in every tile.
+// a paired product has b[0] and b[1] side by side in every tile.  Elsewhere
+// a[1] and b[1] are what the epilogue reads.
 struct Problem {
   const char* a[2];
   const char* b[2];
   char* c[3];
-  const char* e[2];
   uint64_t col0;  // first column's index in the whole matrix (vocabulary offset)
   uint32_t m, n, k;
   uint32_t lda, ldb, ldc;  // elements between rows of storage
   uint32_t tiles_m, tiles_n, first;
-  uint32_t mode;  // accumulation over launches
+  uint32_t nseg;  // K segments
+  uint32_t mode;  // what the epilogue (and PK_GRADS' layout) goes by
 };
 
-struct ProductArgs {
+struct ProductArgs {  // a kernel's arguments: at most 4 KB
   Problem p[MAX_PROBLEMS];
   const int64_t* target;  // cross entropy: per row
   const float* grad;      // cross entropy: per row
   uint64_t vocab;         // cross entropy: targets outside [0, vocab) are ignored
-  int32_t nprob, nseg;
+  int32_t nprob;
   int32_t act;     // gated kinds
   uint32_t tiles;  // of all problems
+  uint32_t head;   // of the problems that start first (ProductPlan::head)
 };
+
+static_assert(sizeof(ProductArgs) <= 4096, "");
 
 // Workgroup -> tile.  Workgroups go to the XCDs round robin; XCD x takes the
 // x-th contiguous eighth of the tiles, so the tiles that share operand panels
@@ -291,6 +295,7 @@ struct Product {
   static constexpr int DT = DT_, LA = LA_, LB = LB_;
   static constexpr bool PAIR = PAIR_;
   using TILE = TILE_;
+  using TN_ = Product<DT_, L_R, L_R, false, TILE_>;  // the same tile of a dy^T x product
   static constexpr int BM = TILE::BM, BN = TILE::BN, WM = TILE::WM, WN = TILE::WN;
   static constexpr int WK = TILE::WK;
   static constexpr int STAGES = TILE::STAGES;
@@ -367,7 +372,7 @@ struct Product {
   // an LDS read.  Before the last substep of step t every wave has read all
   // of t, and step t + 1 must have landed: one barrier there frees step t's
   // buffer for step t + STAGES and publishes t + 1.
-  __device__ __forceinline__ void run(const Problem& p, int nseg, uint32_t row0, uint32_t col0, char* smem) {
+  __device__ __forceinline__ void run(const Problem& p, uint32_t row0, uint32_t col0, char* smem) {
     const int wk = WK == 1 ? 0 : uniform((int)(threadIdx.x / GROUP));
     lds_char* lds = (lds_char*)smem + wk * RING;
 #pragma unroll
@@ -376,7 +381,7 @@ struct Product {
       for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
     constexpr uint32_t BK = LoadA::BK;
     const uint32_t per = (p.k + BK - 1) / BK;
-    const uint32_t all = per * (uint32_t)nseg;
+    const uint32_t all = per * p.nseg;
     // this wave's part of the steps
     const uint32_t part = (all + WK - 1) / WK;
     const uint32_t first = (uint32_t)wk * part;
@@ -390,7 +395,7 @@ struct Product {
     const char* const second_a = p.a[1] + (la.base[0] - p.a[0]);
     const char* const second_b = p.b[1] + (lb.base[0] - p.b[0]);
     // Step t's segment, and its first k there.
-    auto in_second = [&](uint32_t t) { return nseg > 1 && first + t >= per; };
+    auto in_second = [&](uint32_t t) { return p.nseg > 1 && first + t >= per; };
     auto k_of = [&](uint32_t t) { return (in_second(t) ? first + t - per : first + t) * BK; };
     v4u fa[2][TM], fb[2][TN];
     auto start = [&](uint32_t t, lds_char* dst) {
@@ -561,7 +566,8 @@ __device__ __forceinline__ Floats<V> load_floats(const char* row, uint64_t col, 
 // Find this workgroup's problem and tile.  Returns the problem's index.
 template <class P>
 __device__ __forceinline__ int locate(const ProductArgs& a, uint32_t* row0, uint32_t* col0) {
-  const uint32_t t = tile_of_block(blockIdx.x, a.tiles);
+  const uint32_t b = blockIdx.x;
+  const uint32_t t = b < a.head ? tile_of_block(b, a.head) : a.head + tile_of_block(b - a.head, a.tiles - a.head);
   int q = 0;
   while (q + 1 < a.nprob && t >= a.p[q + 1].first) ++q;
   uint32_t tm, tn;
@@ -577,24 +583,31 @@ __device__ __forceinline__ int locate(const ProductArgs& a, uint32_t* row0, uint
 struct ProductPlan {
   ProductArgs a;
   uint64_t tiles = 0;
+  // Problems before this one go first, spread over the XCDs by themselves:
+  // where two sorts of tiles differ in length, the long ones start and the
+  // short ones fill the end of the launch.
+  int head = 0;
 
-  ProductPlan() { memset(&a, 0, sizeof(a)); a.nseg = 1; }
+  ProductPlan() { memset(&a, 0, sizeof(a)); }
 
   // Rows of both operands start on 16-byte boundaries (Packer).
   Problem* add(uint64_t m, uint64_t n, uint64_t k, uint64_t lda, uint64_t ldb, uint64_t ldc) {
     Problem* p = &a.p[a.nprob++];
     p->m = (uint32_t)m, p->n = (uint32_t)n, p->k = (uint32_t)k;
     p->lda = (uint32_t)lda, p->ldb = (uint32_t)ldb, p->ldc = (uint32_t)ldc;
+    p->nseg = 1;
     return p;
   }
   // Tiles of every problem for a kernel whose tile covers bm x cols of C.
   bool cut(uint32_t bm, uint32_t cols) {
     tiles = 0;
+    a.head = 0;
     for (int i = 0; i < a.nprob; ++i) {
       Problem& p = a.p[i];
       p.tiles_m = (uint32_t)(((uint64_t)p.m + bm - 1) / bm);
       p.tiles_n = (uint32_t)(((uint64_t)p.n + cols - 1) / cols);
       p.first = (uint32_t)tiles;
+      if (i == head) a.head = (uint32_t)tiles;
       tiles += (uint64_t)p.tiles_m * p.tiles_n;
     }
     a.tiles = (uint32_t)tiles;

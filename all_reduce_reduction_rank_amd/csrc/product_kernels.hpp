@@ -50,6 +50,26 @@ __device__ __forceinline__ float exp_of(float z) {
 
 struct Nothing {};
 
+// c[0] = the finished tile, rounded once.
+template <class P>
+__device__ __forceinline__ void store_result(P& x, const Problem& p, uint32_t row0, uint32_t col0, char* smem) {
+  constexpr int ES = KElem<P::DT>::ES, V = KElem<P::DT>::E;
+  const bool vec = p.ldc % V == 0;
+  x.template hand_out<V, 2>(
+      smem, [](uint32_t, uint32_t) { return Nothing(); },
+      [&](uint32_t r, uint32_t col, float* v, float*, Nothing) {
+        const uint64_t row = (uint64_t)row0 + r;
+        if (row < p.m) store_row<P::DT, V>(p.c[0] + row * p.ldc * ES, (uint64_t)col0 + col, p.n, vec, v);
+      });
+}
+
+template <class P>
+__device__ __forceinline__ void store_tile(const Problem& p, uint32_t row0, uint32_t col0, char* smem) {
+  P x;
+  x.run(p, row0, col0, smem);
+  store_result(x, p, row0, col0, smem);
+}
+
 // ACT: the gate's activation (gated kinds).
 template <class P, int KIND, uint32_t ACT>
 __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
@@ -59,21 +79,27 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
   constexpr int V = KElem<DT>::E;  // values per 16-byte vector of the payload
   uint32_t row0, col0;
   const Problem& p = a.p[locate<P>(a, &row0, &col0)];
+  if constexpr (KIND == PK_GRADS) {
+    if (p.mode & GRAD_TN) {
+      store_tile<typename P::TN_>(p, row0, col0, smem);
+      return;
+    }
+  }
   P x;
-  x.run(p, a.nseg, row0, col0, smem);
+  x.run(p, row0, col0, smem);
   const uint32_t m = p.m, n = p.n;
   const uint64_t ldc = p.ldc;
   const bool vec = p.ldc % V == 0;
   auto nothing = [](uint32_t, uint32_t) { return Nothing(); };
 
-  if constexpr (KIND == PK_STORE_NT || KIND == PK_STORE_NN || KIND == PK_STORE_TN) {
-    char* c = p.c[0];
-    x.template hand_out<V, 2>(smem, nothing, [&](uint32_t r, uint32_t col, float* v, float*, Nothing) {
-      const uint64_t row = (uint64_t)row0 + r;
-      if (row < m) store_row<DT, V>(c + row * ldc * ES, (uint64_t)col0 + col, n, vec, v);
-    });
-  } else if constexpr (KIND == PK_ACCUM_NN) {
-    const bool add = p.mode & ACC_ADD, last = p.mode & ACC_LAST;
+  if constexpr (KIND == PK_STORE_NT) {
+    store_result(x, p, row0, col0, smem);
+  } else if constexpr (KIND == PK_GRADS) {
+    const bool add = p.mode & GRAD_ADD, partial = p.mode & GRAD_PARTIAL;
+    if (!add && !partial) {
+      store_result(x, p, row0, col0, smem);
+      return;
+    }
     const bool fvec = p.ldc % 4 == 0;
     x.template hand_out<V, 4>(
         smem,
@@ -88,8 +114,8 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
           if (row >= m) return;
 #pragma unroll
           for (int e = 0; e < V; ++e) v[e] = add ? o.v[e] + v[e] : v[e];
-          if (last) store_row<DT, V>(p.c[0] + row * ldc * ES, (uint64_t)col0 + col, n, vec, v);
-          else store_row<DT_F32, V>(p.c[1] + row * ldc * 4, (uint64_t)col0 + col, n, fvec, v);
+          if (partial) store_row<DT_F32, V>(p.c[1] + row * ldc * 4, (uint64_t)col0 + col, n, fvec, v);
+          else store_row<DT, V>(p.c[0] + row * ldc * ES, (uint64_t)col0 + col, n, vec, v);
         });
   } else if constexpr (KIND == PK_GATED) {
     // h's storage has rows of whole chunks (ldc), of which the last columns
@@ -116,8 +142,8 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
           const uint64_t row = (uint64_t)row0 + r;
           Pre q = {};
           if (row < m) {
-            q.g = load_floats<V>(p.e[0] + row * (uint64_t)n * 4, (uint64_t)col0 + col, n, n % 4 == 0);
-            q.u = load_floats<V>(p.e[1] + row * (uint64_t)n * 4, (uint64_t)col0 + col, n, n % 4 == 0);
+            q.g = load_floats<V>(p.a[1] + row * (uint64_t)n * 4, (uint64_t)col0 + col, n, n % 4 == 0);
+            q.u = load_floats<V>(p.b[1] + row * (uint64_t)n * 4, (uint64_t)col0 + col, n, n % 4 == 0);
           }
           return q;
         },
@@ -151,7 +177,7 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
             const int64_t t = a.target[row];
             q.live = t >= 0 && (uint64_t)t < a.vocab;
             q.at = t - (int64_t)p.col0;
-            q.z = ((const float*)p.e[0])[row];
+            q.z = ((const float*)p.a[1])[row];
             q.g = a.grad[row];
           }
           return q;
@@ -247,12 +273,11 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
   }
 }
 
-constexpr int layout_a(int kind) { return kind == PK_STORE_TN ? L_R : L_K; }
-constexpr int layout_b(int kind) { return kind >= PK_STORE_NN ? L_R : L_K; }
+constexpr int layout_b(int kind) { return kind >= PK_GATED_BWD ? L_R : L_K; }
 
 template <int KIND, int DT, class TILE, uint32_t ACT>
 hipError_t launch(ProductPlan& plan, hipStream_t stream) {
-  using P = Product<DT, layout_a(KIND), layout_b(KIND), KIND == PK_GATED, TILE>;
+  using P = Product<DT, L_K, layout_b(KIND), KIND == PK_GATED, TILE>;
   if (!plan.cut(P::BM, P::COLS)) return hipErrorInvalidValue;
   if (plan.tiles == 0) return hipSuccess;
   hipLaunchKernelGGL((product_kernel<P, KIND, ACT>), dim3((unsigned)plan.tiles), dim3(P::NT), 0, stream, plan.a);
@@ -290,10 +315,8 @@ hipError_t launch_typed(int kind, ProductPlan& plan, int device, hipStream_t str
     case PK_STORE_NT: return launch_kind<PK_STORE_NT, DT>(plan, device, stream);
     case PK_STATS: return launch_kind<PK_STATS, DT>(plan, device, stream);
     case PK_DLOGITS: return launch_kind<PK_DLOGITS, DT>(plan, device, stream);
-    case PK_STORE_NN: return launch_kind<PK_STORE_NN, DT>(plan, device, stream);
     case PK_GATED_BWD: return launch_gated<PK_GATED_BWD, DT>(plan, device, stream);
-    case PK_ACCUM_NN: return launch_kind<PK_ACCUM_NN, DT>(plan, device, stream);
-    case PK_STORE_TN: return launch_kind<PK_STORE_TN, DT>(plan, device, stream);
+    case PK_GRADS: return launch_kind<PK_GRADS, DT>(plan, device, stream);
   }
   return hipErrorInvalidValue;
 }

@@ -119,15 +119,17 @@ int product_tile(int kind, int dtype, const ProductPlan& plan, int device) {
     if (c == TILE_LARGE && dtype != DT_BF16) continue;
     if (c == TILE_THIN && max_m > (uint32_t)Thin::BM) continue;
     const ClassCost& k = COST[c];
-    double tiles = 0, work = 0, longest = 0;  // work: steps of all tiles
+    double tiles = 0, work = 0, longest = 0, shortest = 1e30;  // work: steps of all tiles
     for (int i = 0; i < plan.a.nprob; ++i) {
       const Problem& p = plan.a.p[i];
       const double t = (double)((p.m + k.bm - 1) / k.bm) * (double)(((uint64_t)p.n * half + k.bn - 1) / k.bn);
-      const uint64_t steps = (uint64_t)plan.a.nseg * ((p.k + per_step - 1) / per_step);
+      if (t == 0) continue;
+      const uint64_t steps = (uint64_t)p.nseg * ((p.k + per_step - 1) / per_step);
       const double s = (double)((steps + k.parts - 1) / k.parts);
       tiles += t;
       work += t * s;
-      if (t > 0 && s > longest) longest = s;
+      longest = s > longest ? s : longest;
+      shortest = s < shortest ? s : shortest;
     }
     if (tiles == 0) continue;
     double alone = k.alone, full = k.full;
@@ -139,8 +141,11 @@ int product_tile(int kind, int dtype, const ProductPlan& plan, int device) {
     const double slots = cus * k.resident;
     const double rounds = (double)(uint64_t)(tiles / slots);
     const double rest = tiles - rounds * slots;
-    double us = rounds * (k.fixed + work / tiles * full);
-    if (rest > 0) us += k.fixed + longest * (rest <= cus ? alone : full);
+    double us;
+    if (rounds == 0) us = k.fixed + longest * (rest <= cus ? alone : full);
+    else if (longest == shortest) us = rounds * (k.fixed + longest * full) +
+                                       (rest == 0 ? 0 : k.fixed + longest * (rest <= cus ? alone : full));
+    else us = tiles / slots * k.fixed + (work / slots + 0.5 * shortest) * full;  // long tiles first
     if (us < best_us) {
       best_us = us;
       best = c;

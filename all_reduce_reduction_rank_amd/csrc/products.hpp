@@ -13,17 +13,20 @@ enum ProductKind : int {
   PK_GATED = 0,    // paired; c = {act(g) u, g, u} (c[1], c[2] may be null)
   PK_STORE_NT,     // c[0] = C
   PK_STATS,        // per row: c[0] = (max, sum of exponentials) of the tile, c[1] = target's logit
-  PK_DLOGITS,      // c[0] = (exp(C - lse) - onehot(target)) * grad
+  PK_DLOGITS,      // a[1] = lse; c[0] = (exp(C - lse) - onehot(target)) * grad
   // A, B: L_K, L_R (dy W)
-  PK_STORE_NN,     // c[0] = C (two K segments when nseg is 2)
-  PK_GATED_BWD,    // C = dh, e = {g, u}; c = {dg, du, h}
-  PK_ACCUM_NN,     // C added up over launches in fp32 (Problem::mode, ACC_*)
-  // A, B: L_R, L_R (dy^T x)
-  PK_STORE_TN,
+  PK_GATED_BWD,    // C = dh, a[1], b[1] = g, u; c = {dg, du, h}
+  // Both products that end a backward pass, in one launch: problems by layout
+  // (Problem::mode GRAD_*)
+  PK_GRADS,
 };
 
-// Problem::mode of PK_ACCUM_NN
-enum : uint32_t { ACC_ADD = 1 /* add the fp32 sum so far (c[1]) */, ACC_LAST = 2 /* write c[0], else c[1] */ };
+// Problem::mode of PK_GRADS
+enum : uint32_t {
+  GRAD_TN = 1,       // A, B: L_R, L_R (dy^T x): c[0] = C; otherwise L_K, L_R (dy W):
+  GRAD_ADD = 2,      // add the fp32 sum so far (c[1])
+  GRAD_PARTIAL = 4,  // write the fp32 sum (c[1]) instead of the result (c[0])
+};
 // ProductArgs::act
 enum : uint32_t { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
 

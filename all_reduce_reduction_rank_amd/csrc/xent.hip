@@ -248,12 +248,12 @@ ar_status ar_linear_cross_entropy_backward(int nranks, const float* grad_loss, c
   }
   if (pack.launch((hipStream_t)stream) != hipSuccess) return AR_ERR_HIP;
   for (uint64_t i = 0; i < pieces; ++i) {
-    ProductPlan d_plan, dx_plan, dw_plan;
+    const uint64_t first = i * sp.piece;
+    ProductPlan d_plan, grads;
     d_plan.a.target = target;
     d_plan.a.grad = grad_loss;
     d_plan.a.vocab = s.vocab;
     for (int r = 0; r < nranks; ++r) {
-      const uint64_t first = i * sp.piece;
       // a rank without vocabulary still writes dx: a product with k = 0
       if (first >= umax(s.shard[r], 1)) continue;
       const uint64_t len = umin(sp.piece, s.shard[r] - first);
@@ -265,23 +265,28 @@ ar_status ar_linear_cross_entropy_backward(int nranks, const float* grad_loss, c
         p->a[0] = px[r].p;
         p->b[0] = wp;
         p->c[0] = d;
-        p->e[0] = (const char*)lse[r];
+        p->a[1] = (const char*)lse[r];
         p->col0 = s.start[r] + first;
-        p = dw_plan.add(len, s.hidden, s.rows, sp.piece, px[r].ld, s.hidden);
-        p->a[0] = d;
-        p->b[0] = px[r].p;
-        p->c[0] = (char*)dw[r] + first * s.hidden * s.es;
       }
-      p = dx_plan.add(s.rows, s.hidden, len, sp.piece, pw[r].ld, s.hidden);
+      p = grads.add(s.rows, s.hidden, len, sp.piece, pw[r].ld, s.hidden);
       p->a[0] = d;
       p->b[0] = wp;
       p->c[0] = (char*)dx[r];
       p->c[1] = sp.acc_bytes ? ws + (uint64_t)nranks * sp.d_bytes + (uint64_t)r * sp.acc_bytes : (char*)dx[r];
-      p->mode = (i ? ACC_ADD : 0) | (first + len >= s.shard[r] ? ACC_LAST : 0);
+      p->mode = (i ? GRAD_ADD : 0) | (first + len < s.shard[r] ? GRAD_PARTIAL : 0);
+    }
+    grads.head = grads.a.nprob;
+    for (int r = 0; r < nranks; ++r) {
+      if (first >= s.shard[r]) continue;
+      const uint64_t len = umin(sp.piece, s.shard[r] - first);
+      Problem* p = grads.add(len, s.hidden, s.rows, sp.piece, px[r].ld, s.hidden);
+      p->a[0] = ws + (uint64_t)r * sp.d_bytes;
+      p->b[0] = px[r].p;
+      p->c[0] = (char*)dw[r] + first * s.hidden * s.es;
+      p->mode = GRAD_TN;
     }
     if (launch_products(PK_DLOGITS, (int)dtype, d_plan, dev, (hipStream_t)stream) != hipSuccess ||
-        launch_products(PK_ACCUM_NN, (int)dtype, dx_plan, dev, (hipStream_t)stream) != hipSuccess ||
-        launch_products(PK_STORE_TN, (int)dtype, dw_plan, dev, (hipStream_t)stream) != hipSuccess)
+        launch_products(PK_GRADS, (int)dtype, grads, dev, (hipStream_t)stream) != hipSuccess)
       return AR_ERR_HIP;
   }
   return AR_OK;
