@@ -16,7 +16,8 @@
 //
 // Roundings to bf16 beside the stored results: h, dg and du, operands of the
 // matrix cores; half a bf16 step of the value each, so that one rounding lies
-// between the exact value and a product.  g and u are kept for the backward
+// between the exact value and a product (none with up to 64 rows, where a
+// second term holds what the first one's rounding left, fold_of).  g and u are kept for the backward
 // pass in fp32: kept in bf16 they would put two more under every gradient
 // (measured against fp64: 0.0035 relative instead of 0.0024, where the
 // rounding of the result alone is 0.0017).  Every sum is fp32.
@@ -34,6 +35,7 @@ namespace {
 
 struct FfnShape {
   uint64_t rows, hidden, inter, es, pitch;  // pitch: elements per row of h, dg, du (whole chunks)
+  uint32_t fold;                            // h, dg, du: rows down to their second terms, 0: none
   uint64_t mid_bytes;                       // one rank's h (dg, du)
   // one rank's copies of x (dout), of w_gate (w_up), of w_down, where their
   // rows are not whole 16-byte chunks
@@ -48,7 +50,8 @@ FfnShape shape_of(size_t rows, size_t hidden, size_t inter, int dtype) {
   s.rows = rows, s.hidden = hidden, s.inter = inter;
   s.es = dtype == DT_BF16 ? 2 : 4;
   s.pitch = Packer::pitch(inter, s.es);
-  s.mid_bytes = layer_align(s.rows * s.pitch * s.es);
+  s.fold = fold_of(rows, dtype);
+  s.mid_bytes = layer_align((s.fold + s.rows) * s.pitch * s.es);
   s.pack_x = Packer::bytes(rows, hidden, s.es);
   s.pack_up = Packer::bytes(inter, hidden, s.es);
   s.pack_down = Packer::bytes(hidden, inter, s.es);
@@ -111,10 +114,12 @@ ar_status ar_gated_ffn(int nranks, const void* const* x, const void* const* w_ga
     p->a[0] = px.p;
     p->b[0] = pg.p;
     p->b[1] = pu.p;
+    p->fold = s.fold;
     p->c[0] = h(r);
     p->c[1] = gate ? (char*)gate[r] : nullptr;
     p->c[2] = up ? (char*)up[r] : nullptr;
-    p = down_plan.add(s.rows, s.hidden, s.inter, s.pitch, pd.ld, s.hidden);
+    p = down_plan.add(s.fold + s.rows, s.hidden, s.inter, s.pitch, pd.ld, s.hidden);
+    p->fold = s.fold;
     p->a[0] = h(r);
     p->b[0] = pd.p;
     p->c[0] = (char*)out[r];
@@ -159,7 +164,6 @@ ar_status ar_gated_ffn_backward(int nranks, const void* const* dout, const void*
   char* ws = (char*)workspace;
   auto mid = [&](int r, int i) { return ws + ((uint64_t)r * 3 + i) * s.mid_bytes; };  // dg, du, h
 
-  // With no rows every weight gradient is a product with k = 0: zeros.
   ProductPlan mid_plan, grads;
   mid_plan.a.act = (int32_t)act;
   Packer pack(ws + (uint64_t)nranks * 3 * s.mid_bytes, s.es);
@@ -178,7 +182,9 @@ ar_status ar_gated_ffn_backward(int nranks, const void* const* dout, const void*
     p->a[1] = (const char*)gate[r];
     p->b[1] = (const char*)up[r];
     for (int i = 0; i < 3; ++i) p->c[i] = mid(r, i);
-    p = grads.add(s.rows, s.hidden, s.inter, s.pitch, pg.ld, s.hidden);
+    p->fold = s.fold;
+    p = grads.add(s.fold + s.rows, s.hidden, s.inter, s.pitch, pg.ld, s.hidden);
+    p->fold = s.fold;
     p->nseg = 2;
     p->a[0] = mid(r, 0);
     p->a[1] = mid(r, 1);
@@ -187,25 +193,31 @@ ar_status ar_gated_ffn_backward(int nranks, const void* const* dout, const void*
     p->c[0] = (char*)dx[r];
   }
   grads.head = nranks;
-  // With no rows every weight gradient is a product with k = 0: zeros.
+  // With no rows every weight gradient is a product with k = 0: zeros.  The
+  // second terms of dg, du and h, where there are any, are a second segment.
+  const uint64_t low = s.fold * s.pitch * s.es;
   for (int r = 0; r < nranks; ++r) {
     Problem* p;
     for (int i = 0; i < 2; ++i) {
       p = grads.add(s.inter, s.hidden, s.rows, s.pitch, px[r].ld, s.hidden);
+      p->nseg = s.fold ? 2 : 1;
       p->a[0] = mid(r, i);
-      p->b[0] = px[r].p;
+      p->a[1] = mid(r, i) + low;
+      p->b[0] = p->b[1] = px[r].p;
       p->c[0] = (char*)(i ? dw_up[r] : dw_gate[r]);
       p->mode = GRAD_TN;
     }
     p = grads.add(s.hidden, s.inter, s.rows, po[r].ld, s.pitch, s.inter);
-    p->a[0] = po[r].p;
+    p->nseg = s.fold ? 2 : 1;
+    p->a[0] = p->a[1] = po[r].p;
     p->b[0] = mid(r, 2);
+    p->b[1] = mid(r, 2) + low;
     p->c[0] = (char*)dw_down[r];
     p->mode = GRAD_TN;
   }
   if (pack.launch((hipStream_t)stream) != hipSuccess ||
       launch_products(PK_GATED_BWD, (int)dtype, mid_plan, dev, (hipStream_t)stream) != hipSuccess ||
-      launch_products(PK_GRADS, (int)dtype, grads, dev, (hipStream_t)stream) != hipSuccess)
+      launch_grads((int)dtype, grads, dev, (hipStream_t)stream) != hipSuccess)
     return AR_ERR_HIP;
   return AR_OK;
 }

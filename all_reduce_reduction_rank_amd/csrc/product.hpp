@@ -79,6 +79,11 @@ struct Problem {
   uint32_t lda, ldb, ldc;  // elements between rows of storage
   uint32_t tiles_m, tiles_n, first;
   uint32_t nseg;  // K segments
+  // Rows in two bf16 terms, value + what its rounding left (kept so where there
+  // are few of them): the products that write such a matrix put the second
+  // terms `fold` rows below the first; those that read it as A have both in
+  // one tile of 2 fold rows and add row r + fold to row r of the result.
+  uint32_t fold;
   uint32_t mode;  // what the epilogue (and PK_GRADS' layout) goes by
 };
 
@@ -87,6 +92,7 @@ struct ProductArgs {  // a kernel's arguments: at most 4 KB
   const int64_t* target;  // cross entropy: per row
   const float* grad;      // cross entropy: per row
   uint64_t vocab;         // cross entropy: targets outside [0, vocab) are ignored
+  const float* scale;     // cross entropy: one value; d is stored over it, dx and dw times it (null: 1)
   int32_t nprob;
   int32_t act;     // gated kinds
   uint32_t tiles;  // of all problems
@@ -446,8 +452,9 @@ struct Product {
   // product) and pre's result.  Rows and columns count from the tile's corner.
   // 16-byte chunk c of a row sits at chunk c ^ (row & 15): the 16 rows of a
   // write and the neighbouring chunks of a read fall on different banks.
+  // fold: row r + fold is added to row r (tiles of one phase; Problem::fold).
   template <int V, int U, class PRE, class F>
-  __device__ __forceinline__ void hand_out(char* smem, PRE&& pre, F&& f) {
+  __device__ __forceinline__ void hand_out(char* smem, uint32_t fold, PRE&& pre, F&& f) {
     constexpr int PHASES = (BM * BN * 4 * WK + LDS_BYTES - 1) / LDS_BYTES;
     constexpr int PART = TM / PHASES;  // blocks of a wave per phase
     constexpr int ROWS = PART * 16 * WM, UNITS = ROWS * (COLS / V), ROUNDS = (UNITS + NT * U - 1) / (NT * U);
@@ -497,6 +504,15 @@ struct Product {
               const float4 y = t[(z * ROWS + at[u]) * (BN / 4) + (chunk ^ s)];
               a.x += y.x, a.y += y.y, a.z += y.z, a.w += y.w;
             }
+            if (PHASES == 1 && !PAIR && fold) {
+              const uint32_t r = (at[u] + fold) % ROWS;  // (rows from fold on are not wanted)
+#pragma unroll
+              for (int z = 0; z < WK; ++z) {
+                const float4 y = t[(z * ROWS + r) * (BN / 4) + (chunk ^ (r & SWZ))];
+                b.x += y.x, b.y += y.y, b.z += y.z, b.w += y.w;
+              }
+              a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+            }
             v[4 * q] = a.x, v[4 * q + 1] = a.y, v[4 * q + 2] = a.z, v[4 * q + 3] = a.w;
             if constexpr (PAIR) {
 #pragma unroll
@@ -538,6 +554,21 @@ __device__ __forceinline__ void store_row(char* row, uint64_t col, uint32_t n, b
       if constexpr (DT == DT_BF16) *(uint16_t*)(p + e * 2) = (uint16_t)bf16_round(v[e]);
       else *(float*)(p + e * 4) = v[e];
     }
+  }
+}
+
+// The same in two terms: v rounded at `row`, the rest at `low` (if there is one).
+template <int DT, int V>
+__device__ __forceinline__ void store_terms(char* row, char* low, uint64_t col, uint32_t n, bool vec, const float* v) {
+  store_row<DT, V>(row, col, n, vec, v);
+  if (DT == DT_BF16 && low) {
+    float rest[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float top = __uint_as_float(bf16_round(v[e]) << 16);
+      rest[e] = fabsf(top) < INFINITY ? v[e] - top : 0.f;  // nothing to add to an infinity or a NaN
+    }
+    store_row<DT, V>(low, col, n, vec, rest);
   }
 }
 

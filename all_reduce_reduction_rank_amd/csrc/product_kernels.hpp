@@ -50,24 +50,28 @@ __device__ __forceinline__ float exp_of(float z) {
 
 struct Nothing {};
 
-// c[0] = the finished tile, rounded once.
+// c[0] = the finished tile times `scale`, rounded once.
 template <class P>
-__device__ __forceinline__ void store_result(P& x, const Problem& p, uint32_t row0, uint32_t col0, char* smem) {
+__device__ __forceinline__ void store_result(P& x, const Problem& p, float scale, uint32_t row0, uint32_t col0,
+                                             char* smem) {
   constexpr int ES = KElem<P::DT>::ES, V = KElem<P::DT>::E;
   const bool vec = p.ldc % V == 0;
+  const uint32_t m = p.m - p.fold;
   x.template hand_out<V, 2>(
-      smem, [](uint32_t, uint32_t) { return Nothing(); },
+      smem, p.fold, [](uint32_t, uint32_t) { return Nothing(); },
       [&](uint32_t r, uint32_t col, float* v, float*, Nothing) {
         const uint64_t row = (uint64_t)row0 + r;
-        if (row < p.m) store_row<P::DT, V>(p.c[0] + row * p.ldc * ES, (uint64_t)col0 + col, p.n, vec, v);
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] *= scale;
+        if (row < m) store_row<P::DT, V>(p.c[0] + row * p.ldc * ES, (uint64_t)col0 + col, p.n, vec, v);
       });
 }
 
 template <class P>
-__device__ __forceinline__ void store_tile(const Problem& p, uint32_t row0, uint32_t col0, char* smem) {
+__device__ __forceinline__ void store_tile(const Problem& p, float scale, uint32_t row0, uint32_t col0, char* smem) {
   P x;
   x.run(p, row0, col0, smem);
-  store_result(x, p, row0, col0, smem);
+  store_result(x, p, scale, row0, col0, smem);
 }
 
 // ACT: the gate's activation (gated kinds).
@@ -77,11 +81,12 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
   constexpr int DT = P::DT;
   constexpr int ES = KElem<DT>::ES;
   constexpr int V = KElem<DT>::E;  // values per 16-byte vector of the payload
+  constexpr bool FOLDS = P::BM < Large::BM;  // may write second terms (product_tile keeps them from the large tile)
   uint32_t row0, col0;
   const Problem& p = a.p[locate<P>(a, &row0, &col0)];
   if constexpr (KIND == PK_GRADS) {
     if (p.mode & GRAD_TN) {
-      store_tile<typename P::TN_>(p, row0, col0, smem);
+      store_tile<typename P::TN_>(p, a.scale ? *a.scale : 1.0f, row0, col0, smem);
       return;
     }
   }
@@ -93,40 +98,44 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
   auto nothing = [](uint32_t, uint32_t) { return Nothing(); };
 
   if constexpr (KIND == PK_STORE_NT) {
-    store_result(x, p, row0, col0, smem);
+    store_result(x, p, 1.0f, row0, col0, smem);
   } else if constexpr (KIND == PK_GRADS) {
     const bool add = p.mode & GRAD_ADD, partial = p.mode & GRAD_PARTIAL;
+    const float scale = a.scale ? *a.scale : 1.0f;
     if (!add && !partial) {
-      store_result(x, p, row0, col0, smem);
+      store_result(x, p, scale, row0, col0, smem);
       return;
     }
+    const uint32_t rows = m - p.fold;
     const bool fvec = p.ldc % 4 == 0;
     x.template hand_out<V, 4>(
-        smem,
+        smem, p.fold,
         [&](uint32_t r, uint32_t col) {
           const uint64_t row = (uint64_t)row0 + r;
           Floats<V> o = {};
-          if (add && row < m) o = load_floats<V>(p.c[1] + row * ldc * 4, (uint64_t)col0 + col, n, fvec);
+          if (add && row < rows) o = load_floats<V>(p.c[1] + row * ldc * 4, (uint64_t)col0 + col, n, fvec);
           return o;
         },
         [&](uint32_t r, uint32_t col, float* v, float*, const Floats<V>& o) {
           const uint64_t row = (uint64_t)row0 + r;
-          if (row >= m) return;
+          if (row >= rows) return;
+          // (the sum so far is scaled already)
 #pragma unroll
-          for (int e = 0; e < V; ++e) v[e] = add ? o.v[e] + v[e] : v[e];
+          for (int e = 0; e < V; ++e) v[e] = add ? o.v[e] + v[e] * scale : v[e] * scale;
           if (partial) store_row<DT_F32, V>(p.c[1] + row * ldc * 4, (uint64_t)col0 + col, n, fvec, v);
           else store_row<DT, V>(p.c[0] + row * ldc * ES, (uint64_t)col0 + col, n, vec, v);
         });
   } else if constexpr (KIND == PK_GATED) {
     // h's storage has rows of whole chunks (ldc), of which the last columns
     // come out as zeros (their g and u are); g and u are n wide, fp32.
-    x.template hand_out<V, 2>(smem, nothing, [&](uint32_t r, uint32_t col, float* g, float* u, Nothing) {
+    x.template hand_out<V, 2>(smem, 0, nothing, [&](uint32_t r, uint32_t col, float* g, float* u, Nothing) {
       const uint64_t row = (uint64_t)row0 + r;
       if (row >= m) return;
       float h[V];
 #pragma unroll
       for (int e = 0; e < V; ++e) h[e] = activate<ACT, false>(g[e]).v * u[e];
-      store_row<DT, V>(p.c[0] + row * ldc * ES, (uint64_t)col0 + col, p.ldc, vec, h);
+      char* to = p.c[0] + row * ldc * ES;
+      store_terms<DT, V>(to, FOLDS && p.fold ? to + p.fold * ldc * ES : nullptr, (uint64_t)col0 + col, p.ldc, vec, h);
       if (p.c[1]) {
         store_row<DT_F32, V>(p.c[1] + row * (uint64_t)n * 4, (uint64_t)col0 + col, n, n % 4 == 0, g);
         store_row<DT_F32, V>(p.c[2] + row * (uint64_t)n * 4, (uint64_t)col0 + col, n, n % 4 == 0, u);
@@ -137,7 +146,7 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
       Floats<V> g, u;
     };
     x.template hand_out<V, 4>(
-        smem,
+        smem, 0,
         [&](uint32_t r, uint32_t col) {
           const uint64_t row = (uint64_t)row0 + r;
           Pre q = {};
@@ -158,9 +167,11 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
             du[e] = dh[e] * f.v;
             h[e] = f.v * q.u.v[e];
           }
-          store_row<DT, V>(p.c[0] + row * ldc * ES, (uint64_t)col0 + col, p.ldc, vec, dg);
-          store_row<DT, V>(p.c[1] + row * ldc * ES, (uint64_t)col0 + col, p.ldc, vec, du);
-          store_row<DT, V>(p.c[2] + row * ldc * ES, (uint64_t)col0 + col, p.ldc, vec, h);
+          const uint64_t to = row * ldc * ES, low = to + p.fold * ldc * ES;
+          const bool two = FOLDS && p.fold != 0;
+          store_terms<DT, V>(p.c[0] + to, two ? p.c[0] + low : nullptr, (uint64_t)col0 + col, p.ldc, vec, dg);
+          store_terms<DT, V>(p.c[1] + to, two ? p.c[1] + low : nullptr, (uint64_t)col0 + col, p.ldc, vec, du);
+          store_terms<DT, V>(p.c[2] + to, two ? p.c[2] + low : nullptr, (uint64_t)col0 + col, p.ldc, vec, h);
         });
   } else if constexpr (KIND == PK_DLOGITS) {
     struct Row {
@@ -169,7 +180,7 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
       bool live;
     };
     x.template hand_out<V, 4>(
-        smem,
+        smem, 0,
         [&](uint32_t r, uint32_t) {
           const uint64_t row = (uint64_t)row0 + r;
           Row q = {-1, 0.f, 0.f, false};
@@ -178,7 +189,7 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
             q.live = t >= 0 && (uint64_t)t < a.vocab;
             q.at = t - (int64_t)p.col0;
             q.z = ((const float*)p.a[1])[row];
-            q.g = a.grad[row];
+            q.g = a.scale ? a.grad[row] / *a.scale : a.grad[row];
           }
           return q;
         },
@@ -191,12 +202,13 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
             const float d = (exp_of<DT>(v[e] - q.z) - ((int64_t)c == q.at ? 1.0f : 0.0f)) * q.g;
             v[e] = q.live && c < n ? d : 0.f;  // columns n .. ldc: zeros
           }
-          store_row<DT, V>(p.c[0] + row * ldc * ES, (uint64_t)col0 + col, p.ldc, vec, v);
+          char* to = p.c[0] + row * ldc * ES;
+          store_terms<DT, V>(to, FOLDS && p.fold ? to + p.fold * ldc * ES : nullptr, (uint64_t)col0 + col, p.ldc, vec, v);
         });
   } else if constexpr (P::WK > 1) {  // PK_STATS, K split over the waves
     float* at_target = (float*)p.c[1];
     x.template hand_out<V, 1>(
-        smem,
+        smem, 0,
         [&](uint32_t r, uint32_t) {
           const uint64_t row = (uint64_t)row0 + r;
           const int64_t t = row < m ? a.target[row] : -1;

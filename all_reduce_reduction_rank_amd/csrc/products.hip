@@ -111,14 +111,20 @@ int product_tile(int kind, int dtype, const ProductPlan& plan, int device) {
   const double cus = n_cu;
   const uint32_t half = kind == PK_GATED ? 2 : 1;
   const uint64_t per_step = dtype == DT_BF16 ? 64 : 32;  // k of 128 bytes
-  uint32_t max_m = 0;
-  for (int i = 0; i < plan.a.nprob; ++i) max_m = plan.a.p[i].m > max_m ? plan.a.p[i].m : max_m;
+  const bool reads_terms = kind == PK_STORE_NT || kind == PK_GRADS;  // other kinds write them
+  uint32_t max_m = 0, fold = 0;
+  for (int i = 0; i < plan.a.nprob; ++i) {
+    const Problem& p = plan.a.p[i];
+    max_m = p.m > max_m ? p.m : max_m;
+    fold = p.fold > fold ? p.fold : fold;  // the same in all of a launch's problems
+  }
   int best = TILE_SMALL;
   double best_us = 1e30;
   for (int c = 0; c < TILE_CLASSES; ++c) {
-    if (c == TILE_LARGE && dtype != DT_BF16) continue;
+    if (c == TILE_LARGE && (dtype != DT_BF16 || fold)) continue;
     if (c == TILE_THIN && max_m > (uint32_t)Thin::BM) continue;
     const ClassCost& k = COST[c];
+    if (fold && reads_terms && k.bm != 2 * fold) continue;
     double tiles = 0, work = 0, longest = 0, shortest = 1e30;  // work: steps of all tiles
     for (int i = 0; i < plan.a.nprob; ++i) {
       const Problem& p = plan.a.p[i];
@@ -152,6 +158,17 @@ int product_tile(int kind, int dtype, const ProductPlan& plan, int device) {
     }
   }
   return best;
+}
+
+hipError_t launch_grads(int dtype, ProductPlan& plan, int device, hipStream_t stream) {
+  if (plan.head == 0 || plan.a.p[0].fold == 0) return launch_products(PK_GRADS, dtype, plan, device, stream);
+  ProductPlan rest = plan;
+  rest.a.nprob = plan.a.nprob - plan.head;
+  rest.head = 0;
+  for (int i = 0; i < rest.a.nprob; ++i) rest.a.p[i] = plan.a.p[plan.head + i];
+  plan.a.nprob = plan.head;
+  const hipError_t e = launch_products(PK_GRADS, dtype, plan, device, stream);
+  return e != hipSuccess ? e : launch_products(PK_GRADS, dtype, rest, device, stream);
 }
 
 }  // namespace ar

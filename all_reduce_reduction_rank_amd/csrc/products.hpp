@@ -39,6 +39,17 @@ __device__ __forceinline__ float2 merge_stats(float2 x, float2 y) {
   return make_float2(top, x.y * expf(stats_shift(x.x) - shift) + y.y * expf(stats_shift(y.x) - shift));
 }
 
+// Rows below which a bf16 intermediate's second terms go (Problem::fold): half
+// the rows of the tile that will read it, or 0 where the intermediate keeps
+// one term.  With up to 64 rows the second terms cost next to nothing (they
+// fill rows of a tile that would be empty), and few roundings do not average
+// out: with one term, single results of one-token calls came out up to 1.55
+// times as far from the exact ones as the result's own rounding puts them.
+constexpr uint32_t fold_of(uint64_t rows, int dtype) {
+  return dtype != DT_BF16 || rows == 0 ? 0 : rows <= Thin::BM / 2 ? Thin::BM / 2 : rows <= Flat::BM / 2 ? Flat::BM / 2
+         : rows <= Small::BM / 2 ? Small::BM / 2 : 0;
+}
+
 // Tile class that a launch of this plan takes (its problems are final).
 enum TileClass : int { TILE_LARGE = 0, TILE_SMALL, TILE_FLAT, TILE_SPLIT, TILE_THIN, TILE_CLASSES };
 int product_tile(int kind, int dtype, const ProductPlan& plan, int device);
@@ -100,5 +111,9 @@ inline hipError_t launch_products(int kind, int dtype, ProductPlan& plan, int de
   return dtype == DT_BF16 ? launch_products_bf16(kind, plan, device, stream)
                           : launch_products_f32(kind, plan, device, stream);
 }
+
+// A PK_GRADS plan: dx problems first (`head` of them), then GRAD_TN.  One launch;
+// two where dx's operand has second terms, which fix dx's tile class.
+hipError_t launch_grads(int dtype, ProductPlan& plan, int device, hipStream_t stream);
 
 }  // namespace ar
