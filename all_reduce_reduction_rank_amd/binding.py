@@ -19,6 +19,7 @@ if that fails every call raises -- there is no CPU fallback.
 """
 
 import ctypes
+import math
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -406,8 +407,9 @@ def _layer_list(ts, n, shapes, dtype, device, what):
     if len(ts) != n:
         raise ValueError(f"{what} holds {len(ts)} rank buffers; the call needs {n}")
     ptrs = []
+    same = not isinstance(shapes, list)
     for i, t in enumerate(ts):
-        shape = shapes[i] if isinstance(shapes, list) else shapes
+        shape = shapes if same else shapes[i]
         if t.dtype is not dtype:
             raise TypeError(f"{what}[{i}] is {t.dtype}; the call needs {dtype}")
         if t.shape != shape:
@@ -428,8 +430,7 @@ def _layer_vector(t, rows, dtype, device, what):
 
 def _on_device(device):
     """The call's tensors must be device tensors on the current device."""
-    import torch
-
+    torch = _TORCH
     if device < 0:
         raise ValueError("rank buffers must be contiguous device tensors")
     if device != torch.cuda.current_device():
@@ -444,15 +445,22 @@ class _Scratch:
         self.stream, self.device = stream, device
 
     def empty(self, shape, dtype):
-        import torch
-
+        torch = _TORCH
         if self.stream is None:
             return torch.empty(shape, dtype=dtype, device=self.device)
         with torch.cuda.stream(self.stream):
             return torch.empty(shape, dtype=dtype, device=self.device)
 
+    def ranks(self, n, shape, dtype):
+        """N rank buffers of one shape: views of one allocation where each
+        starts on a 16-byte boundary (one allocation costs as much host time
+        as each of N would)."""
+        if n > 1 and (math.prod(shape) * dtype.itemsize) % 16 == 0:
+            return list(self.empty((n, *shape), dtype).unbind(0))
+        return [self.empty(shape, dtype) for _ in range(n)]
+
     def workspace(self, nbytes):
-        ws = self.empty((nbytes,), _torch().uint8)
+        ws = self.empty((nbytes,), _TORCH.uint8)
         return ws, ctypes.c_void_p(ws.data_ptr())
 
 
@@ -500,7 +508,7 @@ def gated_ffn(x, w_gate, w_up, w_down, out=None, gate=None, up=None, act="silu",
     _on_device(device)
     scratch = _Scratch(stream, device)
     if out is None:
-        out = [scratch.empty((rows, hidden), dtype) for _ in range(n)]
+        out = scratch.ranks(n, (rows, hidden), dtype)
         o = (ctypes.c_void_p * n)(*[t.data_ptr() for t in out])
     nbytes = _lib().ar_gated_ffn_workspace(n, rows, hidden, inter, DTYPES[dt], 0)
     ws, ws_ptr = scratch.workspace(nbytes)
@@ -531,7 +539,7 @@ def gated_ffn_backward(dout, x, w_gate, w_up, w_down, gate, up, dx=None, dw_gate
     outs = []
     for i, (_, t, shape) in enumerate(results):
         if t is None:
-            t = [scratch.empty(shape, dtype) for _ in range(n)]
+            t = scratch.ranks(n, shape, dtype)
             given[i] = (ctypes.c_void_p * n)(*[v.data_ptr() for v in t])
         outs.append(t)
     nbytes = _lib().ar_gated_ffn_workspace(n, rows, hidden, inter, DTYPES[dt], 1)
@@ -583,7 +591,7 @@ def linear_cross_entropy(x, w, target, loss=None, lse=None, stream=None):
     outs = []
     for i, t in enumerate((loss, lse)):
         if t is None:
-            t = [scratch.empty((rows,), torch.float32) for _ in range(n)]
+            t = scratch.ranks(n, (rows,), torch.float32)
             given[i] = (ctypes.c_void_p * n)(*[v.data_ptr() for v in t])
         outs.append(t)
     nbytes = _lib().ar_linear_cross_entropy_workspace(n, rows, hidden, vocab, DTYPES[dt], 0, 0)
@@ -614,7 +622,8 @@ def linear_cross_entropy_backward(grad_loss, x, w, target, lse, dx=None, dw=None
     outs = []
     for i, (_, t, shapes) in enumerate(results):
         if t is None:
-            t = [scratch.empty(shape, dtype) for shape in shapes]
+            same = shapes[0] == shapes[-1]  # (shards: all of one length, or not)
+            t = scratch.ranks(n, shapes[0], dtype) if same else [scratch.empty(shape, dtype) for shape in shapes]
             given[i] = (ctypes.c_void_p * n)(*[v.data_ptr() for v in t])
         outs.append(t)
     nbytes = _lib().ar_linear_cross_entropy_workspace(n, rows, hidden, vocab, DTYPES[dt], 1, piece)

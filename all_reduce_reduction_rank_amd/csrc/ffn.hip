@@ -16,7 +16,7 @@
 //
 // Roundings to bf16 beside the stored results: h, dg and du, operands of the
 // matrix cores; half a bf16 step of the value each, so that one rounding lies
-// between the exact value and a product (none with up to 64 rows, where a
+// between the exact value and a product (none with up to 32 rows, where a
 // second term holds what the first one's rounding left, fold_of).  g and u are kept for the backward
 // pass in fp32: kept in bf16 they would put two more under every gradient
 // (measured against fp64: 0.0035 relative instead of 0.0024, where the

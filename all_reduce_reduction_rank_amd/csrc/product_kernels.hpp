@@ -41,6 +41,13 @@ __device__ __forceinline__ Act activate(float z) {
   return r;
 }
 
+// A target's column of a problem (columns col0 .. col0 + n of the vocabulary),
+// or a value no column has.
+__device__ __forceinline__ uint32_t target_column(int64_t target, uint64_t vocab, uint64_t col0, uint32_t n) {
+  const uint64_t at = (uint64_t)target - col0;
+  return target >= 0 && (uint64_t)target < vocab && at < n ? (uint32_t)at : 0xffffffffu;
+}
+
 // exp for probabilities.  bf16 gradients round far above the hardware
 // exponential's error (about |z| 2^-24 relative); fp32 takes the exact one.
 template <int DT>
@@ -175,7 +182,7 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
         });
   } else if constexpr (KIND == PK_DLOGITS) {
     struct Row {
-      int64_t at;  // the target's column in this problem, if it lies there
+      uint32_t at;  // the target's column in this problem, if it lies there
       float z, g;
       bool live;
     };
@@ -183,11 +190,11 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
         smem, 0,
         [&](uint32_t r, uint32_t) {
           const uint64_t row = (uint64_t)row0 + r;
-          Row q = {-1, 0.f, 0.f, false};
+          Row q = {0xffffffffu, 0.f, 0.f, false};
           if (row < m) {
             const int64_t t = a.target[row];
             q.live = t >= 0 && (uint64_t)t < a.vocab;
-            q.at = t - (int64_t)p.col0;
+            q.at = target_column(t, a.vocab, p.col0, n);
             q.z = ((const float*)p.a[1])[row];
             q.g = a.scale ? a.grad[row] / *a.scale : a.grad[row];
           }
@@ -199,7 +206,7 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
 #pragma unroll
           for (int e = 0; e < V; ++e) {
             const uint32_t c = col0 + col + e;
-            const float d = (exp_of<DT>(v[e] - q.z) - ((int64_t)c == q.at ? 1.0f : 0.0f)) * q.g;
+            const float d = (exp_of<DT>(v[e] - q.z) - (c == q.at ? 1.0f : 0.0f)) * q.g;
             v[e] = q.live && c < n ? d : 0.f;  // columns n .. ldc: zeros
           }
           char* to = p.c[0] + row * ldc * ES;
@@ -211,10 +218,9 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
         smem, 0,
         [&](uint32_t r, uint32_t) {
           const uint64_t row = (uint64_t)row0 + r;
-          const int64_t t = row < m ? a.target[row] : -1;
-          return t >= 0 && (uint64_t)t < a.vocab ? t - (int64_t)p.col0 : (int64_t)-1;
+          return target_column(row < m ? a.target[row] : -1, a.vocab, p.col0, n);
         },
-        [&](uint32_t r, uint32_t col, float* v, float*, int64_t at) {
+        [&](uint32_t r, uint32_t col, float* v, float*, uint32_t at) {
           // the COLS / V threads of a row are neighbours in a wave
           const uint64_t row = (uint64_t)row0 + r;
           float top = -INFINITY, sum = 0.f;
@@ -222,7 +228,7 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
           for (int e = 0; e < V; ++e) {
             const uint32_t c = col0 + col + e;
             if (c < n) top = fmaxf(top, v[e]);
-            if (c < n && (int64_t)c == at && row < m) at_target[row] = v[e];
+            if (c == at && row < m) at_target[row] = v[e];
           }
 #pragma unroll
           for (int o = 1; o < P::COLS / V; o *= 2) top = fmaxf(top, __shfl_xor(top, o));
@@ -243,21 +249,21 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
     for (int i = 0; i < P::TM; ++i) {
       const uint32_t r = P::wave_row() + 16 * i + (lane & 15);
       const uint64_t row = (uint64_t)row0 + r;
-      const int64_t t = row < m ? a.target[row] : -1;
-      const int64_t at = t - (int64_t)p.col0;
-      const bool live = t >= 0 && (uint64_t)t < a.vocab;
-      float top = -INFINITY;
+      const uint32_t at = target_column(row < m ? a.target[row] : -1, a.vocab, p.col0, n);
+      float top = -INFINITY, value = 0.f;
+      bool hit = false;
 #pragma unroll
       for (int j = 0; j < P::TN; ++j) {
         const uint32_t col = col0 + P::wave_col() + 16 * j + 4 * (lane >> 4);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          if (col + e < n) {
-            top = fmaxf(top, x.acc[i][j][e]);
-            if (live && (int64_t)(col + e) == at) ((float*)p.c[1])[row] = x.acc[i][j][e];
-          }
+          const float v = x.acc[i][j][e];
+          top = col + e < n ? fmaxf(top, v) : top;
+          value = col + e == at ? v : value;
+          hit = hit || col + e == at;
         }
       }
+      if (hit) ((float*)p.c[1])[row] = value;
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
       const float shift = stats_shift(top);

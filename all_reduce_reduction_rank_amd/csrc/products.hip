@@ -4,7 +4,7 @@
 // A launch takes the tile class with the smallest estimated time.  A
 // workgroup of class c takes fixed + steps x (alone | full) us, a step being
 // 128 bytes of k (of each wave's part of K): `alone` while its CU runs no
-// other, `full` with as many as fit.  Measured on bf16 products of 8 ranks
+// other and no round of workgroups is behind it, `full` with as many as fit.  Measured on bf16 products of 8 ranks
 // [m, 5120] x [1728 pairs, 5120] (80 steps) and [m, 1728] x [5120, 1728] (27):
 //
 //   us            m = 64   128   256   512  1024 |   64   128   256   512  1024
@@ -35,7 +35,7 @@ constexpr ClassCost COST[TILE_CLASSES] = {
     {Large::BM, Large::BN, Large::WK, 1, 9.0, 1.75, 1.75},
     {Small::BM, Small::BN, Small::WK, 2, 4.0, 1.15, 1.35},
     {Flat::BM, Flat::BN, Flat::WK, 2, 4.0, 0.75, 0.95},
-    {Split::BM, Split::BN, Split::WK, 1, 4.5, 1.2, 1.2},
+    {Split::BM, Split::BN, Split::WK, 1, 4.5, 0.8, 1.6},
     {Thin::BM, Thin::BN, Thin::WK, 2, 4.5, 0.25, 0.6},
 };
 constexpr double F32_FLOPS_PER_CU_US = 0.55e6;  // of 0.61e6 (16x16x4 at 2.4 GHz)
@@ -150,7 +150,7 @@ int product_tile(int kind, int dtype, const ProductPlan& plan, int device) {
     double us;
     if (rounds == 0) us = k.fixed + longest * (rest <= cus ? alone : full);
     else if (longest == shortest) us = rounds * (k.fixed + longest * full) +
-                                       (rest == 0 ? 0 : k.fixed + longest * (rest <= cus ? alone : full));
+                                       (rest == 0 ? 0 : k.fixed + longest * (rest <= cus && k.resident > 1 ? alone : full));
     else us = tiles / slots * k.fixed + (work / slots + 0.5 * shortest) * full;  // long tiles first
     if (us < best_us) {
       best_us = us;

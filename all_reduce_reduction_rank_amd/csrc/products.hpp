@@ -39,15 +39,17 @@ __device__ __forceinline__ float2 merge_stats(float2 x, float2 y) {
   return make_float2(top, x.y * expf(stats_shift(x.x) - shift) + y.y * expf(stats_shift(y.x) - shift));
 }
 
-// Rows below which a bf16 intermediate's second terms go (Problem::fold): half
-// the rows of the tile that will read it, or 0 where the intermediate keeps
-// one term.  With up to 64 rows the second terms cost next to nothing (they
-// fill rows of a tile that would be empty), and few roundings do not average
-// out: with one term, single results of one-token calls came out up to 1.55
-// times as far from the exact ones as the result's own rounding puts them.
+// Rows down to a bf16 intermediate's second terms (Problem::fold): half the rows
+// of the tile that will read it, or 0 where the intermediate keeps one term.
+// With up to 32 rows the second terms cost next to nothing (they fill rows of
+// a tile that would be empty), and few roundings do not average out: with one
+// term, results of one-token calls came out up to 1.5 times as far from the
+// exact ones as the result's own rounding puts them, with two 1.00 times.
+// With 33 to 64 rows they would take a tile of twice the rows (the down
+// projection of 64 rows x 8 x 1728 x 5120: 38 -> 48 us) for roundings that
+// average out (1.41 to 1.43 times).
 constexpr uint32_t fold_of(uint64_t rows, int dtype) {
-  return dtype != DT_BF16 || rows == 0 ? 0 : rows <= Thin::BM / 2 ? Thin::BM / 2 : rows <= Flat::BM / 2 ? Flat::BM / 2
-         : rows <= Small::BM / 2 ? Small::BM / 2 : 0;
+  return dtype != DT_BF16 || rows == 0 ? 0 : rows <= Thin::BM / 2 ? Thin::BM / 2 : rows <= Flat::BM / 2 ? Flat::BM / 2 : 0;
 }
 
 // Tile class that a launch of this plan takes (its problems are final).

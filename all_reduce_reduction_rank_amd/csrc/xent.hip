@@ -12,7 +12,7 @@
 // piece's logits, store d = (exp(l - lse) - onehot) grad for the piece only,
 // then dx += d W and dW = d^T x.  dx is added up over the pieces in fp32 and
 // rounded once; d is rounded to bf16 for the matrix cores, over a common scale
-// (scale_kernel) or, with up to 64 rows, in two terms (fold_of).  The piece caps
+// (scale_kernel) or, with up to 32 rows, in two terms (fold_of).  The piece caps
 // the memory d takes.
 #include <hip/hip_runtime.h>
 #include <math.h>

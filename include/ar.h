@@ -379,8 +379,9 @@ size_t ar_gated_ffn_workspace(int nranks, size_t rows, size_t hidden, size_t int
  * ar_allreduce_rmsnorm) over out[0..N-1] completes the block.
  * gate, up: both NULL, or N fp32 buffers [rows, inter] each that receive g and
  * u for the backward pass (fp32 for either dtype: rounded to bf16 they would
- * add two roundings to every gradient).  The inner product act(g) * u is rounded to dtype before it
- * is multiplied by w_down.  rows 0: nothing is done. */
+ * add two roundings to every gradient).  AR_BF16: act(g) * u is rounded to
+ * bf16 before it is multiplied by w_down (with up to 32 rows it is kept in two
+ * bf16 terms instead).  rows 0: nothing is done. */
 ar_status ar_gated_ffn(int nranks, const void* const* x, const void* const* w_gate, const void* const* w_up,
                        const void* const* w_down, void* const* out, void* const* gate, void* const* up, size_t rows,
                        size_t hidden, size_t inter, ar_act act, ar_dtype dtype, void* workspace,
@@ -394,8 +395,9 @@ ar_status ar_gated_ffn(int nranks, const void* const* x, const void* const* w_ga
  *   dw_gate = dg^T x;  dw_up = du^T x                 [inter, hidden]
  *   dw_down = dout^T (act(g) * u)                     [hidden, inter]
  * dx[r] is rank r's partial sum (an all-reduce completes it); every output is
- * overwritten, not added to.  dg, du and act(g) * u are rounded to dtype
- * before they are multiplied.  rows 0: the weight gradients become zeros. */
+ * overwritten, not added to.  AR_BF16: dg, du and act(g) * u are rounded to
+ * bf16 before they are multiplied (two terms with up to 32 rows).  rows 0: the
+ * weight gradients become zeros. */
 ar_status ar_gated_ffn_backward(int nranks, const void* const* dout, const void* const* x, const void* const* w_gate,
                                 const void* const* w_up, const void* const* w_down, const void* const* gate,
                                 const void* const* up, void* const* dx, void* const* dw_gate, void* const* dw_up,
@@ -433,9 +435,10 @@ ar_status ar_linear_cross_entropy(int nranks, const void* const* x, const void* 
  * all-reduce completes it); every output is overwritten.  The logits are
  * computed again, `piece` vocabulary rows of each rank at a time (a multiple
  * of 256 after rounding down, at least 256; 0: as many as keep d of all ranks
- * within 1 GiB); d is rounded to dtype before it is multiplied, and dx is
- * added up in fp32 and rounded once.  `piece` does not change dw.  rows 0: dw
- * becomes zeros. */
+ * within 1 GiB).  dx is added up in fp32 and rounded once.  AR_BF16: d over
+ * the largest finite |grad_loss| is rounded to bf16 before it is multiplied
+ * (with up to 32 rows d is kept in two bf16 terms instead).  `piece` does not
+ * change dw.  rows 0: dw becomes zeros. */
 ar_status ar_linear_cross_entropy_backward(int nranks, const float* grad_loss, const void* const* x,
                                            const void* const* w, const int64_t* target, const float* const* lse,
                                            void* const* dx, void* const* dw, size_t rows, size_t hidden, size_t vocab,
