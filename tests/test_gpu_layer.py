@@ -109,6 +109,19 @@ def test_ffn_large_tiles(dt):
     run_ffn(8, 1288, 1160, 1416, dt, "silu", seed=5, ranks=(0, 7))
 
 
+# Shapes that take the tile classes the ones above do not (n, rows, hidden, inter).
+FFN_CLASS_SHAPES = [
+    (8, 408, 112, 1160), (8, 776, 280, 1632), (8, 603, 40, 1368), (2, 605, 40, 1704), (8, 586, 1856, 72),
+    (8, 763, 752, 32), (1, 1116, 1856, 32),
+]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n,rows,hidden,inter", FFN_CLASS_SHAPES)
+def test_ffn_tile_classes(n, rows, hidden, inter, dt):
+    run_ffn(n, rows, hidden, inter, dt, "silu", seed=rows, ranks=(0, n - 1))
+
+
 def xent_inputs(n, rows, hidden, vocab, dt, seed, ignored=0.2):
     gen = torch.Generator().manual_seed(seed)
     x = _rand(gen, (rows, hidden), dt)
@@ -144,7 +157,8 @@ def run_xent(n, rows, hidden, vocab, dt, piece=0, seed=0, inputs=None):
 XENT_SHAPES = [
     # ranks, rows, hidden, vocab
     (1, 1, 8, 2), (1, 1, 64, 1), (2, 3, 7, 33), (3, 17, 65, 1000), (8, 5, 64, 3), (1, 64, 200, 511), (2, 129, 136, 513),
-    (4, 130, 40, 2050), (8, 260, 72, 4099), (1, 300, 33, 129),
+    (4, 130, 40, 2050), (8, 260, 72, 4099), (1, 300, 33, 129), (8, 1, 200, 16), (3, 1, 40, 17), (1, 22, 144, 29),
+    (3, 1047, 88, 9342),
 ]
 
 

@@ -1,0 +1,110 @@
+"""The product kernels' tile classes (CPU only: a host build of the rule, and the
+kernels' assembly): the GPU tests' shapes reach every class of every kernel, the
+rule's choices at the two ends, and no kernel spills registers."""
+
+import os
+import re
+import subprocess
+
+import pytest
+
+from all_reduce_reduction_rank_amd import vocab_shards
+from tests.test_gpu_layer import FFN_CLASS_SHAPES, FFN_SHAPES, XENT_SHAPES
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "all_reduce_reduction_rank_amd", "csrc")
+FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
+KINDS = ("gated", "store", "stats", "dlogits", "gated_bwd", "grads")
+CLASSES = ("large", "small", "flat", "split", "thin")
+DT = {"f32": 0, "bf16": 1}
+GRAD_TN = 1
+
+
+@pytest.fixture(scope="module")
+def classes(tmp_path_factory):
+    exe = str(tmp_path_factory.mktemp("tiles") / "check")
+    res = subprocess.run(["hipcc", *FLAGS, os.path.join(ROOT, "tests", "product_tile_check.hip"),
+                          os.path.join(CSRC, "products.hip"), "-o", exe], capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr
+
+    def run(plans):
+        text = "\n".join(f"{KINDS.index(kind)} {DT[dt]} {head} {len(probs)} " +
+                         " ".join(" ".join(map(str, p)) for p in probs) for kind, dt, head, probs in plans)
+        out = subprocess.run([exe], input=text, capture_output=True, text=True, timeout=60)
+        assert out.returncode == 0
+        return [CLASSES[int(x)] for x in out.stdout.split()]
+
+    return run
+
+
+def _fold(rows, dt):
+    return 0 if dt == "f32" or rows == 0 or rows > 32 else 8 if rows <= 8 else 32
+
+
+def _split(dt, fold, n, dx, dw):
+    """The gradients' launches: one, or two where dx has second terms."""
+    return [("grads", dt, 0, dx), ("grads", dt, 0, dw)] if fold else [("grads", dt, n, dx + dw)]
+
+
+def ffn_plans(n, rows, hidden, inter, dt):
+    f = _fold(rows, dt)
+    two = 2 if f else 1
+    dw = [(inter, hidden, rows, two, 0, GRAD_TN)] * 2 + [(hidden, inter, rows, two, 0, GRAD_TN)]
+    return [("gated", dt, 0, [(rows, inter, hidden, 1, f, 0)] * n),
+            ("store", dt, 0, [(f + rows, hidden, inter, 1, f, 0)] * n),
+            ("gated_bwd", dt, 0, [(rows, inter, hidden, 1, f, 0)] * n),
+            *_split(dt, f, n, [(f + rows, hidden, inter, 2, f, 0)] * n, dw * n)]
+
+
+def xent_plans(n, rows, hidden, vocab, dt):
+    f = _fold(rows, dt)
+    two = 2 if f else 1
+    shards = vocab_shards(vocab, n)
+    some = [v for v in shards if v]
+    return [("stats", dt, 0, [(rows, v, hidden, 1, 0, 0) for v in some]),
+            ("dlogits", dt, 0, [(rows, v, hidden, 1, f, 0) for v in some]),
+            *_split(dt, f, n, [(f + rows, hidden, v, 1, f, 0) for v in shards],
+                    [(v, hidden, rows, two, 0, GRAD_TN) for v in some])]
+
+
+def test_gpu_tests_reach_every_class_of_every_kernel(classes):
+    plans = []
+    for dt in ("bf16", "f32"):
+        for rows, hidden, inter in FFN_SHAPES:
+            plans += ffn_plans(2, rows, hidden, inter, dt)
+        for n, rows, hidden, inter in [*FFN_CLASS_SHAPES, (8, 1288, 1160, 1416)]:
+            plans += ffn_plans(n, rows, hidden, inter, dt)
+        for n, rows, hidden, vocab in XENT_SHAPES:
+            plans += xent_plans(n, rows, hidden, vocab, dt)
+        plans += xent_plans(2, 1030, 72, 20011 if dt == "bf16" else 16400, dt)
+    seen = {(p[0], p[1], c) for p, c in zip(plans, classes(plans))}
+    missing = {(k, dt, c) for k in KINDS for dt in DT for c in CLASSES if (dt, c) != ("f32", "large")} - seen
+    assert not missing, sorted(missing)
+
+
+def test_choices_at_both_ends(classes):
+    one = ffn_plans(8, 1, 5120, 1728, "bf16")
+    assert classes(one[:2]) == ["thin", "thin"]
+    step = ffn_plans(8, 8192, 5120, 1728, "bf16")
+    assert classes(step) == ["large"] * 4
+    # second terms fix the reader's tile: both terms of every row in one tile
+    for rows, want in ((1, {"thin"}), (8, {"thin"}), (9, {"flat", "split"}), (32, {"flat", "split"})):
+        got = classes([p for p in ffn_plans(4, rows, 2048, 1408, "bf16") if p[0] == "store" or p[3][0][4]])
+        assert got[1] in want, (rows, got)
+    # nor may the large tile write them
+    assert "large" not in classes(ffn_plans(8, 32, 8192, 8192, "bf16")[:4])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_no_kernel_uses_scratch_memory(tmp_path, dt):
+    out = str(tmp_path / "k.s")
+    res = subprocess.run(["hipcc", *FLAGS, "-S", "--cuda-device-only", "-o", out,
+                          os.path.join(CSRC, f"products_{dt}.hip")], capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr
+    text = open(out).read()
+    kernels = re.findall(r"^(_ZN2ar\S*product_kernel\S*):", text, re.M)
+    # 4 kinds + 2 gated kinds x 3 activations, in every class (fp32: not the large one)
+    assert len(kernels) == (4 + 2 * 3) * (5 if dt == "bf16" else 4)
+    spills = re.findall(r"\.vgpr_spill_count:\s+(\d+)", text)
+    assert spills and all(int(x) == 0 for x in spills)
+    assert all(int(x) == 0 for x in re.findall(r"\.private_segment_fixed_size:\s+(\d+)", text))
