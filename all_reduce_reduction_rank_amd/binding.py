@@ -19,6 +19,7 @@ if that fails every call raises -- there is no CPU fallback.
 """
 
 import ctypes
+import functools
 import math
 import os
 
@@ -390,6 +391,20 @@ def allreduce_noalloc(send, recv=None, algo="ring", proto="simple", chunk_bytes=
 
 
 # ---- operators of a tensor-parallel layer ----
+# Small calls are bound by this host work: pointer array types are made once,
+# workspace sizes are kept by shape, checks are one pass of attribute reads.
+
+_PTRS = [ctypes.c_void_p * n for n in range(9)]
+
+
+@functools.lru_cache(maxsize=256)
+def _ffn_workspace(n, rows, hidden, inter, dt, backward):
+    return _lib().ar_gated_ffn_workspace(n, rows, hidden, inter, DTYPES[dt], backward)
+
+
+@functools.lru_cache(maxsize=256)
+def _xent_workspace(n, rows, hidden, vocab, dt, backward, piece):
+    return _lib().ar_linear_cross_entropy_workspace(n, rows, hidden, vocab, DTYPES[dt], backward, piece)
 
 
 def _layer_ranks(first, what):
@@ -410,14 +425,14 @@ def _layer_list(ts, n, shapes, dtype, device, what):
     same = not isinstance(shapes, list)
     for i, t in enumerate(ts):
         shape = shapes if same else shapes[i]
-        if t.dtype is not dtype:
-            raise TypeError(f"{what}[{i}] is {t.dtype}; the call needs {dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{what}[{i}] has shape {tuple(t.shape)}; the call needs {tuple(shape)}")
-        if t.get_device() != device or not t.is_contiguous():
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+            if t.dtype is not dtype:
+                raise TypeError(f"{what}[{i}] is {t.dtype}; the call needs {dtype}")
+            if t.shape != shape:
+                raise ValueError(f"{what}[{i}] has shape {tuple(t.shape)}; the call needs {tuple(shape)}")
             raise ValueError(f"{what}[{i}] must be a contiguous tensor on the call's device")
         ptrs.append(t.data_ptr())
-    return (ctypes.c_void_p * n)(*ptrs)
+    return _PTRS[n](*ptrs)
 
 
 def _layer_vector(t, rows, dtype, device, what):
@@ -509,8 +524,8 @@ def gated_ffn(x, w_gate, w_up, w_down, out=None, gate=None, up=None, act="silu",
     scratch = _Scratch(stream, device)
     if out is None:
         out = scratch.ranks(n, (rows, hidden), dtype)
-        o = (ctypes.c_void_p * n)(*[t.data_ptr() for t in out])
-    nbytes = _lib().ar_gated_ffn_workspace(n, rows, hidden, inter, DTYPES[dt], 0)
+        o = _PTRS[n](*[t.data_ptr() for t in out])
+    nbytes = _ffn_workspace(n, rows, hidden, inter, dt, 0)
     ws, ws_ptr = scratch.workspace(nbytes)
     _check(_lib().ar_gated_ffn(n, *ptrs, o, g, u, rows, hidden, inter, a, DTYPES[dt], ws_ptr, nbytes,
                                _stream_handle(stream, device)), "ar_gated_ffn")
@@ -540,9 +555,9 @@ def gated_ffn_backward(dout, x, w_gate, w_up, w_down, gate, up, dx=None, dw_gate
     for i, (_, t, shape) in enumerate(results):
         if t is None:
             t = scratch.ranks(n, shape, dtype)
-            given[i] = (ctypes.c_void_p * n)(*[v.data_ptr() for v in t])
+            given[i] = _PTRS[n](*[v.data_ptr() for v in t])
         outs.append(t)
-    nbytes = _lib().ar_gated_ffn_workspace(n, rows, hidden, inter, DTYPES[dt], 1)
+    nbytes = _ffn_workspace(n, rows, hidden, inter, dt, 1)
     ws, ws_ptr = scratch.workspace(nbytes)
     _check(_lib().ar_gated_ffn_backward(n, d, *ptrs, g, u, *given, rows, hidden, inter, a, DTYPES[dt], ws_ptr, nbytes,
                                         _stream_handle(stream, device)), "ar_gated_ffn_backward")
@@ -592,9 +607,9 @@ def linear_cross_entropy(x, w, target, loss=None, lse=None, stream=None):
     for i, t in enumerate((loss, lse)):
         if t is None:
             t = scratch.ranks(n, (rows,), torch.float32)
-            given[i] = (ctypes.c_void_p * n)(*[v.data_ptr() for v in t])
+            given[i] = _PTRS[n](*[v.data_ptr() for v in t])
         outs.append(t)
-    nbytes = _lib().ar_linear_cross_entropy_workspace(n, rows, hidden, vocab, DTYPES[dt], 0, 0)
+    nbytes = _xent_workspace(n, rows, hidden, vocab, dt, 0, 0)
     ws, ws_ptr = scratch.workspace(nbytes)
     _check(_lib().ar_linear_cross_entropy(n, *ptrs, *given, rows, hidden, vocab, DTYPES[dt], ws_ptr, nbytes,
                                           _stream_handle(stream, device)), "ar_linear_cross_entropy")
@@ -624,9 +639,9 @@ def linear_cross_entropy_backward(grad_loss, x, w, target, lse, dx=None, dw=None
         if t is None:
             same = shapes[0] == shapes[-1]  # (shards: all of one length, or not)
             t = scratch.ranks(n, shapes[0], dtype) if same else [scratch.empty(shape, dtype) for shape in shapes]
-            given[i] = (ctypes.c_void_p * n)(*[v.data_ptr() for v in t])
+            given[i] = _PTRS[n](*[v.data_ptr() for v in t])
         outs.append(t)
-    nbytes = _lib().ar_linear_cross_entropy_workspace(n, rows, hidden, vocab, DTYPES[dt], 1, piece)
+    nbytes = _xent_workspace(n, rows, hidden, vocab, dt, 1, piece)
     ws, ws_ptr = scratch.workspace(nbytes)
     _check(_lib().ar_linear_cross_entropy_backward(n, gl, *ptrs, z, *given, rows, hidden, vocab, DTYPES[dt], piece,
                                                    ws_ptr, nbytes, _stream_handle(stream, device)),
