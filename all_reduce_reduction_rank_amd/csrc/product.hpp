@@ -286,6 +286,9 @@ struct Large {  // 8 waves of 128 x 64, 128 KB of LDS: one workgroup per CU
 struct Small {  // 4 waves of 64 x 64, 64 KB: two workgroups per CU
   static constexpr int BM = 128, BN = 128, WM = 2, WN = 2, WK = 1, STAGES = 2;
 };
+struct Tall {  // 4 waves of 64 x 32, 48 KB: three workgroups per CU (fp32, Flat's place)
+  static constexpr int BM = 128, BN = 64, WM = 2, WN = 2, WK = 1, STAGES = 2;
+};
 struct Flat {  // 4 waves of 64 x 32, 72 KB: two workgroups per CU
   static constexpr int BM = 64, BN = 128, WM = 1, WN = 4, WK = 1, STAGES = 3;
 };

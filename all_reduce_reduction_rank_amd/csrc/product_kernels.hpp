@@ -304,12 +304,15 @@ hipError_t launch(ProductPlan& plan, hipStream_t stream) {
 
 template <int KIND, int DT, uint32_t ACT = ACT_SILU>
 hipError_t launch_kind(ProductPlan& plan, int device, hipStream_t stream) {
-  switch (product_tile(KIND, DT, plan, device)) {
-    case TILE_LARGE:
-      if constexpr (DT == DT_BF16) return launch<KIND, DT, Large, ACT>(plan, stream);
-      else return hipErrorInvalidValue;  // product_tile does not take it
+  const int tile = product_tile(KIND, DT, plan, device);
+  if constexpr (DT == DT_BF16) {  // classes of one type only
+    if (tile == TILE_LARGE) return launch<KIND, DT, Large, ACT>(plan, stream);
+    if (tile == TILE_FLAT) return launch<KIND, DT, Flat, ACT>(plan, stream);
+  } else {
+    if (tile == TILE_TALL) return launch<KIND, DT, Tall, ACT>(plan, stream);
+  }
+  switch (tile) {
     case TILE_SMALL: return launch<KIND, DT, Small, ACT>(plan, stream);
-    case TILE_FLAT: return launch<KIND, DT, Flat, ACT>(plan, stream);
     case TILE_SPLIT: return launch<KIND, DT, Split, ACT>(plan, stream);
     case TILE_THIN: return launch<KIND, DT, Thin, ACT>(plan, stream);
   }

@@ -17,7 +17,9 @@
 // One small product, [512, 4096] x [1024, 4096]: 83, 50, 31, 16 us.  Thin is
 // for 16 rows at most: with more it reads the weights again for every 16.
 // fp32 runs 16 times as many instructions per byte, so its steps cost what
-// its matrix instructions do.
+// its matrix instructions do, and the choice is which tile fills the CUs most
+// evenly: two ranks of [1024, 1024] x [8000, 1024] 290 us in Small and 315 in
+// Tall, but [1024, 8000] x [8000, 1024] 536, 307, Split 297.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -29,14 +31,16 @@ namespace {
 
 struct ClassCost {
   uint32_t bm, bn, parts, resident;  // parts: of K; resident: workgroups per CU
-  double fixed, alone, full;         // bf16
+  double fixed, alone, full;         // us: of a workgroup, of a step
+  double f32;                        // fp32 matrix instructions: time over Tall's
 };
 constexpr ClassCost COST[TILE_CLASSES] = {
-    {Large::BM, Large::BN, Large::WK, 1, 9.0, 1.75, 1.75},
-    {Small::BM, Small::BN, Small::WK, 2, 4.0, 1.15, 1.35},
-    {Flat::BM, Flat::BN, Flat::WK, 2, 4.0, 0.75, 0.95},
-    {Split::BM, Split::BN, Split::WK, 1, 4.5, 0.8, 1.6},
-    {Thin::BM, Thin::BN, Thin::WK, 2, 4.5, 0.25, 0.6},
+    {Large::BM, Large::BN, Large::WK, 1, 9.0, 1.75, 1.75, 0.0},  // bf16 only
+    {Small::BM, Small::BN, Small::WK, 2, 4.0, 1.15, 1.35, 0.96},
+    {Tall::BM, Tall::BN, Tall::WK, 3, 4.0, 0.75, 1.2, 1.0},      // fp32 only
+    {Flat::BM, Flat::BN, Flat::WK, 2, 4.0, 0.75, 0.95, 0.0},  // bf16 only
+    {Split::BM, Split::BN, Split::WK, 1, 4.5, 0.8, 1.6, 1.22},
+    {Thin::BM, Thin::BN, Thin::WK, 2, 4.5, 0.25, 0.6, 1.22},
 };
 constexpr double F32_FLOPS_PER_CU_US = 0.55e6;  // of 0.61e6 (16x16x4 at 2.4 GHz)
 
@@ -121,7 +125,8 @@ int product_tile(int kind, int dtype, const ProductPlan& plan, int device) {
   int best = TILE_SMALL;
   double best_us = 1e30;
   for (int c = 0; c < TILE_CLASSES; ++c) {
-    if (c == TILE_LARGE && (dtype != DT_BF16 || fold)) continue;
+    if (c == TILE_TALL ? dtype == DT_BF16 : (c == TILE_LARGE || c == TILE_FLAT) && dtype != DT_BF16) continue;
+    if (c == TILE_LARGE && fold) continue;
     if (c == TILE_THIN && max_m > (uint32_t)Thin::BM) continue;
     const ClassCost& k = COST[c];
     if (fold && reads_terms && k.bm != 2 * fold) continue;
@@ -138,20 +143,28 @@ int product_tile(int kind, int dtype, const ProductPlan& plan, int device) {
       shortest = s < shortest ? s : shortest;
     }
     if (tiles == 0) continue;
-    double alone = k.alone, full = k.full;
-    if (dtype != DT_BF16) {
-      const double mm = 2.0 * k.bm * k.bn * per_step * k.parts / F32_FLOPS_PER_CU_US;
-      alone = mm > alone ? mm : alone;
-      full = mm * k.resident > full ? mm * k.resident : full;
-    }
     const double slots = cus * k.resident;
     const double rounds = (double)(uint64_t)(tiles / slots);
     const double rest = tiles - rounds * slots;
     double us;
-    if (rounds == 0) us = k.fixed + longest * (rest <= cus ? alone : full);
-    else if (longest == shortest) us = rounds * (k.fixed + longest * full) +
-                                       (rest == 0 ? 0 : k.fixed + longest * (rest <= cus && k.resident > 1 ? alone : full));
-    else us = tiles / slots * k.fixed + (work / slots + 0.5 * shortest) * full;  // long tiles first
+    if (dtype != DT_BF16) {
+      // matrix instructions: a CU works its tiles off one after the other,
+      // however many share it (`one`: a tile by itself, one wave per SIMD)
+      const double mm = k.f32 * 2.0 * k.bm * k.bn * per_step * k.parts / F32_FLOPS_PER_CU_US;
+      const double per = mm * k.resident > k.full ? mm : k.full / k.resident;
+      const double one = 1.2 * mm > k.alone ? 1.2 * mm : k.alone;
+      const double each = (double)(uint64_t)((tiles + cus - 1) / cus);
+      const double turns = (double)(uint64_t)((each + k.resident - 1) / k.resident);
+      const double busy = longest == shortest ? each * longest * per : (work / cus + 0.5 * shortest) * per;
+      us = turns * k.fixed + (busy > longest * one ? busy : longest * one);
+    } else if (rounds == 0) {
+      us = k.fixed + longest * (rest <= cus ? k.alone : k.full);
+    } else if (longest == shortest) {
+      us = rounds * (k.fixed + longest * k.full) +
+           (rest == 0 ? 0 : k.fixed + longest * (rest <= cus && k.resident > 1 ? k.alone : k.full));
+    } else {  // long tiles first
+      us = tiles / slots * k.fixed + (work / slots + 0.5 * shortest) * k.full;
+    }
     if (us < best_us) {
       best_us = us;
       best = c;

@@ -53,12 +53,12 @@ constexpr uint32_t fold_of(uint64_t rows, int dtype) {
 }
 
 // Tile class that a launch of this plan takes (its problems are final).
-enum TileClass : int { TILE_LARGE = 0, TILE_SMALL, TILE_FLAT, TILE_SPLIT, TILE_THIN, TILE_CLASSES };
+enum TileClass : int { TILE_LARGE = 0, TILE_SMALL, TILE_TALL, TILE_FLAT, TILE_SPLIT, TILE_THIN, TILE_CLASSES };
 int product_tile(int kind, int dtype, const ProductPlan& plan, int device);
 // Columns of C a tile of a class that is not paired covers: PK_STATS writes
 // one partial per row and that many columns.
 constexpr uint32_t tile_cols(int tile) {
-  constexpr uint32_t cols[TILE_CLASSES] = {Large::BN, Small::BN, Flat::BN, Split::BN, Thin::BN};
+  constexpr uint32_t cols[TILE_CLASSES] = {Large::BN, Small::BN, Tall::BN, Flat::BN, Split::BN, Thin::BN};
   return cols[tile];
 }
 constexpr uint32_t MIN_TILE_COLS = Thin::BN;

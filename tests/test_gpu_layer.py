@@ -112,7 +112,7 @@ def test_ffn_large_tiles(dt):
 # Shapes that take the tile classes the ones above do not (n, rows, hidden, inter).
 FFN_CLASS_SHAPES = [
     (8, 408, 112, 1160), (8, 776, 280, 1632), (8, 603, 40, 1368), (2, 605, 40, 1704), (8, 586, 1856, 72),
-    (8, 763, 752, 32), (1, 1116, 1856, 32),
+    (8, 763, 752, 32), (1, 1116, 1856, 32), (8, 1730, 432, 32),
 ]
 
 
