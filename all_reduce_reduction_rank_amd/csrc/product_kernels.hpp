@@ -70,7 +70,7 @@ __device__ __forceinline__ void store_result(P& x, const Problem& p, float scale
         const uint64_t row = (uint64_t)row0 + r;
 #pragma unroll
         for (int e = 0; e < V; ++e) v[e] *= scale;
-        if (row < m) store_row<P::DT, V>(p.c[0] + row * p.ldc * ES, (uint64_t)col0 + col, p.n, vec, v);
+        if (row < m) store_row<P::DT, V, true>(p.c[0] + row * p.ldc * ES, (uint64_t)col0 + col, p.n, vec, v);
       });
 }
 
@@ -144,8 +144,8 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
       char* to = p.c[0] + row * ldc * ES;
       store_terms<DT, V>(to, FOLDS && p.fold ? to + p.fold * ldc * ES : nullptr, (uint64_t)col0 + col, p.ldc, vec, h);
       if (p.c[1]) {
-        store_row<DT_F32, V>(p.c[1] + row * (uint64_t)n * 4, (uint64_t)col0 + col, n, n % 4 == 0, g);
-        store_row<DT_F32, V>(p.c[2] + row * (uint64_t)n * 4, (uint64_t)col0 + col, n, n % 4 == 0, u);
+        store_row<DT_F32, V, true>(p.c[1] + row * (uint64_t)n * 4, (uint64_t)col0 + col, n, n % 4 == 0, g);
+        store_row<DT_F32, V, true>(p.c[2] + row * (uint64_t)n * 4, (uint64_t)col0 + col, n, n % 4 == 0, u);
       }
     });
   } else if constexpr (KIND == PK_GATED_BWD) {
@@ -210,7 +210,7 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
             v[e] = q.live && c < n ? d : 0.f;  // columns n .. ldc: zeros
           }
           char* to = p.c[0] + row * ldc * ES;
-          store_terms<DT, V>(to, FOLDS && p.fold ? to + p.fold * ldc * ES : nullptr, (uint64_t)col0 + col, p.ldc, vec, v);
+          store_terms<DT, V, true>(to, FOLDS && p.fold ? to + p.fold * ldc * ES : nullptr, (uint64_t)col0 + col, p.ldc, vec, v);
         });
   } else if constexpr (P::WK > 1) {  // PK_STATS, K split over the waves
     float* at_target = (float*)p.c[1];
