@@ -40,18 +40,20 @@ struct FfnShape {
   // one rank's copies of x (dout), of w_gate (w_up), of w_down, where their
   // rows are not whole 16-byte chunks
   uint64_t pack_x, pack_up, pack_down;
+  uint64_t share;  // one rank's shares of out (dx)
   uint64_t workspace(int n, bool backward) const {
-    return (uint64_t)n * ((backward ? 3 : 1) * mid_bytes + (backward ? 2 : 1) * pack_x + 2 * pack_up + pack_down);
+    return (uint64_t)n * ((backward ? 3 : 1) * mid_bytes + share + (backward ? 2 : 1) * pack_x + 2 * pack_up + pack_down);
   }
 };
 
-FfnShape shape_of(size_t rows, size_t hidden, size_t inter, int dtype) {
+FfnShape shape_of(int n, size_t rows, size_t hidden, size_t inter, int dtype) {
   FfnShape s;
   s.rows = rows, s.hidden = hidden, s.inter = inter;
   s.es = dtype == DT_BF16 ? 2 : 4;
   s.pitch = Packer::pitch(inter, s.es);
   s.fold = fold_of(rows, dtype);
   s.mid_bytes = layer_align((s.fold + s.rows) * s.pitch * s.es);
+  s.share = share_bytes(n, rows, hidden);
   s.pack_x = Packer::bytes(rows, hidden, s.es);
   s.pack_up = Packer::bytes(inter, hidden, s.es);
   s.pack_down = Packer::bytes(hidden, inter, s.es);
@@ -72,7 +74,7 @@ extern "C" {
 
 size_t ar_gated_ffn_workspace(int nranks, size_t rows, size_t hidden, size_t inter, ar_dtype dtype, int backward) {
   if (check_shape(nranks, rows, hidden, inter, 0, (int)dtype) != AR_OK || rows == 0) return 0;
-  return (size_t)shape_of(rows, hidden, inter, (int)dtype).workspace(nranks, backward != 0);
+  return (size_t)shape_of(nranks, rows, hidden, inter, (int)dtype).workspace(nranks, backward != 0);
 }
 
 ar_status ar_gated_ffn(int nranks, const void* const* x, const void* const* w_gate, const void* const* w_up,
@@ -83,7 +85,7 @@ ar_status ar_gated_ffn(int nranks, const void* const* x, const void* const* w_ga
   if (st != AR_OK) return st;
   if (!x || !w_gate || !w_up || !w_down || !out || !gate != !up) return AR_ERR_INVALID;
   if (rows == 0) return AR_OK;
-  const FfnShape s = shape_of(rows, hidden, inter, (int)dtype);
+  const FfnShape s = shape_of(nranks, rows, hidden, inter, (int)dtype);
   const uint64_t xb = s.rows * s.hidden * s.es, wb = s.hidden * s.inter * s.es, gb = s.rows * s.inter * 4;
   const uint64_t need = s.workspace(nranks, false);
   LayerBuffers b;
@@ -106,7 +108,9 @@ ar_status ar_gated_ffn(int nranks, const void* const* x, const void* const* w_ga
 
   ProductPlan up_plan, down_plan;
   up_plan.a.act = (int32_t)act;
-  Packer pack(ws + (uint64_t)nranks * s.mid_bytes, s.es);
+  char* shares = ws + (uint64_t)nranks * s.mid_bytes;
+  down_plan.may_share = s.share != 0;
+  Packer pack(shares + (uint64_t)nranks * s.share, s.es);
   for (int r = 0; r < nranks; ++r) {
     const Packer::Rows px = pack.rows(x[r], s.rows, s.hidden), pg = pack.rows(w_gate[r], s.inter, s.hidden),
                        pu = pack.rows(w_up[r], s.inter, s.hidden), pd = pack.rows(w_down[r], s.hidden, s.inter);
@@ -123,6 +127,7 @@ ar_status ar_gated_ffn(int nranks, const void* const* x, const void* const* w_ga
     p->a[0] = h(r);
     p->b[0] = pd.p;
     p->c[0] = (char*)out[r];
+    p->c[2] = shares + (uint64_t)r * s.share;
   }
   if (pack.launch((hipStream_t)stream) != hipSuccess) return AR_ERR_HIP;
   if (launch_products(PK_GATED, (int)dtype, up_plan, dev, (hipStream_t)stream) != hipSuccess) return AR_ERR_HIP;
@@ -139,7 +144,7 @@ ar_status ar_gated_ffn_backward(int nranks, const void* const* dout, const void*
   if (st != AR_OK) return st;
   if (!dout || !x || !w_gate || !w_up || !w_down || !gate || !up || !dx || !dw_gate || !dw_up || !dw_down)
     return AR_ERR_INVALID;
-  const FfnShape s = shape_of(rows, hidden, inter, (int)dtype);
+  const FfnShape s = shape_of(nranks, rows, hidden, inter, (int)dtype);
   const uint64_t xb = s.rows * s.hidden * s.es, wb = s.hidden * s.inter * s.es, gb = s.rows * s.inter * 4;
   const uint64_t need = rows ? s.workspace(nranks, true) : 0;
   LayerBuffers b;
@@ -166,7 +171,9 @@ ar_status ar_gated_ffn_backward(int nranks, const void* const* dout, const void*
 
   ProductPlan mid_plan, grads;
   mid_plan.a.act = (int32_t)act;
-  Packer pack(ws + (uint64_t)nranks * 3 * s.mid_bytes, s.es);
+  char* shares = ws + (uint64_t)nranks * 3 * s.mid_bytes;
+  grads.may_share = s.share != 0;
+  Packer pack(shares + (uint64_t)nranks * s.share, s.es);
   Packer::Rows px[MAX_RANKS], po[MAX_RANKS];
   for (int r = 0; r < nranks; ++r) {
     // (with no rows nothing is read, and nothing copied)
@@ -191,6 +198,7 @@ ar_status ar_gated_ffn_backward(int nranks, const void* const* dout, const void*
     p->b[0] = pg.p;
     p->b[1] = pu.p;
     p->c[0] = (char*)dx[r];
+    p->c[2] = shares + (uint64_t)r * s.share;
   }
   grads.head = nranks;
   // With no rows every weight gradient is a product with k = 0: zeros.  The

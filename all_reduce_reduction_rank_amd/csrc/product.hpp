@@ -59,6 +59,7 @@ typedef __attribute__((address_space(3))) char lds_char;
 constexpr int KB = 128;  // bytes of k per operand row and K step: a cache line, two substeps
 constexpr uint32_t OUT_OF_RANGE = 0x7fffff00u;  // beyond every descriptor (at most 2^30 bytes)
 constexpr int MAX_PROBLEMS = 4 * MAX_RANKS;
+constexpr uint32_t MAX_SHARES = 16;  // of a tile's K
 
 template <int DT>
 struct KElem {
@@ -84,6 +85,9 @@ struct Problem {
   // terms `fold` rows below the first; those that read it as A have both in
   // one tile of 2 fold rows and add row r + fold to row r of the result.
   uint32_t fold;
+  // Workgroups that share a tile's K; with more than one, each stores its fp32
+  // sum to c[2] + its share's [rows, ldc] block, and a second kernel adds them.
+  uint32_t shares;
   uint32_t mode;  // what the epilogue (and PK_GRADS' layout) goes by
 };
 
@@ -374,14 +378,14 @@ struct Product {
     }
   }
 
-  // Accumulate the tile at (row0, col0) of problem p.
+  // Accumulate the tile at (row0, col0) of problem p, share `share` of its K.
   //
   // A substep multiplies fragments that were read from LDS during the one
   // before, while it reads the next one's, so the matrix cores never wait for
   // an LDS read.  Before the last substep of step t every wave has read all
   // of t, and step t + 1 must have landed: one barrier there frees step t's
   // buffer for step t + STAGES and publishes t + 1.
-  __device__ __forceinline__ void run(const Problem& p, uint32_t row0, uint32_t col0, char* smem) {
+  __device__ __forceinline__ void run(const Problem& p, uint32_t share, uint32_t row0, uint32_t col0, char* smem) {
     const int wk = WK == 1 ? 0 : uniform((int)(threadIdx.x / GROUP));
     lds_char* lds = (lds_char*)smem + wk * RING;
 #pragma unroll
@@ -392,8 +396,9 @@ struct Product {
     const uint32_t per = (p.k + BK - 1) / BK;
     const uint32_t all = per * p.nseg;
     // this wave's part of the steps
-    const uint32_t part = (all + WK - 1) / WK;
-    const uint32_t first = (uint32_t)wk * part;
+    const uint32_t parts = WK * p.shares;
+    const uint32_t part = (all + parts - 1) / parts;
+    const uint32_t first = (share * WK + (uint32_t)wk) * part;
     const uint32_t steps = first >= all ? 0 : all - first < part ? all - first : part;
     if (steps == 0) return;
     LoadA la;
@@ -421,6 +426,18 @@ struct Product {
     landed<(STAGES - 1) * LOADS>(steps >= (uint32_t)STAGES);
 #pragma unroll
     for (int i = 0; i < TM; ++i) read(lds, 0, fa[0], fb[0], i);
+    // Products of few rows in fp32 add up K in blocks: an error of 1.5e-6 of
+    // a row over k = 6478 in one chain is that of the few values it has, and
+    // no mean over many evens it out.
+    constexpr bool BLOCKED = DT == DT_F32 && WK > 1;
+    constexpr uint32_t BLOCK_STEPS = 4;
+    v4f sum[BLOCKED ? TM : 1][BLOCKED ? TN : 1];
+    if constexpr (BLOCKED) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) sum[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
     uint32_t cur = 0;  // byte offset of step t's buffer
     // the two substeps' fragment sets alternate by name
     for (uint32_t t = 0; t < steps; ++t) {
@@ -440,6 +457,23 @@ struct Product {
         interleave<0>();
       }
       cur = next;
+      if constexpr (BLOCKED) {
+        if (t % BLOCK_STEPS == BLOCK_STEPS - 1) {
+#pragma unroll
+          for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+              sum[i][j] += acc[i][j];
+              acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+            }
+        }
+      }
+    }
+    if constexpr (BLOCKED) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] += sum[i][j];
     }
     landed<0>(false);
   }
@@ -610,15 +644,18 @@ __device__ __forceinline__ Floats<V> load_floats(const char* row, uint64_t col, 
   return r;
 }
 
-// Find this workgroup's problem and tile.  Returns the problem's index.
+// Find this workgroup's problem, tile and share of its K.  Returns the problem's
+// index.
 template <class P>
-__device__ __forceinline__ int locate(const ProductArgs& a, uint32_t* row0, uint32_t* col0) {
+__device__ __forceinline__ int locate(const ProductArgs& a, uint32_t* row0, uint32_t* col0, uint32_t* share) {
   const uint32_t b = blockIdx.x;
   const uint32_t t = b < a.head ? tile_of_block(b, a.head) : a.head + tile_of_block(b - a.head, a.tiles - a.head);
   int q = 0;
   while (q + 1 < a.nprob && t >= a.p[q + 1].first) ++q;
   uint32_t tm, tn;
-  tile_coords(t - a.p[q].first, a.p[q].tiles_m, a.p[q].tiles_n, &tm, &tn);
+  const uint32_t at = t - a.p[q].first;
+  *share = at % a.p[q].shares;
+  tile_coords(at / a.p[q].shares, a.p[q].tiles_m, a.p[q].tiles_n, &tm, &tn);
   *row0 = tm * P::BM;
   *col0 = tn * P::COLS;
   return q;
@@ -630,6 +667,12 @@ __device__ __forceinline__ int locate(const ProductArgs& a, uint32_t* row0, uint
 struct ProductPlan {
   ProductArgs a;
   uint64_t tiles = 0;
+  // Room for shares: c[2] of the head problems (all of them, where head is 0)
+  // holds MAX_SHARES blocks.
+  bool may_share = false;
+  // Order of the sums over K: 0 any; 1 one wave, 4 quarters added up.  Values
+  // that are computed twice are the same bits twice in the same order.
+  uint32_t k_parts = 0;
   // Problems before this one go first, spread over the XCDs by themselves:
   // where two sorts of tiles differ in length, the long ones start and the
   // short ones fill the end of the launch.
@@ -637,12 +680,16 @@ struct ProductPlan {
 
   ProductPlan() { memset(&a, 0, sizeof(a)); }
 
+  // Problems whose K may be shared: the first ones.
+  int sharing() const { return !may_share ? 0 : head ? head : a.nprob; }
+
   // Rows of both operands start on 16-byte boundaries (Packer).
   Problem* add(uint64_t m, uint64_t n, uint64_t k, uint64_t lda, uint64_t ldb, uint64_t ldc) {
     Problem* p = &a.p[a.nprob++];
     p->m = (uint32_t)m, p->n = (uint32_t)n, p->k = (uint32_t)k;
     p->lda = (uint32_t)lda, p->ldb = (uint32_t)ldb, p->ldc = (uint32_t)ldc;
     p->nseg = 1;
+    p->shares = 1;
     return p;
   }
   // Tiles of every problem for a kernel whose tile covers bm x cols of C.
@@ -655,7 +702,7 @@ struct ProductPlan {
       p.tiles_n = (uint32_t)(((uint64_t)p.n + cols - 1) / cols);
       p.first = (uint32_t)tiles;
       if (i == head) a.head = (uint32_t)tiles;
-      tiles += (uint64_t)p.tiles_m * p.tiles_n;
+      tiles += (uint64_t)p.tiles_m * p.tiles_n * p.shares;
     }
     a.tiles = (uint32_t)tiles;
     return tiles < (1ull << 31);

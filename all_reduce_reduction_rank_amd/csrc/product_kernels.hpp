@@ -77,8 +77,24 @@ __device__ __forceinline__ void store_result(P& x, const Problem& p, float scale
 template <class P>
 __device__ __forceinline__ void store_tile(const Problem& p, float scale, uint32_t row0, uint32_t col0, char* smem) {
   P x;
-  x.run(p, row0, col0, smem);
+  x.run(p, 0, row0, col0, smem);
   store_result(x, p, scale, row0, col0, smem);
+}
+
+// The fp32 sum of one share of K, for finish_kernel.  (In order: sums by atomics
+// would change with the workgroups' timing.)
+template <class P>
+__device__ __forceinline__ void store_share(P& x, const Problem& p, uint32_t share, uint32_t row0, uint32_t col0,
+                                            char* smem) {
+  constexpr int V = KElem<P::DT>::E;
+  const uint32_t m = p.m - p.fold;
+  char* to = p.c[2] + (uint64_t)share * m * p.ldc * 4;
+  x.template hand_out<V, 2>(
+      smem, p.fold, [](uint32_t, uint32_t) { return Nothing(); },
+      [&](uint32_t r, uint32_t col, float* v, float*, Nothing) {
+        const uint64_t row = (uint64_t)row0 + r;
+        if (row < m) store_row<DT_F32, V>(to + row * p.ldc * 4, (uint64_t)col0 + col, p.n, p.ldc % 4 == 0, v);
+      });
 }
 
 // ACT: the gate's activation (gated kinds).
@@ -89,8 +105,8 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
   constexpr int ES = KElem<DT>::ES;
   constexpr int V = KElem<DT>::E;  // values per 16-byte vector of the payload
   constexpr bool FOLDS = P::BM < Large::BM;  // may write second terms (product_tile keeps them from the large tile)
-  uint32_t row0, col0;
-  const Problem& p = a.p[locate<P>(a, &row0, &col0)];
+  uint32_t row0, col0, share;
+  const Problem& p = a.p[locate<P>(a, &row0, &col0, &share)];
   if constexpr (KIND == PK_GRADS) {
     if (p.mode & GRAD_TN) {
       store_tile<typename P::TN_>(p, a.scale ? *a.scale : 1.0f, row0, col0, smem);
@@ -98,7 +114,13 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
     }
   }
   P x;
-  x.run(p, row0, col0, smem);
+  x.run(p, share, row0, col0, smem);
+  if constexpr (KIND == PK_STORE_NT || KIND == PK_GRADS) {
+    if (p.shares > 1) {
+      store_share(x, p, share, row0, col0, smem);
+      return;
+    }
+  }
   const uint32_t m = p.m, n = p.n;
   const uint64_t ldc = p.ldc;
   const bool vec = p.ldc % V == 0;
@@ -293,18 +315,51 @@ __global__ __launch_bounds__(P::NT) void product_kernel(const ProductArgs a) {
 
 constexpr int layout_b(int kind) { return kind >= PK_GATED_BWD ? L_R : L_K; }
 
+// Adds the shares of the problems that have them, in order, and finishes as the
+// product kernel would have: times scale, plus the sum so far (GRAD_ADD), as the
+// result or as the sum (GRAD_PARTIAL).
+template <int DT>
+__global__ __launch_bounds__(256) void finish_kernel(const ProductArgs a, int32_t count) {
+  const float scale = a.scale ? *a.scale : 1.0f;
+  for (int q = 0; q < count; ++q) {
+    const Problem& p = a.p[q];
+    const uint64_t total = (uint64_t)(p.m - p.fold) * p.ldc;
+    for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < total; i += gridDim.x * 256ull) {
+      const float* part = (const float*)p.c[2] + i;
+      float v = 0.f;
+      for (uint32_t s = 0; s < p.shares; ++s) v += part[s * total];
+      v *= scale;
+      if (p.mode & GRAD_ADD) v = ((const float*)p.c[1])[i] + v;
+      if (p.mode & GRAD_PARTIAL) ((float*)p.c[1])[i] = v;
+      else if (DT == DT_BF16) ((uint16_t*)p.c[0])[i] = (uint16_t)bf16_round(v);
+      else ((float*)p.c[0])[i] = v;
+    }
+  }
+}
+
 template <int KIND, int DT, class TILE, uint32_t ACT>
 hipError_t launch(ProductPlan& plan, hipStream_t stream) {
   using P = Product<DT, L_K, layout_b(KIND), KIND == PK_GATED, TILE>;
   if (!plan.cut(P::BM, P::COLS)) return hipErrorInvalidValue;
   if (plan.tiles == 0) return hipSuccess;
   hipLaunchKernelGGL((product_kernel<P, KIND, ACT>), dim3((unsigned)plan.tiles), dim3(P::NT), 0, stream, plan.a);
-  return hipGetLastError();
+  const hipError_t e = hipGetLastError();
+  if constexpr (KIND == PK_STORE_NT || KIND == PK_GRADS) {
+    if (e == hipSuccess && plan.a.p[0].shares > 1) {
+      const uint64_t each = ((uint64_t)(plan.a.p[0].m - plan.a.p[0].fold) * plan.a.p[0].ldc + 255) / 256;
+      hipLaunchKernelGGL(finish_kernel<DT>, dim3((unsigned)(each < 1024 ? each : 1024)), dim3(256), 0, stream, plan.a,
+                         plan.sharing());
+      return hipGetLastError();
+    }
+  }
+  return e;
 }
 
 template <int KIND, int DT, uint32_t ACT = ACT_SILU>
 hipError_t launch_kind(ProductPlan& plan, int device, hipStream_t stream) {
-  const int tile = product_tile(KIND, DT, plan, device);
+  const TileChoice choice = product_tile(KIND, DT, plan, device);
+  const int tile = choice.tile;
+  for (int i = 0; i < plan.sharing(); ++i) plan.a.p[i].shares = choice.shares;
   if constexpr (DT == DT_BF16) {  // classes of one type only
     if (tile == TILE_LARGE) return launch<KIND, DT, Large, ACT>(plan, stream);
     if (tile == TILE_FLAT) return launch<KIND, DT, Flat, ACT>(plan, stream);

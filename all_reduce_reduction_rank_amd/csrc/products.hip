@@ -4,8 +4,9 @@
 // A launch takes the tile class with the smallest estimated time.  A
 // workgroup of class c takes fixed + steps x (alone | full) us, a step being
 // 128 bytes of k (of each wave's part of K): `alone` while its CU runs no
-// other and no round of workgroups is behind it, `full` with as many as fit.  Measured on bf16 products of 8 ranks
-// [m, 5120] x [1728 pairs, 5120] (80 steps) and [m, 1728] x [5120, 1728] (27):
+// other and no round of workgroups is behind it, `full` with as many as fit.
+// Measured on bf16 products of 8 ranks [m, 5120] x [1728 pairs, 5120] (80 steps)
+// and [m, 1728] x [5120, 1728] (27):
 //
 //   us            m = 64   128   256   512  1024 |   64   128   256   512  1024
 //   Large            143   150   172   171   302 |   51    55    60   111   162
@@ -16,6 +17,11 @@
 //
 // One small product, [512, 4096] x [1024, 4096]: 83, 50, 31, 16 us.  Thin is
 // for 16 rows at most: with more it reads the weights again for every 16.
+// A product with few tiles and a long K (a gradient summed over the vocabulary)
+// has 2 to 16 workgroups share each tile's K, where the shorter sums are worth a
+// second kernel that adds them: fp32 [11, 7522] x [7522, 314], 5 tiles of 64
+// columns, and its gradients 313 us unshared, 95 with 16 shares.
+//
 // fp32 runs 16 times as many instructions per byte, so its steps cost what
 // its matrix instructions do, and the choice is which tile fills the CUs most
 // evenly: two ranks of [1024, 1024] x [8000, 1024] 290 us in Small and 315 in
@@ -42,6 +48,9 @@ constexpr ClassCost COST[TILE_CLASSES] = {
     {Split::BM, Split::BN, Split::WK, 1, 4.5, 0.8, 1.6, 1.22},
     {Thin::BM, Thin::BN, Thin::WK, 2, 4.5, 0.25, 0.6, 1.22},
 };
+// Sharing a tile's K among workgroups: a second kernel, and the sums written
+// and read.
+constexpr double SHARE_US = 4.0, SHARE_BYTES_PER_US = 3e6;
 constexpr double F32_FLOPS_PER_CU_US = 0.55e6;  // of 0.61e6 (16x16x4 at 2.4 GHz)
 
 constexpr int PACK_THREADS = 256, PACK_CHUNKS = 4;  // chunks per thread
@@ -109,65 +118,74 @@ hipError_t Packer::launch(hipStream_t stream) const {
   return hipGetLastError();
 }
 
-int product_tile(int kind, int dtype, const ProductPlan& plan, int device) {
+TileChoice product_tile(int kind, int dtype, const ProductPlan& plan, int device) {
   int n_cu = 0;
   if (hipDeviceGetAttribute(&n_cu, hipDeviceAttributeMultiprocessorCount, device) != hipSuccess || n_cu < 1) n_cu = 256;
   const double cus = n_cu;
   const uint32_t half = kind == PK_GATED ? 2 : 1;
   const uint64_t per_step = dtype == DT_BF16 ? 64 : 32;  // k of 128 bytes
   const bool reads_terms = kind == PK_STORE_NT || kind == PK_GRADS;  // other kinds write them
+  const int sharing = plan.sharing();
   uint32_t max_m = 0, fold = 0;
+  double results = 0;  // values of the problems that may share
   for (int i = 0; i < plan.a.nprob; ++i) {
     const Problem& p = plan.a.p[i];
     max_m = p.m > max_m ? p.m : max_m;
     fold = p.fold > fold ? p.fold : fold;  // the same in all of a launch's problems
+    if (i < sharing) results += (double)(p.m - p.fold) * p.n;
   }
-  int best = TILE_SMALL;
+  TileChoice best = {TILE_SMALL, 1};
   double best_us = 1e30;
   for (int c = 0; c < TILE_CLASSES; ++c) {
+    const ClassCost& k = COST[c];
     if (c == TILE_TALL ? dtype == DT_BF16 : (c == TILE_LARGE || c == TILE_FLAT) && dtype != DT_BF16) continue;
     if (c == TILE_LARGE && fold) continue;
     if (c == TILE_THIN && max_m > (uint32_t)Thin::BM) continue;
-    const ClassCost& k = COST[c];
     if (fold && reads_terms && k.bm != 2 * fold) continue;
-    double tiles = 0, work = 0, longest = 0, shortest = 1e30;  // work: steps of all tiles
-    for (int i = 0; i < plan.a.nprob; ++i) {
-      const Problem& p = plan.a.p[i];
-      const double t = (double)((p.m + k.bm - 1) / k.bm) * (double)(((uint64_t)p.n * half + k.bn - 1) / k.bn);
-      if (t == 0) continue;
-      const uint64_t steps = (uint64_t)p.nseg * ((p.k + per_step - 1) / per_step);
-      const double s = (double)((steps + k.parts - 1) / k.parts);
-      tiles += t;
-      work += t * s;
-      longest = s > longest ? s : longest;
-      shortest = s < shortest ? s : shortest;
-    }
-    if (tiles == 0) continue;
-    const double slots = cus * k.resident;
-    const double rounds = (double)(uint64_t)(tiles / slots);
-    const double rest = tiles - rounds * slots;
-    double us;
-    if (dtype != DT_BF16) {
-      // matrix instructions: a CU works its tiles off one after the other,
-      // however many share it (`one`: a tile by itself, one wave per SIMD)
-      const double mm = k.f32 * 2.0 * k.bm * k.bn * per_step * k.parts / F32_FLOPS_PER_CU_US;
-      const double per = mm * k.resident > k.full ? mm : k.full / k.resident;
-      const double one = 1.2 * mm > k.alone ? 1.2 * mm : k.alone;
-      const double each = (double)(uint64_t)((tiles + cus - 1) / cus);
-      const double turns = (double)(uint64_t)((each + k.resident - 1) / k.resident);
-      const double busy = longest == shortest ? each * longest * per : (work / cus + 0.5 * shortest) * per;
-      us = turns * k.fixed + (busy > longest * one ? busy : longest * one);
-    } else if (rounds == 0) {
-      us = k.fixed + longest * (rest <= cus ? k.alone : k.full);
-    } else if (longest == shortest) {
-      us = rounds * (k.fixed + longest * k.full) +
-           (rest == 0 ? 0 : k.fixed + longest * (rest <= cus && k.resident > 1 ? k.alone : k.full));
-    } else {  // long tiles first
-      us = tiles / slots * k.fixed + (work / slots + 0.5 * shortest) * k.full;
-    }
-    if (us < best_us) {
-      best_us = us;
-      best = c;
+    if (plan.k_parts && k.parts != plan.k_parts) continue;
+    for (uint32_t shares = 1; shares <= (sharing ? MAX_SHARES : 1); shares *= 2) {
+      double tiles = 0, work = 0, longest = 0, shortest = 1e30;  // work: steps of all tiles
+      for (int i = 0; i < plan.a.nprob; ++i) {
+        const Problem& p = plan.a.p[i];
+        const uint32_t by = i < sharing ? shares : 1;
+        const double t = (double)((p.m + k.bm - 1) / k.bm) * (double)(((uint64_t)p.n * half + k.bn - 1) / k.bn) * by;
+        if (t == 0) continue;
+        const uint64_t steps = (uint64_t)p.nseg * ((p.k + per_step - 1) / per_step);
+        const double s = (double)((steps + k.parts * by - 1) / (k.parts * by));
+        tiles += t;
+        work += t * s;
+        longest = s > longest ? s : longest;
+        shortest = s < shortest ? s : shortest;
+      }
+      if (tiles == 0) continue;
+      const double slots = cus * k.resident;
+      const double rounds = (double)(uint64_t)(tiles / slots);
+      const double rest = tiles - rounds * slots;
+      double us;
+      if (dtype != DT_BF16) {
+        // matrix instructions: a CU works its tiles off one after the other,
+        // however many share it (`one`: a tile by itself, one wave per SIMD)
+        const double mm = k.f32 * 2.0 * k.bm * k.bn * per_step * k.parts / F32_FLOPS_PER_CU_US;
+        const double per = mm * k.resident > k.full ? mm : k.full / k.resident;
+        const double one = 1.2 * mm > k.alone ? 1.2 * mm : k.alone;
+        const double each = (double)(uint64_t)((tiles + cus - 1) / cus);
+        const double turns = (double)(uint64_t)((each + k.resident - 1) / k.resident);
+        const double busy = longest == shortest ? each * longest * per : (work / cus + 0.5 * shortest) * per;
+        us = turns * k.fixed + (busy > longest * one ? busy : longest * one);
+      } else if (rounds == 0) {
+        us = k.fixed + longest * (rest <= cus ? k.alone : k.full);
+      } else if (longest == shortest) {
+        us = rounds * (k.fixed + longest * k.full) +
+             (rest == 0 ? 0 : k.fixed + longest * (rest <= cus && k.resident > 1 ? k.alone : k.full));
+      } else {  // long tiles first, and none longer than the whole
+        const double all = (work / slots + 0.5 * shortest) * k.full;
+        us = tiles / slots * k.fixed + (all > longest * k.full ? all : longest * k.full);
+      }
+      if (shares > 1) us += SHARE_US + shares * results * 8 / SHARE_BYTES_PER_US;
+      if (us < best_us) {
+        best_us = us;
+        best = {c, shares};
+      }
     }
   }
   return best;
@@ -176,6 +194,7 @@ int product_tile(int kind, int dtype, const ProductPlan& plan, int device) {
 hipError_t launch_grads(int dtype, ProductPlan& plan, int device, hipStream_t stream) {
   if (plan.head == 0 || plan.a.p[0].fold == 0) return launch_products(PK_GRADS, dtype, plan, device, stream);
   ProductPlan rest = plan;
+  rest.may_share = false;
   rest.a.nprob = plan.a.nprob - plan.head;
   rest.head = 0;
   for (int i = 0; i < rest.a.nprob; ++i) rest.a.p[i] = plan.a.p[plan.head + i];

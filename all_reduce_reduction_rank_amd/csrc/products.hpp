@@ -39,6 +39,12 @@ __device__ __forceinline__ float2 merge_stats(float2 x, float2 y) {
   return make_float2(top, x.y * expf(stats_shift(x.x) - shift) + y.y * expf(stats_shift(y.x) - shift));
 }
 
+// Bytes of c[2] for MAX_SHARES blocks of every rank's [rows, cols] result; 0 where
+// the result has tiles enough by itself (128 of 64 x 128) and is not shared.
+constexpr uint64_t share_bytes(int n, uint64_t rows, uint64_t cols) {
+  return (uint64_t)n * rows * cols <= 128ull * 64 * 128 ? (MAX_SHARES * rows * cols * 4 + 255) & ~255ull : 0;
+}
+
 // Rows down to a bf16 intermediate's second terms (Problem::fold): half the rows
 // of the tile that will read it, or 0 where the intermediate keeps one term.
 // With up to 32 rows the second terms cost next to nothing (they fill rows of
@@ -54,7 +60,11 @@ constexpr uint32_t fold_of(uint64_t rows, int dtype) {
 
 // Tile class that a launch of this plan takes (its problems are final).
 enum TileClass : int { TILE_LARGE = 0, TILE_SMALL, TILE_TALL, TILE_FLAT, TILE_SPLIT, TILE_THIN, TILE_CLASSES };
-int product_tile(int kind, int dtype, const ProductPlan& plan, int device);
+struct TileChoice {
+  int tile;
+  uint32_t shares;  // workgroups per tile's K, of the problems that may share
+};
+TileChoice product_tile(int kind, int dtype, const ProductPlan& plan, int device);
 // Columns of C a tile of a class that is not paired covers: PK_STATS writes
 // one partial per row and that many columns.
 constexpr uint32_t tile_cols(int tile) {
@@ -62,6 +72,8 @@ constexpr uint32_t tile_cols(int tile) {
   return cols[tile];
 }
 constexpr uint32_t MIN_TILE_COLS = Thin::BN;
+// Order in which a class adds up K (ProductPlan::k_parts).
+constexpr uint32_t tile_k_parts(int tile) { return tile == TILE_SPLIT ? Split::WK : tile == TILE_THIN ? Thin::WK : 1; }
 
 // Products read rows that start on 16-byte boundaries.  A matrix whose rows do
 // not (an odd width) is copied into the workspace once per call, its rows

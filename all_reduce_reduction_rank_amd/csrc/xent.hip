@@ -153,14 +153,16 @@ uint64_t piece_of(const XentShape& s, int n, size_t piece) {
 struct BackwardSpace {
   uint64_t piece, d_bytes, acc_bytes;  // per rank
   uint32_t fold;                       // d: rows down to its second terms, 0: none
+  uint64_t share;                      // dx's shares
   uint64_t scale_bytes;                // the scale of d, of all ranks
-  uint64_t bytes(int n) const { return (uint64_t)n * (d_bytes + acc_bytes) + scale_bytes; }
+  uint64_t bytes(int n) const { return (uint64_t)n * (d_bytes + acc_bytes + share) + scale_bytes; }
 };
 BackwardSpace space_of(const XentShape& s, int n, int dtype, size_t piece) {
   BackwardSpace b;
   b.piece = piece_of(s, n, piece);
   b.fold = fold_of(s.rows, dtype);
   b.d_bytes = layer_align((b.fold + s.rows) * b.piece * s.es);
+  b.share = share_bytes(n, s.rows, s.hidden);
   b.scale_bytes = dtype == DT_BF16 && !b.fold ? layer_align(sizeof(float)) : 0;
   // fp32 gradients add up in dx itself
   b.acc_bytes = dtype == DT_BF16 && b.piece < s.max_shard ? layer_align(s.rows * s.hidden * 4) : 0;
@@ -225,7 +227,7 @@ ar_status ar_linear_cross_entropy(int nranks, const void* const* x, const void* 
     p->c[1] = ws;
     p->col0 = s.start[r];
   }
-  const uint64_t cols = tile_cols(product_tile(PK_STATS, (int)dtype, plan, dev));
+  const uint64_t cols = tile_cols(product_tile(PK_STATS, (int)dtype, plan, dev).tile);
   for (int r = 0; r < nranks; ++r) c.tiles[r] = (uint32_t)((s.shard[r] + cols - 1) / cols);
   c.max_tiles = c.tiles[0];  // the first shard is the longest
   c.at = (const float*)ws;
@@ -278,6 +280,16 @@ ar_status ar_linear_cross_entropy_backward(int nranks, const float* grad_loss, c
     pw[r] = pack.rows(w[r], rows ? s.shard[r] : 0, s.hidden);
   }
   if (pack.launch((hipStream_t)stream) != hipSuccess) return AR_ERR_HIP;
+  // The logits are the forward pass's bits again: their sums run in the order
+  // that pass's tile class takes (else lse and the logits differ in their
+  // roundings, which d of a confident row, 1 - p, does not forgive).
+  uint32_t k_parts = 0;
+  if (rows) {
+    ProductPlan plan;
+    for (int r = 0; r < nranks; ++r)
+      if (s.shard[r]) plan.add(s.rows, s.shard[r], s.hidden, px[r].ld, pw[r].ld, 0);
+    k_parts = tile_k_parts(product_tile(PK_STATS, (int)dtype, plan, dev).tile);
+  }
   const float* scale = nullptr;
   if (rows && sp.scale_bytes) {
     float* out = (float*)(ws + sp.bytes(nranks) - sp.scale_bytes);
@@ -293,6 +305,8 @@ ar_status ar_linear_cross_entropy_backward(int nranks, const float* grad_loss, c
     d_plan.a.grad = grad_loss;
     d_plan.a.vocab = s.vocab;
     d_plan.a.scale = grads.a.scale = scale;
+    d_plan.k_parts = k_parts;
+    grads.may_share = sp.share != 0;
     for (int r = 0; r < nranks; ++r) {
       // a rank without vocabulary still writes dx: a product with k = 0
       if (first >= umax(s.shard[r], 1)) continue;
@@ -315,6 +329,7 @@ ar_status ar_linear_cross_entropy_backward(int nranks, const float* grad_loss, c
       p->b[0] = wp;
       p->c[0] = (char*)dx[r];
       p->c[1] = sp.acc_bytes ? ws + (uint64_t)nranks * sp.d_bytes + (uint64_t)r * sp.acc_bytes : (char*)dx[r];
+      p->c[2] = ws + (uint64_t)nranks * (sp.d_bytes + sp.acc_bytes) + (uint64_t)r * sp.share;
       p->mode = (i ? GRAD_ADD : 0) | (first + len < s.shard[r] ? GRAD_PARTIAL : 0);
     }
     grads.head = grads.a.nprob;

@@ -1,6 +1,6 @@
-// Prints the tile class product_tile takes for each product named on standard
-// input, one per line: kind dtype head nprob, then m n k nseg fold mode of every
-// problem.
+// Prints the tile class product_tile takes, and the workgroups that share a
+// tile's K, for each product named on standard input, one per line: kind dtype
+// head may_share k_parts nprob, then m n k nseg fold mode of every problem.
 #include <stdio.h>
 
 #include "../all_reduce_reduction_rank_amd/csrc/products.hpp"
@@ -11,10 +11,12 @@ hipError_t launch_products_f32(int, ProductPlan&, int, hipStream_t) { return hip
 }  // namespace ar
 
 int main() {
-  int kind, dtype, head, nprob;
-  while (scanf("%d %d %d %d", &kind, &dtype, &head, &nprob) == 4) {
+  int kind, dtype, head, share, parts, nprob;
+  while (scanf("%d %d %d %d %d %d", &kind, &dtype, &head, &share, &parts, &nprob) == 6) {
     ar::ProductPlan plan;
     plan.head = head;
+    plan.may_share = share != 0;
+    plan.k_parts = (uint32_t)parts;
     for (int i = 0; i < nprob; ++i) {
       unsigned long long m, n, k;
       unsigned nseg, fold, mode;
@@ -24,7 +26,8 @@ int main() {
       p->fold = fold;
       p->mode = mode;
     }
-    printf("%d\n", ar::product_tile(kind, dtype, plan, 0));
+    const ar::TileChoice c = ar::product_tile(kind, dtype, plan, 0);
+    printf("%d %u\n", c.tile, c.shares);
   }
   return 0;
 }

@@ -122,6 +122,16 @@ def test_ffn_tile_classes(n, rows, hidden, inter, dt):
     run_ffn(n, rows, hidden, inter, dt, "silu", seed=rows, ranks=(0, n - 1))
 
 
+# Few results and a long K: several workgroups share each tile's sum.
+FFN_SHARED_SHAPES = [(1, 11, 40, 7522), (2, 5, 33, 8000), (1, 40, 72, 6001), (1, 130, 64, 9000), (2, 30, 100, 4100)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n,rows,hidden,inter", FFN_SHARED_SHAPES)
+def test_ffn_shared_sums(n, rows, hidden, inter, dt):
+    run_ffn(n, rows, hidden, inter, dt, "silu", seed=rows)
+
+
 def xent_inputs(n, rows, hidden, vocab, dt, seed, ignored=0.2):
     gen = torch.Generator().manual_seed(seed)
     x = _rand(gen, (rows, hidden), dt)
@@ -173,6 +183,31 @@ def test_xent_shapes(n, rows, hidden, vocab, dt):
 def test_xent_in_pieces(n, vocab, dt):
     # several pieces, the last one short; ranks with fewer pieces than others
     run_xent(n, 70, 96, vocab, dt, piece=256, seed=vocab)
+
+
+# ranks, rows, hidden, vocab: few results of dx, summed over many columns
+XENT_SHARED_SHAPES = [(1, 20, 72, 9000), (2, 7, 100, 20011), (1, 40, 136, 30000), (2, 150, 72, 24000)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("piece", [0, 7000])
+@pytest.mark.parametrize("n,rows,hidden,vocab", XENT_SHARED_SHAPES)
+def test_xent_shared_sums(n, rows, hidden, vocab, piece, dt):
+    run_xent(n, rows, hidden, vocab, dt, piece=piece, seed=vocab)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_xent_logits_are_the_same_bits_in_every_piece(dt):
+    # with one row that counts, dw is that row's d times x whatever the order of
+    # the sum over the rows: its bits are those of the recomputed logits
+    rows, hidden, vocab = 40, 136, 30000
+    x, w, target, grad = xent_inputs(1, rows, hidden, vocab, dt, 4, ignored=0.0)
+    grad *= (torch.arange(rows) == 23).cuda()
+    _, lse = ar.linear_cross_entropy(x, w, target)
+    _, whole = ar.linear_cross_entropy_backward(grad, x, w, target, lse)
+    for piece in (64, 1000, 9999):
+        _, dw = ar.linear_cross_entropy_backward(grad, x, w, target, lse, piece=piece)
+        assert torch.equal(dw[0], whole[0]), piece
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])

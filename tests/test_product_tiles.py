@@ -9,7 +9,7 @@ import subprocess
 import pytest
 
 from all_reduce_reduction_rank_amd import vocab_shards
-from tests.test_gpu_layer import FFN_CLASS_SHAPES, FFN_SHAPES, XENT_SHAPES
+from tests.test_gpu_layer import FFN_CLASS_SHAPES, FFN_SHAPES, FFN_SHARED_SHAPES, XENT_SHAPES, XENT_SHARED_SHAPES
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "all_reduce_reduction_rank_amd", "csrc")
@@ -28,14 +28,32 @@ def classes(tmp_path_factory):
                           os.path.join(CSRC, "products.hip"), "-o", exe], capture_output=True, text=True)
     assert res.returncode == 0, res.stderr
 
-    def run(plans):
-        text = "\n".join(f"{KINDS.index(kind)} {DT[dt]} {head} {len(probs)} " +
-                         " ".join(" ".join(map(str, p)) for p in probs) for kind, dt, head, probs in plans)
+    def choose(plans):
+        text = "\n".join(f"{KINDS.index(kind)} {DT[dt]} {head} {_may_share(kind, head, probs):d} {parts} {len(probs)} " +
+                         " ".join(" ".join(map(str, p)) for p in probs) for (kind, dt, head, probs), parts in plans)
         out = subprocess.run([exe], input=text, capture_output=True, text=True, timeout=60)
         assert out.returncode == 0
-        return [CLASSES[int(x)] for x in out.stdout.split()]
+        got = [line.split() for line in out.stdout.splitlines()]
+        return [(CLASSES[int(tile)], int(shares)) for tile, shares in got]
+
+    def run(plans, shares=False):
+        """The classes (and shares) of a list of plans; a dlogits plan follows
+        its stats plan and adds up K in the same order."""
+        got = choose([(p, 0) for p in plans])
+        for i, p in enumerate(plans):
+            if p[0] == "dlogits":
+                got[i] = choose([(p, 4 if got[i - 1][0] in ("split", "thin") else 1)])[0]
+        return got if shares else [tile for tile, _ in got]
 
     return run
+
+
+def _may_share(kind, head, probs):
+    """Results of the first launch's problems small enough for shares of K."""
+    first = probs[:head] if head else probs
+    if not (kind == "store" or kind == "grads" and first[0][5] != GRAD_TN):
+        return False
+    return sum((m - fold) * n for m, n, _, _, fold, _ in first) <= 128 * 64 * 128
 
 
 def _fold(rows, dt):
@@ -81,6 +99,27 @@ def test_gpu_tests_reach_every_class_of_every_kernel(classes):
     seen = {(p[0], p[1], c) for p, c in zip(plans, classes(plans))}
     missing = {(k, dt, c) for k in KINDS for dt in DT for c in CLASSES if ONLY.get(c, dt) == dt} - seen
     assert not missing, sorted(missing)
+
+
+def test_gpu_tests_share_sums(classes):
+    for dt in ("bf16", "f32"):
+        for shape in FFN_SHARED_SHAPES:
+            got = classes(ffn_plans(*shape, dt), shares=True)
+            assert got[1][1] > 1 and got[3][1] > 1, (dt, shape, got)
+            assert all(n == 1 for i, (_, n) in enumerate(got) if i not in (1, 3)), (dt, shape, got)
+        for shape in XENT_SHARED_SHAPES:
+            got = classes(xent_plans(*shape, dt), shares=True)
+            assert got[2][1] > 1 and all(n == 1 for i, (_, n) in enumerate(got) if i != 2), (dt, shape, got)
+
+
+def test_recomputed_logits_are_summed_in_the_order_of_the_forward_pass(classes):
+    def order(tile):
+        return tile in ("split", "thin")
+
+    for dt in ("bf16", "f32"):
+        for shape in [*XENT_SHAPES, *XENT_SHARED_SHAPES]:
+            got = classes(xent_plans(*shape, dt))
+            assert order(got[0]) == order(got[1]), (dt, shape, got)
 
 
 def test_choices_at_both_ends(classes):
