@@ -80,7 +80,7 @@ constexpr uint32_t tile_k_parts(int tile) { return tile == TILE_SPLIT ? Split::W
 // padded with zeros to whole 16-byte chunks.  Measured against reading such
 // rows in place through registers, element by element at their ends: the
 // copies cost less than the products gain (cross entropy step of 611 rows,
-// width 1003, vocabulary 10007 over 3 ranks, bf16: 290 -> 131 us).
+// width 1003, vocabulary 10007 over 3 ranks, bf16: 288 -> 170 us).
 class Packer {
  public:
   struct Rows {
