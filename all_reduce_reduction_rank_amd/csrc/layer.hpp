@@ -18,11 +18,11 @@ constexpr uint64_t LAYER_MAX_ROWS = 1ull << 30;
 inline uint64_t layer_align(uint64_t x) { return (x + 255) & ~255ull; }
 
 // The device buffers of one call: every one of nonzero size must be non-null
-// and 16-byte aligned, and no output may overlap any other buffer.
+// and aligned (matrices to 16 bytes, vectors to an element), and no output may overlap any other buffer.
 class LayerBuffers {
  public:
-  void in(const void* p, uint64_t bytes) { add(p, bytes, false); }
-  void out(const void* p, uint64_t bytes) { add(p, bytes, true); }
+  void in(const void* p, uint64_t bytes, uint32_t align = 16) { add(p, bytes, align, false); }
+  void out(const void* p, uint64_t bytes, uint32_t align = 16) { add(p, bytes, align, true); }
   bool ok() {
     if (bad_) return false;
     std::sort(s_, s_ + n_, [](const Span& a, const Span& b) { return a.at < b.at; });
@@ -44,9 +44,9 @@ class LayerBuffers {
     uint64_t bytes;
     bool out;
   };
-  void add(const void* p, uint64_t bytes, bool out) {
+  void add(const void* p, uint64_t bytes, uint32_t align, bool out) {
     if (!bytes) return;
-    if (!p || ((uintptr_t)p & 15) || n_ == MAX_SPANS) bad_ = true;
+    if (!p || (uintptr_t)p % align || n_ == MAX_SPANS) bad_ = true;
     else s_[n_++] = {(uintptr_t)p, bytes, out};
   }
   static constexpr int MAX_SPANS = 12 * MAX_RANKS + 8;

@@ -75,7 +75,9 @@ __global__ __launch_bounds__(PACK_THREADS) void pack_kernel(Packer::Args a) {
     const uint32_t col = (uint32_t)(t % e.chunks) * per;
     const char* src = e.src + (row * e.cols + col) * a.es;
     v4u v = {0, 0, 0, 0};
-    if (col + per <= e.cols) {
+    const int64_t target = e.live ? a.target[row] : 0;
+    if (e.live && (target < 0 || (uint64_t)target >= a.vocab)) {
+    } else if (col + per <= e.cols) {
       v = *(const v4u_any*)src;
     } else if (a.es == 2) {
 #pragma unroll
@@ -94,18 +96,30 @@ __global__ __launch_bounds__(PACK_THREADS) void pack_kernel(Packer::Args a) {
 
 Packer::Rows Packer::rows(const void* src, uint64_t rows, uint64_t cols) {
   if ((cols * es_) % 16 == 0 || rows == 0) return {(const char*)src, pitch(cols, es_)};
+  return copy(src, rows, cols, 0);
+}
+
+Packer::Rows Packer::live_rows(const void* src, uint64_t rows, uint64_t cols, const int64_t* target, uint64_t vocab) {
+  if (rows == 0) return {(const char*)src, pitch(cols, es_)};
+  a_.target = target;
+  a_.vocab = vocab;
+  return copy(src, rows, cols, 1);
+}
+
+Packer::Rows Packer::copy(const void* src, uint64_t rows, uint64_t cols, uint32_t live) {
   for (int i = 0; i < a_.n; ++i)  // the same matrix on several ranks
-    if (a_.e[i].src == (const char*)src && a_.e[i].rows == rows && a_.e[i].cols == cols)
+    if (a_.e[i].src == (const char*)src && a_.e[i].rows == rows && a_.e[i].cols == cols && a_.e[i].live == live)
       return {a_.e[i].dst, pitch(cols, es_)};
   Entry& e = a_.e[a_.n++];
   e.src = (const char*)src;
   e.dst = space_;
   e.rows = rows;
   e.cols = (uint32_t)cols;
+  e.live = live;
   e.chunks = (uint32_t)(pitch(cols, es_) * es_ / 16);
   e.first = (uint32_t)blocks_;
   blocks_ += (rows * e.chunks + PACK_THREADS * PACK_CHUNKS - 1) / (PACK_THREADS * PACK_CHUNKS);
-  space_ += bytes(rows, cols, es_);
+  space_ += copy_bytes(rows, cols, es_);
   return {e.dst, pitch(cols, es_)};
 }
 

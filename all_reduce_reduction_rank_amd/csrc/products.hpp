@@ -89,13 +89,19 @@ class Packer {
   };
   // Bytes of the copy of a [rows, cols] matrix; 0 if none is needed.
   static uint64_t bytes(uint64_t rows, uint64_t cols, uint64_t es) {
-    return (cols * es) % 16 ? (rows * pitch(cols, es) * es + 255) & ~255ull : 0;
+    return (cols * es) % 16 ? copy_bytes(rows, cols, es) : 0;
+  }
+  static uint64_t copy_bytes(uint64_t rows, uint64_t cols, uint64_t es) {
+    return (rows * pitch(cols, es) * es + 255) & ~255ull;
   }
   static uint64_t pitch(uint64_t cols, uint64_t es) { return (cols * es + 15) / 16 * 16 / es; }
 
   Packer(char* space, uint64_t es) : space_(space), es_(es) {}
   // A row-major [rows, cols] matrix without gaps, or its copy to be.
   Rows rows(const void* src, uint64_t rows, uint64_t cols);
+  // The copy of a [rows, cols] matrix with zeros in the rows whose target is
+  // outside [0, vocab).
+  Rows live_rows(const void* src, uint64_t rows, uint64_t cols, const int64_t* target, uint64_t vocab);
   // Make the copies (one kernel, or none).
   hipError_t launch(hipStream_t stream) const;
 
@@ -106,13 +112,18 @@ class Packer {
     uint64_t rows;
     uint32_t cols, chunks;  // elements, 16-byte chunks of a row
     uint32_t first;         // first workgroup
+    uint32_t live;          // only rows with a target are copied
   };
   struct Args {
     Entry e[MAX];
+    const int64_t* target;
+    uint64_t vocab;
     int32_t n, es;
   };
 
  private:
+  Rows copy(const void* src, uint64_t rows, uint64_t cols, uint32_t live);
+
   char* space_;
   uint64_t es_;
   Args a_ = {};

@@ -114,6 +114,7 @@ struct XentShape {
   uint64_t shard[MAX_RANKS], start[MAX_RANKS], max_shard;
   uint64_t part_tiles;  // partials per row and rank, at the smallest tile
   uint64_t pack_bytes;  // copies of every rank's x and w, where their rows are not whole 16-byte chunks
+  uint64_t live_bytes;  // the same with x copied always
 };
 
 XentShape shape_of(int n, size_t rows, size_t hidden, size_t vocab, int dtype) {
@@ -127,9 +128,12 @@ XentShape shape_of(int n, size_t rows, size_t hidden, size_t vocab, int dtype) {
   }
   s.max_shard = b;
   s.part_tiles = (b + MIN_TILE_COLS - 1) / MIN_TILE_COLS;
-  s.pack_bytes = 0;
-  for (int r = 0; r < n; ++r)
-    s.pack_bytes += Packer::bytes(s.rows, s.hidden, s.es) + Packer::bytes(s.shard[r], s.hidden, s.es);
+  s.pack_bytes = s.live_bytes = 0;
+  for (int r = 0; r < n; ++r) {
+    const uint64_t w = Packer::bytes(s.shard[r], s.hidden, s.es);
+    s.pack_bytes += Packer::bytes(s.rows, s.hidden, s.es) + w;
+    s.live_bytes += Packer::copy_bytes(s.rows, s.hidden, s.es) + w;
+  }
   return s;
 }
 
@@ -179,7 +183,7 @@ size_t ar_linear_cross_entropy_workspace(int nranks, size_t rows, size_t hidden,
   const XentShape s = shape_of(nranks, rows, hidden, vocab, (int)dtype);
   if (backward) {
     const BackwardSpace b = space_of(s, nranks, (int)dtype, piece);
-    return (size_t)(b.bytes(nranks) + s.pack_bytes);
+    return (size_t)(b.bytes(nranks) + s.live_bytes);
   }
   return (size_t)(layer_align(s.rows * 4) + (uint64_t)nranks * layer_align(s.part_tiles * s.rows * 8) + s.pack_bytes);
 }
@@ -198,10 +202,10 @@ ar_status ar_linear_cross_entropy(int nranks, const void* const* x, const void* 
   for (int r = 0; r < nranks; ++r) {
     b.in(x[r], s.rows * s.hidden * s.es);
     b.in(w[r], s.shard[r] * s.hidden * s.es);
-    b.out(loss[r], s.rows * 4);
-    b.out(lse[r], s.rows * 4);
+    b.out(loss[r], s.rows * 4, 4);
+    b.out(lse[r], s.rows * 4, 4);
   }
-  b.in(target, s.rows * 8);
+  b.in(target, s.rows * 8, 8);
   b.out(workspace, need);
   if (!b.ok()) return AR_ERR_INVALID;
   if (workspace_bytes < need) return AR_ERR_TOO_LARGE;
@@ -254,18 +258,18 @@ ar_status ar_linear_cross_entropy_backward(int nranks, const float* grad_loss, c
   if (!x || !w || !lse || !dx || !dw) return AR_ERR_INVALID;
   const XentShape s = shape_of(nranks, rows, hidden, vocab, (int)dtype);
   const BackwardSpace sp = space_of(s, nranks, (int)dtype, piece);
-  const uint64_t need = rows ? sp.bytes(nranks) + s.pack_bytes : 0;
+  const uint64_t need = rows ? sp.bytes(nranks) + s.live_bytes : 0;
   const uint64_t xb = s.rows * s.hidden * s.es;
   LayerBuffers b;
   for (int r = 0; r < nranks; ++r) {
     b.in(x[r], xb);
     b.in(w[r], s.shard[r] * s.hidden * s.es);
-    b.in(lse[r], s.rows * 4);
+    b.in(lse[r], s.rows * 4, 4);
     b.out(dx[r], xb);
     b.out(dw[r], s.shard[r] * s.hidden * s.es);
   }
-  b.in(target, s.rows * 8);
-  b.in(grad_loss, s.rows * 4);
+  b.in(target, s.rows * 8, 8);
+  b.in(grad_loss, s.rows * 4, 4);
   b.out(workspace, need);
   if (!b.ok()) return AR_ERR_INVALID;
   if (workspace_bytes < need) return AR_ERR_TOO_LARGE;
@@ -275,8 +279,11 @@ ar_status ar_linear_cross_entropy_backward(int nranks, const float* grad_loss, c
   const uint64_t pieces = (s.max_shard + sp.piece - 1) / sp.piece;
   Packer pack(ws + sp.bytes(nranks), s.es);
   Packer::Rows px[MAX_RANKS], pw[MAX_RANKS];
+  // x is a sum's operand over the rows (dw): a row without loss has weight 0 there,
+  // but 0 times what a padding row may hold (infinities, NaN) is not 0.  x is
+  // read from a copy that has zeros in those rows.
   for (int r = 0; r < nranks; ++r) {  // (with no rows nothing is read, and nothing copied)
-    px[r] = pack.rows(x[r], s.rows, s.hidden);
+    px[r] = pack.live_rows(x[r], s.rows, s.hidden, target, s.vocab);
     pw[r] = pack.rows(w[r], rows ? s.shard[r] : 0, s.hidden);
   }
   if (pack.launch((hipStream_t)stream) != hipSuccess) return AR_ERR_HIP;

@@ -348,7 +348,8 @@ ar_status ar_stream_ceiling(int nread, const void* const* src, int nwrite, void*
  * all-reduce adds, twice per layer and once more for each gradient).  They
  * make the partial sums the collectives above add.  Like the collectives they
  * take HOST arrays of N (1..8) DEVICE pointers, one per simulated rank, 16-byte
- * aligned and row-major without gaps, run every rank's program on the current
+ * aligned (the vectors target, grad_loss, loss and lse: to their elements) and
+ * row-major without gaps, run every rank's program on the current
  * HIP device in order on `stream`, and allocate nothing: scratch memory is the
  * caller's `workspace` (a 16-byte aligned DEVICE buffer of at least the bytes
  * the matching *_workspace function returns; its contents need not be kept
@@ -429,7 +430,8 @@ ar_status ar_linear_cross_entropy(int nranks, const void* const* x, const void* 
  * (rows) shared by all ranks, the gradient of each row's loss; lse[r]: what
  * the forward pass stored.
  *   d[i][v] = (exp(l[i][v] - lse[i]) - (v == target[i])) * grad_loss[i],
- *   0 in rows without loss (grad_loss is not looked at there)
+ *   0 in rows without loss (grad_loss, lse and x are not looked at there, and
+ *   may hold anything)
  *   dx[r] = d_r w[r]  [rows, hidden];  dw[r] = d_r^T x[r]  [shard, hidden]
  * where d_r is rank r's columns of d.  dx[r] is rank r's partial sum (an
  * all-reduce completes it); every output is overwritten.  The logits are
@@ -437,8 +439,9 @@ ar_status ar_linear_cross_entropy(int nranks, const void* const* x, const void* 
  * of 256 after rounding down, at least 256; 0: as many as keep d of all ranks
  * within 1 GiB).  dx is added up in fp32 and rounded once.  AR_BF16: d over
  * the largest finite |grad_loss| is rounded to bf16 before it is multiplied
- * (with up to 32 rows d is kept in two bf16 terms instead).  `piece` does not
- * change dw.  rows 0: dw becomes zeros. */
+ * (with up to 32 rows d is kept in two bf16 terms instead).  `piece`
+ * changes no term of dw (the order of its sums over the rows may differ).
+ * rows 0: dw becomes zeros. */
 ar_status ar_linear_cross_entropy_backward(int nranks, const float* grad_loss, const void* const* x,
                                            const void* const* w, const int64_t* target, const float* const* lse,
                                            void* const* dx, void* const* dw, size_t rows, size_t hidden, size_t vocab,

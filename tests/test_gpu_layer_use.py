@@ -271,6 +271,46 @@ def test_non_finite_values_stay_in_their_rows():
         assert torch.isnan(dx2[r][4]).all() and not dx2[r][11].any()
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n,rows,hidden,vocab", [(2, 5, 64, 300), (3, 150, 63, 400), (1, 300, 128, 2000), (2, 20, 72, 9001)])
+def test_rows_without_loss_may_hold_anything(n, rows, hidden, vocab, dt):
+    xs, w, target, grad = xent_inputs(n, rows, hidden, vocab, dt, 63, ignored=0.0)
+    target[1::3] = torch.tensor([-100, vocab, -1, 2 ** 40], device="cuda").repeat(rows)[: len(target[1::3])]
+    dead = (target < 0) | (target >= vocab)
+    loss, lse = ar.linear_cross_entropy(xs, w, target)
+    want = ar.linear_cross_entropy_backward(grad, xs, w, target, lse)
+    before = [t.clone() for t in xs]
+    for i, t in enumerate(xs):
+        t[dead] = (float("nan"), float("inf"), float("-inf"))[i % 3]
+    grad[dead] = float("nan")
+    l2, z2 = ar.linear_cross_entropy(xs, w, target)
+    got = ar.linear_cross_entropy_backward(grad, xs, w, target, z2)
+    for r in range(n):
+        assert torch.equal(l2[r], loss[r]) and not l2[r][dead].any()
+        assert torch.equal(got[0][r], want[0][r]) and not got[0][r][dead].any()
+        assert torch.equal(got[1][r], want[1][r])
+        assert torch.equal(xs[r][~dead], before[r][~dead])
+
+
+def test_vectors_at_any_element():
+    # the next token's targets are ids[1:]
+    n, rows, hidden, vocab = 2, 70, 64, 500
+    xs, w, target, grad = xent_inputs(n, rows, hidden, vocab, "bf16", 64)
+    loss, lse = ar.linear_cross_entropy(xs, w, target)
+    want = ar.linear_cross_entropy_backward(grad, xs, w, target, lse)
+
+    def at_one(t):
+        return torch.cat([t[:1], t])[1:]
+
+    l2, z2 = ([torch.full((rows + 2,), 7.0, device="cuda") for _ in range(n)] for _ in range(2))
+    ar.linear_cross_entropy(xs, w, at_one(target), loss=[t[1:-1] for t in l2], lse=[t[1:-1] for t in z2])
+    got = ar.linear_cross_entropy_backward(at_one(grad), xs, w, at_one(target), [t[1:-1] for t in z2])
+    for r in range(n):
+        assert torch.equal(l2[r][1:-1], loss[r]) and torch.equal(z2[r][1:-1], lse[r])
+        assert all(t[0] == 7 and t[-1] == 7 for t in (l2[r], z2[r]))
+        assert torch.equal(got[0][r], want[0][r]) and torch.equal(got[1][r], want[1][r])
+
+
 @pytest.mark.parametrize("scale", [2.0 ** -20, 1.0, 2.0 ** 20])
 def test_gradients_scale_with_grad_loss(scale):
     # powers of two move every value alike: the results are the same bits moved

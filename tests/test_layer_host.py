@@ -203,6 +203,7 @@ def test_c_abi_cross_entropy_argument_errors():
     assert fwd(n=0) == 1 and fwd(vocab=0) == 1 and fwd(hidden=0) == 1 and fwd(dtype=2) == 2 and fwd(target=0) == 1
     assert fwd(vocab=(1 << 30) + 1) == 4
     assert fwd(ws_bytes=LIB.ar_linear_cross_entropy_workspace(3, 4, 16, 100, 1, 0, 0) - 1) == 4
+    assert fwd(target=(7 << 40) + 8) == 5 and fwd(target=(7 << 40) + 4) == 1   # vectors: at their elements
     # ranks past the vocabulary need no buffer, ranks within it do
     assert fwd(n=8, vocab=2, w=P8(2 << 40, 9 << 40, *[0] * 6)) == 5
     assert fwd(n=8, vocab=3, w=P8(2 << 40, 9 << 40, *[0] * 6)) == 1
@@ -225,11 +226,12 @@ def test_workspace_sizes():
     odd = ws(1, 128, 33, 9, 1, 0)
     assert odd >= 128 * 16 * 2 + 128 * 40 * 2 + 2 * 9 * 40 * 2 + 33 * 16 * 2
     xe = LIB.ar_linear_cross_entropy_workspace
-    # the pieces cap what backward needs: d of all ranks within 1 GiB
+    # the pieces cap what backward needs: d of all ranks within 1 GiB, dx's fp32
+    # sum and the copy of x
     whole = xe(1, 8192, 1024, 131072, 1, 1, 0)
-    assert whole < (1 << 30) + 8192 * 1024 * 4 + 4096
+    assert whole < (1 << 30) + 8192 * 1024 * (4 + 2) + 4096
     small = xe(1, 8192, 1024, 131072, 1, 1, 256)
-    assert small < 8192 * (256 * 2 + 1024 * 4) + 4096
+    assert small < 8192 * (256 * 2 + 1024 * (4 + 2)) + 4096
     # every piece a caller may name fits the bytes named for it
     for piece in (0, 1, 255, 256, 300, 1000, 1 << 30):
         assert xe(2, 100, 64, 1001, 0, 1, piece) > 0
