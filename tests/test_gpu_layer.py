@@ -132,6 +132,16 @@ def test_ffn_shared_sums(n, rows, hidden, inter, dt):
     run_ffn(n, rows, hidden, inter, dt, "silu", seed=rows)
 
 
+# ... in other tile classes, the large one among them.
+FFN_SHARED_CLASSES = [(2, 990, 528, 9524), (8, 500, 14, 28612), (8, 43, 110, 2126), (8, 152, 15, 13737), (1, 3, 625, 34035)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n,rows,hidden,inter", FFN_SHARED_CLASSES)
+def test_ffn_shared_sums_of_every_class(n, rows, hidden, inter, dt):
+    run_ffn(n, rows, hidden, inter, dt, "silu", seed=rows, ranks=(n - 1,))
+
+
 def xent_inputs(n, rows, hidden, vocab, dt, seed, ignored=0.2):
     gen = torch.Generator().manual_seed(seed)
     x = _rand(gen, (rows, hidden), dt)
@@ -194,6 +204,15 @@ XENT_SHARED_SHAPES = [(1, 20, 72, 9000), (2, 7, 100, 20011), (1, 40, 136, 30000)
 @pytest.mark.parametrize("n,rows,hidden,vocab", XENT_SHARED_SHAPES)
 def test_xent_shared_sums(n, rows, hidden, vocab, piece, dt):
     run_xent(n, rows, hidden, vocab, dt, piece=piece, seed=vocab)
+
+
+XENT_SHARED_CLASSES = [(1, 394, 767, 11339), (2, 300, 8, 26308), (2, 2, 1100, 15083), (1, 764, 39, 3456)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n,rows,hidden,vocab", XENT_SHARED_CLASSES)
+def test_xent_shared_sums_of_every_class(n, rows, hidden, vocab, dt):
+    run_xent(n, rows, hidden, vocab, dt, seed=vocab)
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])

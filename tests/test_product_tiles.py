@@ -9,7 +9,8 @@ import subprocess
 import pytest
 
 from all_reduce_reduction_rank_amd import vocab_shards
-from tests.test_gpu_layer import FFN_CLASS_SHAPES, FFN_SHAPES, FFN_SHARED_SHAPES, XENT_SHAPES, XENT_SHARED_SHAPES
+from tests.test_gpu_layer import (FFN_CLASS_SHAPES, FFN_SHAPES, FFN_SHARED_CLASSES, FFN_SHARED_SHAPES, XENT_SHAPES,
+                                  XENT_SHARED_CLASSES, XENT_SHARED_SHAPES)
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "all_reduce_reduction_rank_amd", "csrc")
@@ -110,6 +111,21 @@ def test_gpu_tests_share_sums(classes):
         for shape in XENT_SHARED_SHAPES:
             got = classes(xent_plans(*shape, dt), shares=True)
             assert got[2][1] > 1 and all(n == 1 for i, (_, n) in enumerate(got) if i != 2), (dt, shape, got)
+
+
+def test_gpu_tests_share_sums_in_every_class(classes):
+    seen = set()
+    for dt in ("bf16", "f32"):
+        for shape in [*FFN_SHARED_SHAPES, *FFN_SHARED_CLASSES]:
+            got = classes(ffn_plans(*shape, dt), shares=True)
+            seen |= {(kind, dt, got[i][0]) for kind, i in (("store", 1), ("grads", 3)) if got[i][1] > 1}
+        for shape in [*XENT_SHARED_SHAPES, *XENT_SHARED_CLASSES]:
+            got = classes(xent_plans(*shape, dt), shares=True)
+            seen |= {("grads", dt, got[2][0])} if got[2][1] > 1 else set()
+    want = {(kind, "bf16", c) for kind in ("store", "grads") for c in ("large", "small", "split", "thin")}
+    want |= {("grads", "bf16", "flat"), ("grads", "f32", "small")}
+    want |= {(kind, "f32", c) for kind in ("store", "grads") for c in ("tall", "split")} | {("store", "f32", "thin")}
+    assert not want - seen, sorted(want - seen)
 
 
 def test_recomputed_logits_are_summed_in_the_order_of_the_forward_pass(classes):
