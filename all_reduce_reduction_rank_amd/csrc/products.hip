@@ -15,8 +15,14 @@
 //   Split             73   116   185   347   687 |   42    60   108   205   377
 //   Thin (m = 1)      55                         |   31
 //
-// One small product, [512, 4096] x [1024, 4096]: 83, 50, 31, 16 us.  Thin is
-// for 16 rows at most: with more it reads the weights again for every 16.
+// One small product, [512, 4096] x [1024, 4096]: 83, 50, 31, 16 us.  Thin
+// is for up to 64 rows where other tiles would be few (bf16) or mostly empty
+// (fp32): logits of 27 rows, width 7424, 4 x 296 columns in fp32 137 us in Split, 35 in
+// Thin.  With more tiles than run at once it reads the weights again for every
+// 16 rows: [17, 7360] x [6816 pairs, 7360] x 2 and back, bf16, 125 us in Flat, 144
+// in Thin; fp32 loss step [43, 3172] x 60815 over 2 ranks 1228 in Split, 1456 in
+// Thin, but the loss of [30, 1408] x 101216 over 3 ranks 237 and 182.
+//
 // A product with few tiles and a long K (a gradient summed over the vocabulary)
 // has 2 to 16 workgroups share each tile's K, where the shorter sums are worth a
 // second kernel that adds them: fp32 [11, 7522] x [7522, 314], 5 tiles of 64
@@ -154,7 +160,7 @@ TileChoice product_tile(int kind, int dtype, const ProductPlan& plan, int device
     const ClassCost& k = COST[c];
     if (c == TILE_TALL ? dtype == DT_BF16 : (c == TILE_LARGE || c == TILE_FLAT) && dtype != DT_BF16) continue;
     if (c == TILE_LARGE && fold) continue;
-    if (c == TILE_THIN && max_m > (uint32_t)Thin::BM) continue;
+    if (c == TILE_THIN && max_m > 4 * (uint32_t)Thin::BM) continue;
     if (fold && reads_terms && k.bm != 2 * fold) continue;
     if (plan.k_parts && k.parts != plan.k_parts) continue;
     for (uint32_t shares = 1; shares <= (sharing ? MAX_SHARES : 1); shares *= 2) {
@@ -175,6 +181,9 @@ TileChoice product_tile(int kind, int dtype, const ProductPlan& plan, int device
       const double slots = cus * k.resident;
       const double rounds = (double)(uint64_t)(tiles / slots);
       const double rest = tiles - rounds * slots;
+      // every 16 rows read the weights again: from the caches, if all of them run
+      // at once; fp32 gains more by half as many empty rows as by fewer reads
+      if (c == TILE_THIN && rounds > 0 && max_m > (uint32_t)Thin::BM * (dtype == DT_BF16 ? 1 : 2)) continue;
       double us;
       if (dtype != DT_BF16) {
         // matrix instructions: a CU works its tiles off one after the other,

@@ -112,7 +112,7 @@ def test_ffn_large_tiles(dt):
 # Shapes that take the tile classes the ones above do not (n, rows, hidden, inter).
 FFN_CLASS_SHAPES = [
     (8, 408, 112, 1160), (8, 776, 280, 1632), (8, 603, 40, 1368), (2, 605, 40, 1704), (8, 586, 1856, 72),
-    (8, 763, 752, 32), (1, 1116, 1856, 32), (8, 1730, 432, 32),
+    (8, 763, 752, 32), (1, 1116, 1856, 32), (8, 1730, 432, 32), (2, 44, 1024, 72), (3, 18, 640, 130),
 ]
 
 
@@ -178,7 +178,7 @@ XENT_SHAPES = [
     # ranks, rows, hidden, vocab
     (1, 1, 8, 2), (1, 1, 64, 1), (2, 3, 7, 33), (3, 17, 65, 1000), (8, 5, 64, 3), (1, 64, 200, 511), (2, 129, 136, 513),
     (4, 130, 40, 2050), (8, 260, 72, 4099), (1, 300, 33, 129), (8, 1, 200, 16), (3, 1, 40, 17), (1, 22, 144, 29),
-    (3, 1047, 88, 9342),
+    (3, 1047, 88, 9342), (3, 84, 120, 699), (2, 44, 72, 300),
 ]
 
 
