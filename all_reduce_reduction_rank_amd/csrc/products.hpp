@@ -30,13 +30,15 @@ enum : uint32_t {
 // ProductArgs::act
 enum : uint32_t { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
 
-// The (max, sum of exp(v - max)) pairs of two sets of values, joined.  An
-// infinite max shifts by 0 instead, so that a set of -inf adds nothing and
-// +inf gives an infinite sum (not inf - inf).
-__device__ __forceinline__ float stats_shift(float top) { return fabsf(top) == INFINITY ? 0.f : top; }
-__device__ __forceinline__ float2 merge_stats(float2 x, float2 y) {
+// The (max, sum of exp(v - max)) pairs of two sets of values, joined: each sum
+// is scaled by exp(its max - the joint max).  An infinite joint max shifts by 0
+// instead, so that +inf gives an infinite sum (not inf - inf).  An empty set, or
+// one of -inf alone, is (-inf, 0); its own max in the exponent weighs it 0
+// wherever the other set lies, and a sum of NaN stays NaN.
+__host__ __device__ __forceinline__ float stats_shift(float top) { return fabsf(top) == INFINITY ? 0.f : top; }
+__host__ __device__ __forceinline__ float2 merge_stats(float2 x, float2 y) {
   const float top = fmaxf(x.x, y.x), shift = stats_shift(top);
-  return make_float2(top, x.y * expf(stats_shift(x.x) - shift) + y.y * expf(stats_shift(y.x) - shift));
+  return make_float2(top, x.y * expf(x.x - shift) + y.y * expf(y.x - shift));
 }
 
 // Bytes of c[2] for MAX_SHARES blocks of every rank's [rows, cols] result; 0 where
