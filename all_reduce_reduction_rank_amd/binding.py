@@ -20,7 +20,6 @@ if that fails every call raises -- there is no CPU fallback.
 
 import ctypes
 import functools
-import math
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -467,11 +466,9 @@ class _Scratch:
             return torch.empty(shape, dtype=dtype, device=self.device)
 
     def ranks(self, n, shape, dtype):
-        """N rank buffers of one shape: views of one allocation where each
-        starts on a 16-byte boundary (one allocation costs as much host time
-        as each of N would)."""
-        if n > 1 and (math.prod(shape) * dtype.itemsize) % 16 == 0:
-            return list(self.empty((n, *shape), dtype).unbind(0))
+        """N rank buffers of one shape, each a tensor of its own: views of one
+        allocation would keep each other alive, be saved together, and count
+        as one tensor's views in autograd."""
         return [self.empty(shape, dtype) for _ in range(n)]
 
     def workspace(self, nbytes):
@@ -637,8 +634,7 @@ def linear_cross_entropy_backward(grad_loss, x, w, target, lse, dx=None, dw=None
     outs = []
     for i, (_, t, shapes) in enumerate(results):
         if t is None:
-            same = shapes[0] == shapes[-1]  # (shards: all of one length, or not)
-            t = scratch.ranks(n, shapes[0], dtype) if same else [scratch.empty(shape, dtype) for shape in shapes]
+            t = [scratch.empty(shape, dtype) for shape in shapes]
             given[i] = _PTRS[n](*[v.data_ptr() for v in t])
         outs.append(t)
     nbytes = _xent_workspace(n, rows, hidden, vocab, dt, 1, piece)
