@@ -442,11 +442,15 @@ def _layer_vector(t, rows, dtype, device, what):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _on_device(device):
-    """The call's tensors must be device tensors on the current device."""
+def _on_device(device, stream):
+    """The call's tensors must be device tensors on the current device, and its
+    stream one of that device (the workspace goes back to the device's memory
+    pool of that stream)."""
     torch = _TORCH
     if device < 0:
         raise ValueError("rank buffers must be contiguous device tensors")
+    if stream is not None and stream.device_index != device:
+        raise ValueError("stream must be a stream of the rank buffers' device")
     if device != torch.cuda.current_device():
         raise ValueError("rank buffers must live on the current device")
 
@@ -517,7 +521,7 @@ def gated_ffn(x, w_gate, w_up, w_down, out=None, gate=None, up=None, act="silu",
     g = _layer_list(gate, n, (rows, inter), f32, device, "gate") if gate is not None else None
     u = _layer_list(up, n, (rows, inter), f32, device, "up") if up is not None else None
     o = _layer_list(out, n, (rows, hidden), dtype, device, "out") if out is not None else None
-    _on_device(device)
+    _on_device(device, stream)
     scratch = _Scratch(stream, device)
     if out is None:
         out = scratch.ranks(n, (rows, hidden), dtype)
@@ -546,7 +550,7 @@ def gated_ffn_backward(dout, x, w_gate, w_up, w_down, gate, up, dx=None, dw_gate
     results = [("dx", dx, (rows, hidden)), ("dw_gate", dw_gate, (inter, hidden)), ("dw_up", dw_up, (inter, hidden)),
                ("dw_down", dw_down, (hidden, inter))]
     given = [_layer_list(t, n, shape, dtype, device, what) if t is not None else None for what, t, shape in results]
-    _on_device(device)
+    _on_device(device, stream)
     scratch = _Scratch(stream, device)
     outs = []
     for i, (_, t, shape) in enumerate(results):
@@ -598,7 +602,7 @@ def linear_cross_entropy(x, w, target, loss=None, lse=None, stream=None):
     n, device, _, dt, rows, hidden, vocab, _, ptrs = _xent_inputs(x, w, target)
     given = [_layer_list(t, n, (rows,), torch.float32, device, what) if t is not None else None
              for what, t in (("loss", loss), ("lse", lse))]
-    _on_device(device)
+    _on_device(device, stream)
     scratch = _Scratch(stream, device)
     outs = []
     for i, t in enumerate((loss, lse)):
@@ -629,7 +633,7 @@ def linear_cross_entropy_backward(grad_loss, x, w, target, lse, dx=None, dw=None
     z = _layer_list(lse, n, (rows,), torch.float32, device, "lse")
     results = [("dx", dx, [(rows, hidden)] * n), ("dw", dw, [(v, hidden) for v in shards])]
     given = [_layer_list(t, n, shapes, dtype, device, what) if t is not None else None for what, t, shapes in results]
-    _on_device(device)
+    _on_device(device, stream)
     scratch = _Scratch(stream, device)
     outs = []
     for i, (_, t, shapes) in enumerate(results):
