@@ -21,6 +21,12 @@ adds sum b |w|.  A value rounded to the payload type adds step |value|.  An
 activation and its derivative are at most 16 fp32 roundings of values of
 magnitude at most 1 + |value| each, and change by at most 1.2 (2 for the
 derivative) times a change of their argument.
+
+`terms`: the bf16 terms an intermediate (h, dg, du, d) is kept in.  With two, its
+error is at most step^2 |value| (what rounding leaves is exact in fp32, at most
+step |value|, and rounded once more), a product sums twice as many terms, and
+the result's bound is the sharper `nearest`, under which a lost or misplaced
+second term shows.
 """
 
 import math
@@ -56,11 +62,12 @@ def act(z, name):
     return 0.5 * z * (1 + t), 0.5 * (1 + t) + 0.5 * z * (1 - t * t) * k * (1 + 3 * 0.044715 * z * z)
 
 
-def product(a, b, ea=None, eb=None):
-    """a b^T and the bound on its fp32 evaluation; ea, eb bound the operands."""
+def product(a, b, ea=None, eb=None, terms=1):
+    """a b^T and the bound on its fp32 evaluation; ea, eb bound the operands,
+    one of which is in `terms` terms."""
     k = a.shape[1]
     size = np.abs(a) @ np.abs(b).T
-    err = k * E * size + TINY
+    err = terms * k * E * size * (1 + 2.0 ** -7 * (terms - 1)) + TINY
     if ea is not None:
         err = err + ea @ np.abs(b).T
     if eb is not None:
@@ -68,38 +75,54 @@ def product(a, b, ea=None, eb=None):
     return a @ b.T, err
 
 
-def rounded(v, err, dt):
-    return v, err + step(dt) * (np.abs(v) + err)
+def rounded(v, err, dt, terms=1):
+    return v, err + step(dt) ** terms * (np.abs(v) + err)
 
 
-def gated_ffn(x, wg, wu, wd, name, dt):
+def bf16_of(v):
+    """The bf16 value nearest to an fp64 one, ties to even."""
+    m, e = np.frexp(v)
+    return np.ldexp(np.rint(np.ldexp(m, 8)), e - 8)
+
+
+def nearest(v, err):
+    """A value y within err of v, rounded to bf16: y's nearest is no further from
+    y than v's nearest is, so off v by at most |bf16(v) - v| + 2 err."""
+    return v, np.abs(bf16_of(v) - v) + 2 * err
+
+
+def result(v, err, dt, terms):
+    return nearest(v, err) if terms == 2 else rounded(v, err, dt)
+
+
+def gated_ffn(x, wg, wu, wd, name, dt, terms=1):
     """{"gate", "up", "out"}: (value, bound) of one rank."""
     g, eg = product(x, wg)
     u, eu = product(x, wu)
     a, _ = act(g, name)
     ea = 1.2 * eg + 16 * E * (1 + np.abs(a))
     h = a * u
-    _, eh = rounded(h, ea * (np.abs(u) + eu) + np.abs(a) * eu + E * np.abs(h), dt)
-    out, eo = product(h, wd, eh)
-    return {"gate": (g, eg), "up": (u, eu), "out": rounded(out, eo, dt)}
+    _, eh = rounded(h, ea * (np.abs(u) + eu) + np.abs(a) * eu + E * np.abs(h), dt, terms)
+    out, eo = product(h, wd, eh, terms=terms)
+    return {"gate": (g, eg), "up": (u, eu), "out": result(out, eo, dt, terms)}
 
 
-def gated_ffn_backward(dout, x, wg, wu, wd, g, u, name, dt):
+def gated_ffn_backward(dout, x, wg, wu, wd, g, u, name, dt, terms=1):
     """{"dx", "dw_gate", "dw_up", "dw_down"} of one rank, given the stored g and u."""
     dh, edh = product(dout, wd.T)
     a, da = act(g, name)
     ea, eda = 16 * E * (1 + np.abs(a)), 16 * E * (1 + np.abs(da))
     dg, du, h = dh * u * da, dh * a, a * u
-    _, edg = rounded(dg, edh * np.abs(u) * (np.abs(da) + eda) + np.abs(dh * u) * eda + 2 * E * np.abs(dg), dt)
-    _, edu = rounded(du, edh * (np.abs(a) + ea) + np.abs(dh) * ea + E * np.abs(du), dt)
-    _, eh = rounded(h, np.abs(u) * ea + E * np.abs(h), dt)
+    _, edg = rounded(dg, edh * np.abs(u) * (np.abs(da) + eda) + np.abs(dh * u) * eda + 2 * E * np.abs(dg), dt, terms)
+    _, edu = rounded(du, edh * (np.abs(a) + ea) + np.abs(dh) * ea + E * np.abs(du), dt, terms)
+    _, eh = rounded(h, np.abs(u) * ea + E * np.abs(h), dt, terms)
     # dx is one sum of 2 inter terms
-    dx, edx = product(np.concatenate([dg, du], 1), np.concatenate([wg, wu], 0).T, np.concatenate([edg, edu], 1))
-    dwg, edwg = product(dg.T, x.T, edg.T)
-    dwu, edwu = product(du.T, x.T, edu.T)
-    dwd, edwd = product(dout.T, h.T, None, eh.T)
-    return {"dx": rounded(dx, edx, dt), "dw_gate": rounded(dwg, edwg, dt), "dw_up": rounded(dwu, edwu, dt),
-            "dw_down": rounded(dwd, edwd, dt)}
+    dx, edx = product(np.concatenate([dg, du], 1), np.concatenate([wg, wu], 0).T, np.concatenate([edg, edu], 1), terms=terms)
+    dwg, edwg = product(dg.T, x.T, edg.T, terms=terms)
+    dwu, edwu = product(du.T, x.T, edu.T, terms=terms)
+    dwd, edwd = product(dout.T, h.T, None, eh.T, terms=terms)
+    return {"dx": result(dx, edx, dt, terms), "dw_gate": result(dwg, edwg, dt, terms),
+            "dw_up": result(dwu, edwu, dt, terms), "dw_down": result(dwd, edwd, dt, terms)}
 
 
 def cross_entropy(x, w, target):
@@ -128,7 +151,7 @@ def cross_entropy(x, w, target):
     return (loss, eloss), (lse, elen)
 
 
-def cross_entropy_backward(grad, x, w, target, lse, dt, first=0, vocab=None):
+def cross_entropy_backward(grad, x, w, target, lse, dt, first=0, vocab=None, terms=1):
     """(dx, dw) of the vocabulary rows w = W[first : first + len(w)], given the
     stored lse."""
     logits, el = product(x, w)
@@ -144,9 +167,9 @@ def cross_entropy_backward(grad, x, w, target, lse, dt, first=0, vocab=None):
     ez = el + E * np.abs(z)
     ep = p * (np.expm1(ez) + 2 * E * np.abs(z) + 4 * E)
     d = (p - hit) * g
-    _, ed = rounded(d, (ep + 2 * E * np.abs(p - hit)) * np.abs(g), dt)
-    dx, edx = product(d, w.T, ed)
-    dw, edw = product(d.T, x.T, ed.T)
+    _, ed = rounded(d, (ep + 2 * E * np.abs(p - hit)) * np.abs(g), dt, terms)
+    dx, edx = product(d, w.T, ed, terms=terms)
+    dw, edw = product(d.T, x.T, ed.T, terms=terms)
     # dx is added up over pieces of the vocabulary: as many terms, plus one
     # fp32 addition per piece, within the count of terms
-    return rounded(dx, edx, dt), rounded(dw, edw, dt)
+    return result(dx, edx, dt, terms), result(dw, edw, dt, terms)
