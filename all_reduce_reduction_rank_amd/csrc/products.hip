@@ -160,7 +160,7 @@ TileChoice product_tile(int kind, int dtype, const ProductPlan& plan, int device
     const ClassCost& k = COST[c];
     if (c == TILE_TALL ? dtype == DT_BF16 : (c == TILE_LARGE || c == TILE_FLAT) && dtype != DT_BF16) continue;
     if (c == TILE_LARGE && fold) continue;
-    if (c == TILE_THIN && max_m > 4 * (uint32_t)Thin::BM) continue;
+    if (c == TILE_THIN && max_m > THIN_MAX_ROWS) continue;
     if (fold && reads_terms && k.bm != 2 * fold) continue;
     if (plan.k_parts && k.parts != plan.k_parts) continue;
     for (uint32_t shares = 1; shares <= (sharing ? MAX_SHARES : 1); shares *= 2) {

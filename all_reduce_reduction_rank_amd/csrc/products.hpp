@@ -73,7 +73,11 @@ constexpr uint32_t tile_cols(int tile) {
   constexpr uint32_t cols[TILE_CLASSES] = {Large::BN, Small::BN, Tall::BN, Flat::BN, Split::BN, Thin::BN};
   return cols[tile];
 }
-constexpr uint32_t MIN_TILE_COLS = Thin::BN;
+// The fewest columns a tile covers in a product of that many rows: Thin tiles are
+// for few rows (product_tile), the others have 64 columns or more.
+constexpr uint32_t THIN_MAX_ROWS = 4 * Thin::BM;
+constexpr uint32_t min_tile_cols(uint64_t rows) { return rows <= THIN_MAX_ROWS ? Thin::BN : Split::BN; }
+static_assert(Split::BN <= Tall::BN && Split::BN <= Flat::BN && Split::BN <= Small::BN && Split::BN <= Large::BN, "");
 // Order in which a class adds up K (ProductPlan::k_parts).
 constexpr uint32_t tile_k_parts(int tile) { return tile == TILE_SPLIT ? Split::WK : tile == TILE_THIN ? Thin::WK : 1; }
 

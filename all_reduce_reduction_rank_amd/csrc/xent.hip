@@ -112,7 +112,7 @@ constexpr uint64_t DEFAULT_PIECE_BYTES = 1ull << 30;  // d of all ranks, unless 
 struct XentShape {
   uint64_t rows, hidden, vocab, es;
   uint64_t shard[MAX_RANKS], start[MAX_RANKS], max_shard;
-  uint64_t part_tiles;  // partials per row and rank, at the smallest tile
+  uint64_t part_tiles;  // partials per row and rank, at the narrowest tile that many rows may take
   uint64_t pack_bytes;  // copies of every rank's x and w, where their rows are not whole 16-byte chunks
   uint64_t live_bytes;  // the same with x copied always
 };
@@ -127,7 +127,7 @@ XentShape shape_of(int n, size_t rows, size_t hidden, size_t vocab, int dtype) {
     s.shard[r] = umin((uint64_t)(r + 1) * b, s.vocab) - s.start[r];
   }
   s.max_shard = b;
-  s.part_tiles = (b + MIN_TILE_COLS - 1) / MIN_TILE_COLS;
+  s.part_tiles = (b + min_tile_cols(rows) - 1) / min_tile_cols(rows);
   s.pack_bytes = s.live_bytes = 0;
   for (int r = 0; r < n; ++r) {
     const uint64_t w = Packer::bytes(s.shard[r], s.hidden, s.es);
