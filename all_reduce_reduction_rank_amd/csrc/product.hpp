@@ -128,12 +128,6 @@ __device__ __forceinline__ void tile_coords(uint32_t t, uint32_t tiles_m, uint32
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); }
-template <class T>
-__device__ __forceinline__ T* uniform(T* p) {
-  const uint64_t x = (uint64_t)p;
-  const uint32_t lo = uniform((uint32_t)x), hi = uniform((uint32_t)(x >> 32));
-  return (T*)(((uint64_t)hi << 32) | lo);
-}
 
 // Buffer descriptor of `bytes` bytes from p on (raw 32-bit data; offsets past
 // the end read as zero).
@@ -576,19 +570,16 @@ struct Product {
 template <int DT, int V, bool STREAM = false>
 __device__ __forceinline__ void store_row(char* row, uint64_t col, uint32_t n, bool vec, const float* v) {
   constexpr int ES = KElem<DT>::ES;
+  static_assert(DT != DT_BF16 || V == 8, "a 16-byte store");
   char* p = row + col * ES;
   if (vec && col + V <= n) {
     if constexpr (DT == DT_BF16) {
       uint32_t h[V / 2];
 #pragma unroll
       for (int e = 0; e < V / 2; ++e) h[e] = bf16_round(v[2 * e]) | (bf16_round(v[2 * e + 1]) << 16);
-      if constexpr (V == 8) {
-        const v4u x = {h[0], h[1], h[2], h[3]};
-        if constexpr (STREAM) __builtin_nontemporal_store(x, (v4u*)p);
-        else *(v4u*)p = x;
-      } else {
-        *(uint2*)p = make_uint2(h[0], h[1]);
-      }
+      const v4u x = {h[0], h[1], h[2], h[3]};
+      if constexpr (STREAM) __builtin_nontemporal_store(x, (v4u*)p);
+      else *(v4u*)p = x;
     } else {
 #pragma unroll
       for (int e = 0; e < V; e += 4) {

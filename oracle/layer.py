@@ -41,10 +41,6 @@ def step(dt):
     return 2.0 ** -8 if dt == "bf16" else E
 
 
-def _erf(z):
-    return np.vectorize(math.erf, otypes=[np.float64])(z) if z.size else z
-
-
 def _erfc(z):
     return np.vectorize(math.erfc, otypes=[np.float64])(z) if z.size else z
 
