@@ -512,7 +512,9 @@ def gated_ffn(x, w_gate, w_up, w_down, out=None, gate=None, up=None, act="silu",
     [hidden, inter]; out[r]: [rows, hidden], allocated when None.  gate, up:
     None, or N fp32 tensors [rows, inter] that receive the two projections for
     ``gated_ffn_backward``.  act: "silu", "gelu" or "gelu_tanh".  Runs on the
-    current device; fp32 and bf16."""
+    current device; fp32 and bf16.  Every matrix is contiguous and starts on a
+    16-byte boundary (rows cut out of a tensor of odd width may not: ARError
+    AR_ERR_INVALID)."""
     a = _act(act)
     n, device, dtype, dt, rows, hidden, inter, ptrs = _ffn_weights(x, w_gate, w_up, w_down)
     f32 = _torch().float32
@@ -597,7 +599,9 @@ def linear_cross_entropy(x, w, target, loss=None, lse=None, stream=None):
     ``vocab_shards(vocab, N)[r]`` rows of W [vocab, hidden]; x[r]: [rows,
     hidden], the same on every rank; target: one int64 vector [rows]; rows whose
     target is outside [0, vocab) have loss 0.  Every rank receives the whole
-    loss = lse - logit of the target, and lse, which the backward pass needs."""
+    loss = lse - logit of the target, and lse, which the backward pass needs.
+    Every matrix is contiguous and starts on a 16-byte boundary (a shard cut out of
+    a W of odd width may not: ARError AR_ERR_INVALID)."""
     torch = _torch()
     n, device, _, dt, rows, hidden, vocab, _, ptrs = _xent_inputs(x, w, target)
     given = [_layer_list(t, n, (rows,), torch.float32, device, what) if t is not None else None
@@ -624,7 +628,8 @@ def linear_cross_entropy_backward(grad_loss, x, w, target, lse, dx=None, dw=None
     grad_loss: fp32 vector [rows], the gradient of each row's loss; lse: what
     ``linear_cross_entropy`` returned.  dx[r] is rank r's partial sum
     (``Comm.allreduce`` completes it).  `piece`: vocabulary rows of each rank
-    worked on at a time (0: chosen by the library), which caps the workspace."""
+    worked on at a time (at least 256; 0: chosen by the library), which caps the
+    workspace."""
     torch = _torch()
     n, device, dtype, dt, rows, hidden, vocab, shards, ptrs = _xent_inputs(x, w, target)
     if piece < 0:

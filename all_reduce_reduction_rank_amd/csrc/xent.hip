@@ -107,7 +107,8 @@ __global__ __launch_bounds__(COMBINE_THREADS) void scale_kernel(const float* gra
   }
 }
 
-constexpr uint64_t DEFAULT_PIECE_BYTES = 1ull << 30;  // d of all ranks, unless the caller says otherwise
+// d of all ranks, unless the caller says otherwise or 256 columns of each take more
+constexpr uint64_t DEFAULT_PIECE_BYTES = 1ull << 30;
 
 struct XentShape {
   uint64_t rows, hidden, vocab, es;
@@ -146,7 +147,8 @@ ar_status check_shape(int n, size_t rows, size_t hidden, size_t vocab, int dtype
 }
 
 // Vocabulary rows per rank and piece: the caller's, or as many as keep d of
-// all ranks within DEFAULT_PIECE_BYTES; whole tiles, at least one.
+// all ranks within DEFAULT_PIECE_BYTES; whole tiles, at least one (256 columns,
+// however many rows there are).
 uint64_t piece_of(const XentShape& s, int n, size_t piece) {
   uint64_t p = piece ? (uint64_t)piece : DEFAULT_PIECE_BYTES / umax(1, (uint64_t)n * s.rows * s.es);
   p = umin(p, LAYER_MAX_WIDTH);

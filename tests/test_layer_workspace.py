@@ -37,3 +37,21 @@ def test_no_choice_is_narrower(classes, dt):  # noqa: F811
     for (n, rows, hidden, vocab), tile in zip(shapes, got):
         assert COLS[tile] >= narrowest(rows), (n, rows, hidden, vocab, tile)
     assert {"thin"} < set(got)
+
+
+@pytest.mark.parametrize("n,rows,hidden,vocab", [(2, 100000, 16, 100000), (8, 400000, 8, 131072), (1, 5000, 1024, 700)])
+def test_pieces_are_as_documented(n, rows, hidden, vocab):
+    shard = -(-vocab // n)
+
+    def d_bytes(piece):  # fp32: d, and the copy of x; dx is summed in place
+        total = binding.library().ar_linear_cross_entropy_workspace(n, rows, hidden, vocab, 0, 1, piece)
+        return total - n * align(rows * hidden * 4)
+
+    def of(columns):
+        return n * align(rows * min(columns, (shard + 7) // 8 * 8) * 4)
+
+    for piece, columns in ((1, 256), (255, 256), (256, 256), (300, 256), (1023, 768), (1 << 40, 1 << 20)):
+        assert d_bytes(piece) == of(columns), piece
+    # chosen by the library: within 1 GiB, but no fewer than 256 columns
+    assert d_bytes(0) == of(max(256, (1 << 30) // (n * rows * 4) // 256 * 256))
+    assert d_bytes(0) <= max(1 << 30, of(256))
