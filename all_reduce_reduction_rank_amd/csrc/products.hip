@@ -31,7 +31,8 @@
 // fp32 runs 16 times as many instructions per byte, so its steps cost what
 // its matrix instructions do, and the choice is which tile fills the CUs most
 // evenly: two ranks of [1024, 1024] x [8000, 1024] 290 us in Small and 315 in
-// Tall, but [1024, 8000] x [8000, 1024] 536, 307, Split 297.
+// Tall, but [1024, 8000] x [8000, 1024] 536, 307, Split 297 (all from a cold clock;
+// after a second of such calls the first takes 265).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
