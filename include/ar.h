@@ -440,9 +440,10 @@ ar_status ar_linear_cross_entropy(int nranks, const void* const* x, const void* 
  * shard, rounded up to 8; 0: as many as keep d of all ranks within 1 GiB, but
  * also at least 256, so that d takes nranks * rows * 256 elements or more: over
  * 1 GiB beyond 262144 bf16 rows of 8 ranks).  dx is added up in fp32 and
- * rounded once.  AR_BF16: d over the largest finite |grad_loss| is rounded to bf16 before it is multiplied
- * (with up to 32 rows d is kept in two bf16 terms instead).  `piece`
- * changes no term of dw (the order of its sums over the rows may differ).
+ * rounded once.  AR_BF16: d over the largest finite |grad_loss| is rounded to
+ * bf16 before it is multiplied (with up to 32 rows d is kept in two bf16 terms
+ * instead).  `piece` changes no term of dw (the order of its sums over the rows
+ * may differ).
  * rows 0: dw becomes zeros. */
 ar_status ar_linear_cross_entropy_backward(int nranks, const float* grad_loss, const void* const* x,
                                            const void* const* w, const int64_t* target, const float* const* lse,
