@@ -12,6 +12,10 @@ C names (``include/ar.h``):
     select(nranks, op, count, dtype, algo="auto", proto="auto", max_line_bytes_per_rank=0)
     gated_ffn(x, w_gate, w_up, w_down, act="silu")                           # + gated_ffn_backward
     linear_cross_entropy(x, w, target)                                       # + linear_cross_entropy_backward
+    qk_norm_rope(q, k, q_weight, k_weight, pos, freq)                        # + qk_norm_rope_backward
+    cache = KVCache.empty(nranks, pages, kv_heads, head_dim, page=64)
+    cache_write(cache, k, v, table, first, start)                            # + cache_read
+    cache_attention(q, cache, table, first, length)
 
 ``send`` / ``recv`` are lists of N contiguous CUDA (HIP) tensors on the
 communicator's device.  If the library is missing it is built once with hipcc;
@@ -47,6 +51,8 @@ SYMBOLS = (
     "ar_allreduce_noalloc", "ar_debug_calls", "ar_stream_ceiling",
     "ar_gated_ffn_workspace", "ar_gated_ffn", "ar_gated_ffn_backward",
     "ar_linear_cross_entropy_workspace", "ar_linear_cross_entropy", "ar_linear_cross_entropy_backward",
+    "ar_qk_norm_rope", "ar_qk_norm_rope_workspace", "ar_qk_norm_rope_backward",
+    "ar_cache_write", "ar_cache_read", "ar_cache_attention_workspace", "ar_cache_attention",
 )
 
 
@@ -57,6 +63,20 @@ class CallRecord(ctypes.Structure):
                 ("in_place", ctypes.c_int32), ("grid", ctypes.c_uint32), ("batch", ctypes.c_uint32),
                 ("counter_free", ctypes.c_uint32), ("by_die", ctypes.c_uint32), ("count", ctypes.c_uint64),
                 ("ntasks", ctypes.c_uint64), ("tile_bytes", ctypes.c_uint64)]
+
+
+class CacheRecord(ctypes.Structure):
+    """ar_kv_cache (include/ar.h)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("pages", ctypes.c_size_t), ("page", ctypes.c_size_t), ("kv_heads", ctypes.c_size_t),
+                ("head_dim", ctypes.c_size_t), ("nranks", ctypes.c_int)]
+
+
+class PagedRows(ctypes.Structure):
+    """ar_paged_rows (include/ar.h)."""
+    _fields_ = [("table", ctypes.c_void_p), ("first", ctypes.c_void_p), ("at", ctypes.c_void_p),
+                ("table_stride", ctypes.c_size_t), ("width", ctypes.c_size_t), ("seqs", ctypes.c_size_t),
+                ("rows", ctypes.c_size_t)]
 
 
 class ARError(RuntimeError):
@@ -96,10 +116,19 @@ def _declare(lib):
     lib.ar_linear_cross_entropy_workspace.argtypes = [I, S, S, S, I, I, S]
     lib.ar_linear_cross_entropy.argtypes = [I, PP, PP, P, PP, PP, S, S, S, I, P, S, P]
     lib.ar_linear_cross_entropy_backward.argtypes = [I, P, PP, PP, P, PP, PP, PP, S, S, S, I, S, P, S, P]
+    F, C, R = ctypes.c_float, ctypes.POINTER(CacheRecord), ctypes.POINTER(PagedRows)
+    lib.ar_qk_norm_rope.argtypes = [I, PP, S, PP, S, P, P, P, P, PP, PP, S, S, S, S, S, I, F, I, P]
+    lib.ar_qk_norm_rope_workspace.argtypes = [I, S, S, S, S]
+    lib.ar_qk_norm_rope_backward.argtypes = ([I, PP, PP, PP, S, PP, S, P, P, P, P, PP, S, PP, S, PP, PP, S, S, S, S, S, I, F, I,
+                                              P, S, P])
+    lib.ar_cache_write.argtypes = [C, PP, S, PP, S, R, I, P]
+    lib.ar_cache_read.argtypes = [C, PP, PP, R, I, P]
+    lib.ar_cache_attention_workspace.argtypes = [C, S, S, S, S, S, I]
+    lib.ar_cache_attention.argtypes = [C, PP, S, R, PP, PP, S, F, I, S, S, I, P, S, P]
     lib.ar_status_string.argtypes = [I]
     lib.ar_status_string.restype = ctypes.c_char_p
     for name in SYMBOLS:
-        if name in ("ar_gated_ffn_workspace", "ar_linear_cross_entropy_workspace"):
+        if name.endswith("_workspace"):
             getattr(lib, name).restype = S
         elif name not in ("ar_comm_workspace_bytes", "ar_status_string"):
             getattr(lib, name).restype = I
@@ -652,6 +681,289 @@ def linear_cross_entropy_backward(grad_loss, x, w, target, lse, dx=None, dw=None
                                                    ws_ptr, nbytes, _stream_handle(stream, device)),
            "ar_linear_cross_entropy_backward")
     return tuple(outs)
+
+
+def _head_list(ts, n, rows, width, dtype, device, what):
+    """(pointer array, stride) of N rank tensors [rows, heads, head_dim] whose
+    rows are contiguous and all the same distance apart (views of a wider
+    matrix are fine); `width` = (heads, head_dim) or None for the first one's."""
+    if len(ts) != n:
+        raise ValueError(f"{what} holds {len(ts)} rank buffers; the call needs {n}")
+    first = ts[0]
+    if first.dim() != 3:
+        raise ValueError(f"{what} must be [rows, heads, head_dim] on every rank")
+    shape = (rows, *(width or first.shape[1:]))
+    dim = shape[2]
+    strides = first.stride()
+    ptrs = []
+    for i, t in enumerate(ts):
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != device or t.stride() != strides:
+            if t.dtype is not dtype:
+                raise TypeError(f"{what}[{i}] is {t.dtype}; the call needs {dtype}")
+            if t.shape != shape:
+                raise ValueError(f"{what}[{i}] has shape {tuple(t.shape)}; the call needs {tuple(shape)}")
+            raise ValueError(f"{what}[{i}] must lie on the call's device with the strides of {what}[0]")
+        ptrs.append(t.data_ptr())
+    if rows and shape[1] and (strides[2] != 1 or (shape[1] > 1 and strides[1] != dim)):
+        raise ValueError(f"{what} must have each row's heads side by side (strides {strides})")
+    # (the stride of a single row is arbitrary)
+    return _PTRS[n](*ptrs), strides[0] if rows > 1 else shape[1] * dim
+
+
+def _rope_inputs(q, k, q_weight, k_weight, pos, freq):
+    """(n, device, dtype, name, sizes, pointers and strides) of a qk_norm_rope call."""
+    torch = _torch()
+    n, device, dt = _layer_ranks(q, "q")
+    dtype = q[0].dtype
+    if q[0].dim() != 3:
+        raise ValueError("q must be [rows, heads, head_dim] on every rank")
+    rows, heads, dim = q[0].shape
+    qp, qs = _head_list(q, n, rows, None, dtype, device, "q")
+    kp, ks, kw, kv = None, 0, None, 0
+    if (k is None) != (k_weight is None):
+        raise ValueError("k and k_weight are given together or not at all")
+    if k is not None:
+        kp, ks = _head_list(k, n, rows, (k[0].shape[1] if k[0].dim() == 3 else 0, dim), dtype, device, "k")
+        kv = k[0].shape[1]
+        kw = _layer_vector(k_weight, dim, dtype, device, "k_weight")
+    rot = 0 if freq is None else 2 * freq.numel()
+    if rot and pos is None:
+        raise ValueError("freq needs pos")
+    args = [_layer_vector(q_weight, dim, dtype, device, "q_weight"), kw,
+            _layer_vector(pos, rows, torch.int64, device, "pos") if rot else None,
+            _layer_vector(freq, rot // 2, torch.float32, device, "freq") if rot else None]
+    return n, device, dtype, dt, (rows, heads, kv, dim, rot), (qp, qs, kp, ks), args
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, pos, freq, eps=1e-6, pairs=False, q_out=None, k_out=None, stream=None):
+    """ar_qk_norm_rope: (q_out, k_out), lists of N = len(q) tensors: each head of
+    each row over its root mean square, times its weight, its first
+    2 * len(freq) values turned by the angles pos * freq (halves together, or
+    with `pairs` neighbours).
+
+    q[r]: [rows, heads, head_dim], k[r]: [rows, kv_heads, head_dim], each row's
+    heads side by side (views of one projection's result are fine);
+    q_weight, k_weight: [head_dim]; pos: int64 [rows]; freq: fp32 [rot / 2] (None:
+    no rotation).  k and k_weight None: queries alone, k_out is None.  q_out,
+    k_out: contiguous, allocated when None.  head_dim 64, 128 or 256; fp32 and bf16."""
+    n, device, dtype, dt, (rows, heads, kv, dim, rot), x, shared = _rope_inputs(q, k, q_weight, k_weight, pos, freq)
+    qo = _layer_list(q_out, n, (rows, heads, dim), dtype, device, "q_out") if q_out is not None else None
+    if k is None and k_out is not None:
+        raise ValueError("k_out needs k")
+    ko = _layer_list(k_out, n, (rows, kv, dim), dtype, device, "k_out") if k_out is not None else None
+    _on_device(device, stream)
+    scratch = _Scratch(stream, device)
+    if qo is None:
+        q_out = scratch.ranks(n, (rows, heads, dim), dtype)
+        qo = _PTRS[n](*[t.data_ptr() for t in q_out])
+    if ko is None and k is not None:
+        k_out = scratch.ranks(n, (rows, kv, dim), dtype)
+        ko = _PTRS[n](*[t.data_ptr() for t in k_out])
+    _check(_lib().ar_qk_norm_rope(n, *x, *shared, qo, ko, rows, heads, kv, dim, rot, bool(pairs), eps, DTYPES[dt],
+                                  _stream_handle(stream, device)), "ar_qk_norm_rope")
+    return q_out, k_out
+
+
+@functools.lru_cache(maxsize=256)
+def _rope_workspace(n, rows, heads, kv, dim):
+    return _lib().ar_qk_norm_rope_workspace(n, rows, heads, kv, dim)
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, pos, freq, eps=1e-6, pairs=False, dq=None, dk=None,
+                          dq_weight=None, dk_weight=None, stream=None):
+    """ar_qk_norm_rope_backward: (dq, dk, dq_weight, dk_weight), lists of N tensors.
+
+    dq_out, dk_out: the gradients of ``qk_norm_rope``'s results, contiguous; the
+    rest as there.  dq, dk may be views of one matrix (the projection's gradient).
+    dq_weight[r], dk_weight[r] are rank r's partial sums (``Comm.allreduce``
+    completes them).  Results the caller gives no tensors for are allocated;
+    given ones are overwritten."""
+    n, device, dtype, dt, (rows, heads, kv, dim, rot), x, shared = _rope_inputs(q, k, q_weight, k_weight, pos, freq)
+    if k is None and not dk_out is dk is dk_weight is None:
+        raise ValueError("dk_out, dk and dk_weight need k")
+    go = [_layer_list(dq_out, n, (rows, heads, dim), dtype, device, "dq_out"),
+          _layer_list(dk_out, n, (rows, kv, dim), dtype, device, "dk_out") if k is not None else None]
+    given = [_head_list(dq, n, rows, (heads, dim), dtype, device, "dq") if dq is not None else None,
+             _head_list(dk, n, rows, (kv, dim), dtype, device, "dk") if dk is not None else None]
+    sums = [_layer_list(t, n, (dim,), dtype, device, what) if t is not None else None
+            for what, t in (("dq_weight", dq_weight), ("dk_weight", dk_weight))]
+    _on_device(device, stream)
+    scratch = _Scratch(stream, device)
+    outs, weights = [dq, dk], [dq_weight, dk_weight]
+    for i, width in enumerate((heads, kv)):
+        if i == 1 and k is None:
+            given[i] = (None, 0)
+            continue
+        if given[i] is None:
+            outs[i] = scratch.ranks(n, (rows, width, dim), dtype)
+            given[i] = (_PTRS[n](*[t.data_ptr() for t in outs[i]]), width * dim)
+        if sums[i] is None:
+            weights[i] = scratch.ranks(n, (dim,), dtype)
+            sums[i] = _PTRS[n](*[t.data_ptr() for t in weights[i]])
+    nbytes = _rope_workspace(n, rows, heads, kv, dim)
+    ws, ws_ptr = scratch.workspace(nbytes)
+    _check(_lib().ar_qk_norm_rope_backward(n, *go, *x, *shared, *given[0], *given[1], *sums, rows, heads, kv, dim, rot,
+                                           bool(pairs), eps, DTYPES[dt], ws_ptr, nbytes, _stream_handle(stream, device)),
+           "ar_qk_norm_rope_backward")
+    return outs[0], outs[1], weights[0], weights[1]
+
+
+class KVCache:
+    """ar_kv_cache: the 8-bit key/value cache of N ranks, held as lists of N
+    uint8 tensors: ``k`` [pages, kv_heads, page, head_dim] and ``v`` [pages,
+    kv_heads, head_dim, page] (e4m3 codes), ``k_scale`` and ``v_scale`` [pages,
+    kv_heads] (a code c stands for value(c) * 2^(scale - 127)).
+
+    ``KVCache(k, v, k_scale, v_scale)`` takes tensors of the caller's;
+    ``KVCache.empty(nranks, pages, kv_heads, head_dim, page=64)`` allocates
+    them on the current device (contents unset: a page counts from its first
+    write on)."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        torch = _torch()
+        n = len(k)
+        if not 1 <= n <= 8:
+            raise ValueError(f"k holds {n} rank buffers; a cache has 1 to 8 ranks")
+        if k[0].dim() != 4:
+            raise ValueError("k must be [pages, kv_heads, page, head_dim] on every rank")
+        pages, kv, page, dim = k[0].shape
+        self.device = k[0].get_device()
+        self.nranks, self.pages, self.kv_heads, self.page, self.head_dim = n, pages, kv, page, dim
+        self.k, self.v, self.k_scale, self.v_scale = tuple(k), tuple(v), tuple(k_scale), tuple(v_scale)
+        shapes = (("k", self.k, (pages, kv, page, dim)), ("v", self.v, (pages, kv, dim, page)),
+                  ("k_scale", self.k_scale, (pages, kv)), ("v_scale", self.v_scale, (pages, kv)))
+        # kept alive beside the record, which holds their addresses
+        self._ptrs = [_layer_list(ts, n, shape, torch.uint8, self.device, what) for what, ts, shape in shapes]
+        self.record = CacheRecord(*[ctypes.cast(p, ctypes.c_void_p) for p in self._ptrs], pages, page, kv, dim, n)
+
+    @classmethod
+    def empty(cls, nranks, pages, kv_heads, head_dim, page=64):
+        torch = _torch()
+
+        def make(*shape):
+            return [torch.empty(shape, dtype=torch.uint8, device="cuda") for _ in range(nranks)]
+        return cls(make(pages, kv_heads, page, head_dim), make(pages, kv_heads, head_dim, page), make(pages, kv_heads),
+                   make(pages, kv_heads))
+
+
+def _paged_rows(cache, table, first, at, rows, what):
+    """ar_paged_rows of a call's sequences."""
+    torch = _TORCH
+    for name, t, dim in (("table", table, 2), ("first", first, 1), (what, at, 1)):
+        if t.dtype is not torch.int32:
+            raise TypeError(f"{name} is {t.dtype}; the call needs {torch.int32}")
+        if t.dim() != dim or t.get_device() != cache.device or (t.stride(-1) != 1 and t.shape[-1] > 1):
+            raise ValueError(f"{name} must be an int32 tensor of {dim} dimension{'s' * (dim > 1)} on the cache's device, its last one contiguous")
+    seqs, width = table.shape
+    if first.shape[0] != seqs + 1 or at.shape[0] != seqs:
+        raise ValueError(f"table names {seqs} sequences, so first has {seqs + 1} entries and {what} {seqs}; "
+                         f"got {first.shape[0]} and {at.shape[0]}")
+    stride = table.stride(0) if seqs > 1 else width
+    if stride < width:
+        raise ValueError("table must not repeat or overlap its rows")
+    return PagedRows(table.data_ptr(), first.data_ptr(), at.data_ptr(), stride, width, seqs, rows)
+
+
+def cache_write(cache, k, v, table, first, start, stream=None):
+    """ar_cache_write: stores new keys and values in the cache's pages.
+
+    k[r], v[r]: [rows, kv_heads, head_dim], each row's heads side by side (views
+    of one projection's result are fine); table: int32 [seqs, width], the pages
+    of each sequence in order (a view of a wider table is fine); first: int32
+    [seqs + 1], sequence s has the rows first[s] .. first[s + 1] - 1; start:
+    int32 [seqs], the position of its first row.  fp32 and bf16.  A page must
+    belong to one sequence of the call; one that grows may change its scale,
+    which rounds its smallest earlier values again."""
+    n, device, dt = _layer_ranks(k, "k")
+    _cache_ranks(cache, n, device, "k")
+    if k[0].dim() != 3:
+        raise ValueError("k must be [rows, kv_heads, head_dim] on every rank")
+    rows, width, dtype = k[0].shape[0], (cache.kv_heads, cache.head_dim), k[0].dtype
+    kp, ks = _head_list(k, n, rows, width, dtype, device, "k")
+    vp, vs = _head_list(v, n, rows, width, dtype, device, "v")
+    paged = _paged_rows(cache, table, first, start, rows, "start")
+    _on_device(device, stream)
+    _check(_lib().ar_cache_write(cache.record, kp, ks, vp, vs, paged, DTYPES[dt], _stream_handle(stream, device)),
+           "ar_cache_write")
+
+
+def _cache_ranks(cache, n, device, what):
+    if n != cache.nranks:
+        raise ValueError(f"{what} holds {n} rank buffers; the cache has {cache.nranks}")
+    if device != cache.device:
+        raise ValueError(f"{what} and the cache must live on one device")
+
+
+def cache_read(cache, table, first, start, k, v, stream=None):
+    """ar_cache_read: (k, v) filled with tokens read back from the cache.
+
+    k[r], v[r]: contiguous [rows, kv_heads, head_dim], fp32 or bf16 (exact in
+    both); rows first[s] .. first[s + 1] - 1 receive the tokens of sequence s from
+    position start[s] on, zeros where the table names no page."""
+    n, device, dt = _layer_ranks(k, "k")
+    _cache_ranks(cache, n, device, "k")
+    if k[0].dim() != 3:
+        raise ValueError("k must be [rows, kv_heads, head_dim] on every rank")
+    shape, dtype = (k[0].shape[0], cache.kv_heads, cache.head_dim), k[0].dtype
+    kp = _layer_list(k, n, shape, dtype, device, "k")
+    vp = _layer_list(v, n, shape, dtype, device, "v")
+    paged = _paged_rows(cache, table, first, start, shape[0], "start")
+    _on_device(device, stream)
+    _check(_lib().ar_cache_read(cache.record, kp, vp, paged, DTYPES[dt], _stream_handle(stream, device)), "ar_cache_read")
+    return k, v
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_workspace(n, pages, page, kv, dim, seqs, rows, width, heads, max_rows, dt):
+    ptr = ctypes.cast(_PTRS[n](*[16] * n), ctypes.c_void_p)  # the sizes do not depend on the buffers
+    rec = CacheRecord(ptr, ptr, ptr, ptr, pages, page, kv, dim, n)
+    return _lib().ar_cache_attention_workspace(rec, seqs, rows, width, heads, max_rows, DTYPES[dt])
+
+
+def cache_attention(q, cache, table, first, length, scale=None, causal=True, window=0, max_rows=0, out=None, lse=None,
+                    stream=None):
+    """ar_cache_attention: out[r] = softmax(scale q k^T) v over the cache, lists
+    of N tensors [rows, heads, head_dim].
+
+    q[r]: [rows, heads, head_dim], each row's heads side by side; heads a
+    multiple of the cache's kv_heads (head h reads key/value head
+    h // (heads // kv_heads)); table, first as for ``cache_write``; length:
+    int32 [seqs], the cached tokens of each sequence, those of its own rows
+    among them: the last row stands at position length - 1.  causal False:
+    every row sees all of them (an encoder's states).  window: with causal, a row
+    sees the last `window` positions up to its own (0: all).  scale: 1 /
+    sqrt(head_dim) when None.  max_rows: the most rows a sequence has, where
+    the caller knows (it spares a launch).  lse: None, or N fp32 tensors
+    [rows, heads] that receive the log of the softmax denominators.  Rows that
+    see nothing have out 0 and lse minus infinity."""
+    n, device, dt = _layer_ranks(q, "q")
+    _cache_ranks(cache, n, device, "q")
+    dtype = q[0].dtype
+    if q[0].dim() != 3:
+        raise ValueError("q must be [rows, heads, head_dim] on every rank")
+    rows, heads, dim = q[0].shape
+    qp, qs = _head_list(q, n, rows, (heads, cache.head_dim), dtype, device, "q")
+    if heads < 1 or heads % cache.kv_heads:
+        raise ValueError(f"heads must be a multiple of the cache's {cache.kv_heads} kv_heads; got {heads}")
+    if window < 0 or max_rows < 0:
+        raise ValueError("window and max_rows must not be negative")
+    if window and not causal:
+        raise ValueError("window needs causal")
+    op = _layer_list(out, n, (rows, heads, dim), dtype, device, "out") if out is not None else None
+    lp = _layer_list(lse, n, (rows, heads), _TORCH.float32, device, "lse") if lse is not None else None
+    paged = _paged_rows(cache, table, first, length, rows, "length")
+    _on_device(device, stream)
+    scratch = _Scratch(stream, device)
+    if out is None:
+        out = scratch.ranks(n, (rows, heads, dim), dtype)
+        op = _PTRS[n](*[t.data_ptr() for t in out])
+    nbytes = _attention_workspace(n, cache.pages, cache.page, cache.kv_heads, dim, paged.seqs, rows, paged.width, heads,
+                                  max_rows, dt)
+    ws, ws_ptr = scratch.workspace(nbytes) if nbytes else (None, None)
+    _check(_lib().ar_cache_attention(cache.record, qp, qs, paged, op, lp, heads,
+                                     dim ** -0.5 if scale is None else scale, bool(causal), window, max_rows, DTYPES[dt],
+                                     ws_ptr, nbytes, _stream_handle(stream, device)), "ar_cache_attention")
+    return out
 
 
 def stream_ceiling(src, dst, sink=None, nt_loads=False, nt_stores=False, unroll=8, wg_per_cu=0, stream=None):

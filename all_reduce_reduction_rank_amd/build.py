@@ -13,7 +13,7 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libar.so")
-SOURCES = ("api.hip", "kernels.hip", "rmsnorm.hip", "noalloc.hip", "ceiling.hip", "ffn.hip", "xent.hip",
+SOURCES = ("api.hip", "kernels.hip", "rmsnorm.hip", "noalloc.hip", "ceiling.hip", "ffn.hip", "xent.hip", "rope.hip", "cache.hip", "attention.hip",
            "products.hip", "products_bf16.hip", "products_f32.hip")
 
 # -packed-fp32-ops: keep hipcc from fusing float adds into packed-FP32

@@ -1,0 +1,354 @@
+// cache.hip -- the 8-bit key/value cache of the attention operators: storing
+// new tokens (ar_cache_write) and reading tokens back (ar_cache_read).
+//
+// A page and head has one scale, a power of two: the smallest that brings the
+// largest new magnitude to 448 or less, and no smaller than what the page has.
+// Dividing by it is exact, so a code is one rounding of the value; when it
+// grows, the codes of the page's earlier tokens move by whole binades and only
+// those that become subnormal are rounded.
+//
+// Both are bound by memory, or by latency for a few tokens.  One workgroup owns
+// a page and head of keys or of values, so a scale has one writer and nothing is
+// atomic.  Values are kept with tokens running fastest, as the product with the
+// softmax weights reads them; a page is turned in LDS.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/ar.h"
+#include "device.hpp"
+#include "heads.hpp"
+#include "layer.hpp"
+
+using namespace ar;
+
+namespace {
+
+constexpr int THREADS = 256;
+
+struct CacheArgs {
+  const char* x[2][MAX_RANKS];  // new keys, values (write); results (read)
+  uint8_t* codes[2][MAX_RANKS];
+  uint8_t* scale[2][MAX_RANKS];
+  uint64_t pitch[2];  // bytes from row to row
+  Paged p;
+  uint32_t kv_heads;
+};
+
+// A workgroup's page: rows row .. row + (hi - lo) of the call are the page's
+// tokens lo .. hi - 1.
+struct Piece {
+  uint32_t row, lo, hi, id;
+};
+
+// Item -> page of a sequence.  A sequence's n tokens lie on at most
+// floor(n / page) + 2 pages.
+__device__ __forceinline__ bool piece_of(const Paged& p, uint64_t item, Piece* out) {
+  uint32_t row0, n;
+  uint64_t local;
+  const uint32_t s = find_sequence(p, item, 1, 1u << p.page_shift, 2, &row0, &n, &local);
+  if (s >= p.seqs) return false;
+  const int32_t at = p.at[s];
+  const uint64_t start = at < 0 ? 0 : (uint64_t)at, end = start + n;
+  const uint64_t j = (start >> p.page_shift) + local, t0 = j << p.page_shift;
+  if (t0 >= end) return false;
+  const uint64_t lo = start > t0 ? start : t0, hi = end < t0 + (1ull << p.page_shift) ? end : t0 + (1ull << p.page_shift);
+  out->row = row0 + (uint32_t)(lo - start);
+  out->lo = (uint32_t)(lo - t0);
+  out->hi = (uint32_t)(hi - t0);
+  out->id = page_id(p, s, j);
+  return true;
+}
+
+// Eight elements of a row.
+template <int DT>
+__device__ __forceinline__ void load8(const char* p, float* f) {
+  const uint4 v = ld16(p);
+  if (DT == DT_BF16) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  } else {
+    const uint4 u = ld16(p + 16);
+    const uint32_t w[8] = {v.x, v.y, v.z, v.w, u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(char* p, const float* f) {
+  if (DT == DT_BF16) {
+    st16(p, make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      st16(p + 16 * i, make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]),
+                                  __float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3])));
+  }
+}
+
+// Four codes at another scale: what they stand for, rounded again.
+__device__ __forceinline__ uint32_t rescaled(uint32_t codes, float from, float inv_to) {
+  float x[4];
+  values_of(codes, from, x);
+  return codes_of(x, inv_to);
+}
+
+// The workgroup's largest value, and thread 0's byte for everyone.
+__device__ float block_max(float m, float* s, uint32_t* byte) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = m;
+  if (threadIdx.x == 0) s[THREADS / 64] = __uint_as_float(*byte);
+  __syncthreads();
+  *byte = __float_as_uint(s[THREADS / 64]);
+  m = s[0];
+#pragma unroll
+  for (int w = 1; w < THREADS / 64; ++w) m = fmaxf(m, s[w]);
+  return m;
+}
+
+template <int DT, int DIM>
+__global__ __launch_bounds__(THREADS) void write_kernel(CacheArgs a) {
+  constexpr uint32_t ES = DT == DT_BF16 ? 2 : 4, LANES = DIM / 8;  // lanes of a token
+  constexpr uint32_t PITCH = DIM + 4;                              // of a token's codes in LDS
+  extern __shared__ uint8_t tile[];                                // values: [page][PITCH]
+  __shared__ float maxima[THREADS / 64 + 1];
+  const uint32_t kind = blockIdx.y & 1, r = blockIdx.z, head = blockIdx.y >> 1;
+  Piece pc;
+  if (!piece_of(a.p, blockIdx.x, &pc) || pc.id >= a.p.pages) return;
+  const uint32_t page = 1u << a.p.page_shift, count = pc.hi - pc.lo;
+  const char* x = a.x[kind][r] + (uint64_t)pc.row * a.pitch[kind] + (uint64_t)head * (DIM * ES);
+  uint8_t* codes = a.codes[kind][r] + page_at(pc.id, a.kv_heads, head, page * DIM);
+  uint8_t* scale = a.scale[kind][r] + (uint64_t)pc.id * a.kv_heads + head;
+  // one thread reads the byte and writes it, in that order
+  uint32_t held = threadIdx.x == 0 ? *scale : 0;
+  const uint32_t lane = threadIdx.x % LANES;
+
+  float m = 0.f;
+  for (uint32_t i = threadIdx.x / LANES; i < count; i += THREADS / LANES) {
+    float f[8];
+    load8<DT>(x + i * a.pitch[kind] + lane * 8 * ES, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float v = fabsf(f[e]);
+      m = fmaxf(m, v < __builtin_inff() ? v : 0.f);
+    }
+  }
+  uint32_t byte = scale_byte(block_max(m, maxima, &held));
+  const uint32_t before = held < SCALE_MIN ? SCALE_MIN : held > SCALE_MAX ? SCALE_MAX : held;
+  const bool grows = pc.lo > 0 && byte > before;
+  if (pc.lo > 0 && byte < before) byte = before;
+  const float inv = scale_of(254 - byte < SCALE_MIN ? SCALE_MIN : 254 - byte), from = scale_of(before);
+  const float half = 254 - byte < SCALE_MIN ? 0.5f : 1.f;  // 2^-127 is not a normal number
+  if (threadIdx.x == 0) *scale = (uint8_t)byte;
+
+  for (uint32_t i = threadIdx.x / LANES; i < count; i += THREADS / LANES) {
+    float f[8];
+    load8<DT>(x + i * a.pitch[kind] + lane * 8 * ES, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] *= half;
+    const uint2 w = make_uint2(codes_of(f, inv), codes_of(f + 4, inv));
+    if (kind == 0) {
+      *(uint2*)(codes + (pc.lo + i) * DIM + lane * 8) = w;
+    } else {
+      uint32_t* t = (uint32_t*)(tile + i * PITCH + lane * 8);
+      t[0] = w.x, t[1] = w.y;
+    }
+  }
+  if (kind == 0) {
+    if (grows)
+      for (uint32_t i = threadIdx.x * 4; i < pc.lo * DIM; i += THREADS * 4) {
+        uint32_t* at = (uint32_t*)(codes + i);
+        *at = rescaled(*at, from * half, inv);
+      }
+    return;
+  }
+  __syncthreads();
+  // Values: dword q of dimension d holds tokens 4 q .. 4 q + 3.
+  const uint32_t q0 = grows ? 0 : pc.lo / 4, q1 = (pc.hi + 3) / 4, words = q1 - q0;
+  for (uint32_t i = threadIdx.x; i < words * DIM; i += THREADS) {
+    const uint32_t d = i / words, q = q0 + i - d * words;
+    uint32_t* at = (uint32_t*)(codes + d * page + q * 4);
+    uint32_t w = 0;
+    const bool whole = q * 4 >= pc.lo && q * 4 + 4 <= pc.hi;
+    if (!whole) {
+      w = *at;
+      const uint32_t old = grows ? rescaled(w, from * half, inv) : w;
+      // tokens before lo are the page's, those from hi on stay as they are
+#pragma unroll
+      for (uint32_t e = 0; e < 4; ++e)
+        if (q * 4 + e < pc.lo) w = (w & ~(0xffu << (8 * e))) | (old & (0xffu << (8 * e)));
+    }
+#pragma unroll
+    for (uint32_t e = 0; e < 4; ++e) {
+      const uint32_t t = q * 4 + e;
+      if (t >= pc.lo && t < pc.hi) w = (w & ~(0xffu << (8 * e))) | ((uint32_t)tile[(t - pc.lo) * PITCH + d] << (8 * e));
+    }
+    *at = w;
+  }
+}
+
+template <int DT, int DIM>
+__global__ __launch_bounds__(THREADS) void read_kernel(CacheArgs a) {
+  constexpr uint32_t ES = DT == DT_BF16 ? 2 : 4, LANES = DIM / 8, PITCH = DIM + 4;
+  extern __shared__ uint8_t tile[];
+  const uint32_t kind = blockIdx.y & 1, r = blockIdx.z, head = blockIdx.y >> 1;
+  Piece pc;
+  if (!piece_of(a.p, blockIdx.x, &pc)) return;
+  const uint32_t page = 1u << a.p.page_shift, count = pc.hi - pc.lo;
+  const bool there = pc.id < a.p.pages;
+  char* x = (char*)a.x[kind][r] + (uint64_t)pc.row * a.pitch[kind] + (uint64_t)head * (DIM * ES);
+  const uint8_t* codes = a.codes[kind][r] + page_at(there ? pc.id : 0, a.kv_heads, head, page * DIM);
+  float scale = 0.f;
+  if (there) {
+    const uint32_t byte = a.scale[kind][r][(uint64_t)pc.id * a.kv_heads + head];
+    scale = scale_of(byte < SCALE_MIN ? SCALE_MIN : byte > SCALE_MAX ? SCALE_MAX : byte);
+  }
+  if (kind == 1 && there) {
+    const uint32_t q0 = pc.lo / 4, words = (pc.hi + 3) / 4 - q0;
+    for (uint32_t i = threadIdx.x; i < words * DIM; i += THREADS) {
+      const uint32_t d = i / words, q = i - d * words;
+      const uint32_t w = *(const uint32_t*)(codes + d * page + (q0 + q) * 4);
+#pragma unroll
+      for (uint32_t e = 0; e < 4; ++e) tile[(q * 4 + e) * PITCH + d] = (uint8_t)(w >> (8 * e));
+    }
+    __syncthreads();
+  }
+  const uint32_t lane = threadIdx.x % LANES;
+  for (uint32_t i = threadIdx.x / LANES; i < count; i += THREADS / LANES) {
+    uint2 w = make_uint2(0, 0);
+    if (there) {
+      if (kind == 0) {
+        w = *(const uint2*)(codes + (pc.lo + i) * DIM + lane * 8);
+      } else {
+        const uint32_t* t = (const uint32_t*)(tile + (i + pc.lo % 4) * PITCH + lane * 8);
+        w = make_uint2(t[0], t[1]);
+      }
+    }
+    float f[8];
+    values_of(w.x, scale, f);
+    values_of(w.y, scale, f + 4);
+    store8<DT>(x + i * a.pitch[kind] + lane * 8 * ES, f);
+  }
+}
+
+}  // namespace
+
+namespace ar {
+
+ar_status check_cache(const ar_kv_cache* c) {
+  if (!c || c->nranks < 1 || c->nranks > MAX_RANKS || !c->k || !c->v || !c->k_scale || !c->v_scale) return AR_ERR_INVALID;
+  if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return AR_ERR_UNSUPPORTED;
+  if (!head_dim_ok(c->head_dim)) return AR_ERR_UNSUPPORTED;
+  if (c->kv_heads < 1) return AR_ERR_INVALID;
+  if (c->kv_heads > MAX_HEADS || c->pages >= (1ull << 31)) return AR_ERR_TOO_LARGE;
+  if (c->pages * c->kv_heads * c->page * c->head_dim >= (1ull << 47)) return AR_ERR_TOO_LARGE;
+  return AR_OK;
+}
+
+ar_status check_rows(const ar_kv_cache* c, const ar_paged_rows* p) {
+  if (!p) return AR_ERR_INVALID;
+  if (p->rows > LAYER_MAX_ROWS || p->seqs > (1ull << 20) || p->width > (1ull << 31) ||
+      p->width * c->page >= (1ull << 31) || p->table_stride >= (1ull << 31))
+    return AR_ERR_TOO_LARGE;
+  if (p->seqs && (!p->first || !p->at || (uintptr_t)p->first % 4 || (uintptr_t)p->at % 4)) return AR_ERR_INVALID;
+  if (p->seqs && p->width && (!p->table || (uintptr_t)p->table % 4 || (p->seqs > 1 && p->table_stride < p->width)))
+    return AR_ERR_INVALID;
+  return AR_OK;
+}
+
+Paged paged_of(const ar_kv_cache* c, const ar_paged_rows* p) {
+  Paged r;
+  r.table = p->table;
+  r.first = p->first;
+  r.at = p->at;
+  r.table_stride = p->table_stride;
+  r.width = (uint32_t)p->width;
+  r.seqs = (uint32_t)p->seqs;
+  r.rows = (uint32_t)p->rows;
+  r.pages = (uint32_t)c->pages;
+  r.page_shift = (uint32_t)__builtin_ctzll(c->page);
+  return r;
+}
+
+void add_cache(LayerBuffers& b, const ar_kv_cache* c, bool written) {
+  const uint64_t heads = c->pages * c->kv_heads, bytes = heads * c->page * c->head_dim;
+  for (int r = 0; r < c->nranks; ++r) {
+    const void* codes[2] = {c->k[r], c->v[r]};
+    const void* scales[2] = {c->k_scale[r], c->v_scale[r]};
+    for (int i = 0; i < 2; ++i) {
+      if (written) b.out(codes[i], bytes), b.out(scales[i], heads, 1);
+      else b.in(codes[i], bytes), b.in(scales[i], heads, 1);
+    }
+  }
+}
+
+void add_rows(LayerBuffers& b, const ar_paged_rows* p) {
+  b.in(p->first, p->seqs ? (p->seqs + 1) * 4 : 0, 4);
+  b.in(p->at, p->seqs * 4, 4);
+  b.in(p->table, p->seqs && p->width ? ((p->seqs - 1) * p->table_stride + p->width) * 4 : 0, 4);
+}
+
+}  // namespace ar
+
+namespace {
+
+// What a write and a read share: checks, arguments, the grid.
+ar_status cache_call(const ar_kv_cache* c, const void* const* k, size_t k_stride, const void* const* v, size_t v_stride,
+                     const ar_paged_rows* p, int dtype, bool write, hipStream_t stream) {
+  ar_status st = check_cache(c);
+  if (st == AR_OK) st = check_rows(c, p);
+  if (st != AR_OK) return st;
+  if (dtype < 0 || dtype > 2 || !k || !v) return AR_ERR_INVALID;
+  if (dtype == DT_I32) return AR_ERR_UNSUPPORTED;
+  if (p->rows == 0 || p->seqs == 0) return AR_OK;
+  const uint64_t es = dtype == DT_BF16 ? 2 : 4, width = c->kv_heads * c->head_dim;
+  if (!stride_ok(k_stride, width, es) || !stride_ok(v_stride, width, es)) return AR_ERR_INVALID;
+  CacheArgs a;
+  LayerBuffers b;
+  for (int r = 0; r < c->nranks; ++r) {
+    a.x[0][r] = (const char*)k[r];
+    a.x[1][r] = (const char*)v[r];
+    a.codes[0][r] = (uint8_t*)c->k[r];
+    a.codes[1][r] = (uint8_t*)c->v[r];
+    a.scale[0][r] = (uint8_t*)c->k_scale[r];
+    a.scale[1][r] = (uint8_t*)c->v_scale[r];
+    const uint64_t kb = span_bytes(p->rows, k_stride, width, es), vb = span_bytes(p->rows, v_stride, width, es);
+    if (write) b.in(k[r], kb), b.in(v[r], vb);
+    else b.out(k[r], kb), b.out(v[r], vb);
+  }
+  add_cache(b, c, write);
+  add_rows(b, p);
+  if (!b.ok()) return AR_ERR_INVALID;
+  a.pitch[0] = k_stride * es;
+  a.pitch[1] = v_stride * es;
+  a.p = paged_of(c, p);
+  a.kv_heads = (uint32_t)c->kv_heads;
+  const dim3 grid((uint32_t)item_count(p->rows, p->seqs, 1, c->page, 2), 2 * (uint32_t)c->kv_heads, (uint32_t)c->nranks);
+  const uint32_t lds = (uint32_t)(c->page * (c->head_dim + 4));
+  by_head_dim(dtype, c->head_dim, [&](auto dt, auto dim) {
+    if (write) write_kernel<decltype(dt)::value, decltype(dim)::value><<<grid, THREADS, lds, stream>>>(a);
+    else read_kernel<decltype(dt)::value, decltype(dim)::value><<<grid, THREADS, lds, stream>>>(a);
+  });
+  return hipGetLastError() == hipSuccess ? AR_OK : AR_ERR_HIP;
+}
+
+}  // namespace
+
+extern "C" {
+
+ar_status ar_cache_write(const ar_kv_cache* cache, const void* const* k, size_t k_stride, const void* const* v,
+                         size_t v_stride, const ar_paged_rows* rows, ar_dtype dtype, ar_stream_t stream) {
+  return cache_call(cache, k, k_stride, v, v_stride, rows, (int)dtype, true, (hipStream_t)stream);
+}
+
+ar_status ar_cache_read(const ar_kv_cache* cache, void* const* k, void* const* v, const ar_paged_rows* rows,
+                        ar_dtype dtype, ar_stream_t stream) {
+  const size_t width = cache ? cache->kv_heads * cache->head_dim : 0;
+  return cache_call(cache, (const void* const*)k, width, (const void* const*)v, width, rows, (int)dtype, false,
+                    (hipStream_t)stream);
+}
+
+}  // extern "C"

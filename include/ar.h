@@ -451,6 +451,138 @@ ar_status ar_linear_cross_entropy_backward(int nranks, const float* grad_loss, c
                                            ar_dtype dtype, size_t piece, void* workspace, size_t workspace_bytes,
                                            ar_stream_t stream);
 
+/* ---- Attention of a tensor-parallel layer: the operators between the column
+ * split of the query, key and value projection, which leaves every rank its
+ * share of the heads, and the row split of the output projection, whose
+ * partial sums an all-reduce adds ([Q] "Direct answer").  The conventions of the
+ * layer operators above hold (HOST arrays of N DEVICE pointers, current
+ * device, order on `stream`, nothing allocated, no overlap of outputs with
+ * other buffers, errors, AR_F32 or AR_BF16), with these additions: rank
+ * buffers [rows, heads, head_dim] named with a stride lie `stride` elements
+ * from one row to the next (at least heads * head_dim, a multiple of 16
+ * bytes, below 2^31), so queries, keys and values may stay where one
+ * projection left them; the others are contiguous.  Vectors shared by all
+ * ranks are DEVICE pointers, aligned to their elements.  head_dim is 64, 128 or
+ * 256 (AR_ERR_UNSUPPORTED otherwise); heads is a multiple of kv_heads, at most
+ * 1024; query head h reads key/value head h / (heads / kv_heads).  rows *
+ * heads at most 2^30. */
+
+/* Norms of queries and keys for each head, with the rotation to their
+ * positions in the same pass: for every row t and head
+ *   n = x / sqrt(mean(x^2) + eps),  y = n * weight          (head_dim values)
+ *   a(j) = pos[t] * freq[j];  out = y with the pairs (y_j, y_j') of the first
+ *   `rot` values turned by a(j): (y_j cos a - y_j' sin a, y_j' cos a + y_j sin a)
+ * pairs 0: j' = j + rot / 2, j < rot / 2;  pairs 1: neighbours 2 j, 2 j + 1.
+ * weight: head_dim elements, one vector for queries and one for keys.
+ * pos: `rows` int64; freq: rot / 2 floats; the angle is computed in fp64, the
+ * rest in fp32, rounded once.  rot: a multiple of 16, 0 to head_dim (0: norms
+ * alone; freq and pos may be NULL).  kv_heads may be 0 here (queries alone;
+ * k, k_weight and k_out may be NULL), and heads need not be a multiple of it. */
+ar_status ar_qk_norm_rope(int nranks, const void* const* q, size_t q_stride, const void* const* k, size_t k_stride,
+                          const void* q_weight, const void* k_weight, const int64_t* pos, const float* freq,
+                          void* const* q_out, void* const* k_out, size_t rows, size_t heads, size_t kv_heads,
+                          size_t head_dim, size_t rot, int pairs, float eps, ar_dtype dtype, ar_stream_t stream);
+
+/* Workspace bytes of ar_qk_norm_rope_backward; 0 for arguments it refuses, and
+ * for rows 0. */
+size_t ar_qk_norm_rope_workspace(int nranks, size_t rows, size_t heads, size_t kv_heads, size_t head_dim);
+
+/* Gradients of ar_qk_norm_rope.  dq_out, dk_out: gradients of its outputs; q, k:
+ * its inputs.  With g the gradient turned back by the same angles:
+ *   dn = g * weight;  dx = (dn - n * mean(dn * n)) / sqrt(mean(x^2) + eps)
+ *   dweight[r] = sum over rows and heads of g * n
+ * dq, dk have strides as q and k do, and may be the columns of one matrix.
+ * dq_weight[r], dk_weight[r] are rank r's partial sums (an all-reduce
+ * completes them), summed in fp32 in a fixed order and rounded once.  rows 0:
+ * the weight gradients become zeros. */
+ar_status ar_qk_norm_rope_backward(int nranks, const void* const* dq_out, const void* const* dk_out,
+                                   const void* const* q, size_t q_stride, const void* const* k, size_t k_stride,
+                                   const void* q_weight, const void* k_weight, const int64_t* pos, const float* freq,
+                                   void* const* dq, size_t dq_stride, void* const* dk, size_t dk_stride,
+                                   void* const* dq_weight, void* const* dk_weight, size_t rows, size_t heads,
+                                   size_t kv_heads, size_t head_dim, size_t rot, int pairs, float eps, ar_dtype dtype,
+                                   void* workspace, size_t workspace_bytes, ar_stream_t stream);
+
+/* A key/value cache in 8 bits, in pages of `page` tokens (16, 32, 64 or 128).
+ * Per rank (arrays of nranks DEVICE pointers, 16-byte aligned; the scales to
+ * a byte):
+ *   k        [pages, kv_heads, page, head_dim]  e4m3 codes (4 exponent bits, bias
+ *            7, 3 mantissa bits, largest value 448, 0x7f and 0xff: NaN)
+ *   v        [pages, kv_heads, head_dim, page]  e4m3 codes, tokens fastest
+ *   k_scale, v_scale  [pages, kv_heads]  one byte b for each page and head
+ * A code c stands for value(c) * 2^(b - 127).  Scales are powers of two, so a
+ * page whose scale grows keeps the bits of all but its smallest values.  pages at
+ * most 2^31 - 1, pages * kv_heads * page * head_dim below 2^47. */
+typedef struct {
+  void* const* k;
+  void* const* v;
+  void* const* k_scale;
+  void* const* v_scale;
+  size_t pages, page, kv_heads, head_dim;
+  int nranks;
+} ar_kv_cache;
+
+/* The sequences of a call: sequence s has the rows [first[s], first[s + 1]) of
+ * the call's row buffers, and its tokens j * page .. of page table[s *
+ * table_stride + j], j < width.
+ *   first  seqs + 1 int32, not decreasing, within [0, rows]; rows before
+ *          first[0] and from first[seqs] on are neither read nor written
+ *   table  int32; an entry outside [0, pages) names no page
+ *   at     seqs int32: what the call says (below 0 is taken as 0)
+ * All three are DEVICE vectors, read when the stream reaches the call; entries
+ * outside these ranges read and write nothing outside the buffers.  width *
+ * page below 2^31, seqs at most 2^20. */
+typedef struct {
+  const int32_t* table;
+  const int32_t* first;
+  const int32_t* at;
+  size_t table_stride, width, seqs, rows;
+} ar_paged_rows;
+
+/* Stores new keys and values: row first[s] + i is token at[s] + i of sequence s.
+ * For each page and head written, with m the largest finite magnitude of the
+ * new values (k and v on their own):
+ *   b' = the smallest b in [1, 254] with m <= 448 * 2^(b - 127)
+ *   b <- b' if the page's first token is among the new ones, else max(b, b')
+ * new values become the codes nearest to x / 2^(b - 127), ties to even
+ * (infinities and NaN: 0x7f); if b grew, the codes of the page's earlier tokens
+ * become the codes nearest to what they stood for.  Tokens beyond width * page
+ * or on no page are dropped.  A page must belong to one sequence of the call.
+ * Codes of other tokens are left as they were. */
+ar_status ar_cache_write(const ar_kv_cache* cache, const void* const* k, size_t k_stride, const void* const* v,
+                         size_t v_stride, const ar_paged_rows* rows, ar_dtype dtype, ar_stream_t stream);
+
+/* Reads tokens back: row first[s] + i of k[r] and v[r] ([rows, kv_heads,
+ * head_dim], contiguous) receives token at[s] + i of sequence s, exact in either
+ * dtype; zeros for tokens beyond width * page or on no page. */
+ar_status ar_cache_read(const ar_kv_cache* cache, void* const* k, void* const* v, const ar_paged_rows* rows,
+                        ar_dtype dtype, ar_stream_t stream);
+
+/* Workspace bytes of ar_cache_attention; 0 for arguments it refuses, and where
+ * it needs none. */
+size_t ar_cache_attention_workspace(const ar_kv_cache* cache, size_t seqs, size_t rows, size_t width, size_t heads,
+                                    size_t max_rows, ar_dtype dtype);
+
+/* Attention over the cache.  Sequence s has L = min(at[s], width * page) cached
+ * tokens, and n = first[s + 1] - first[s] query rows; row i of them stands at
+ * position P = L - n + i (its own key and value are in the cache already).
+ *   z[j] = scale * q . k[j] over the tokens j < L on a page that the row sees:
+ *          causal 0: all;  causal 1: j <= P and, with window > 0, j > P - window
+ *   lse = log sum_j exp(z[j]);  out = sum_j exp(z[j] - lse) v[j]
+ * A row that sees no token has out 0 and lse minus infinity.  What tokens that
+ * a row does not see hold, NaN among it, does not reach the row.
+ * q[r] [rows, heads, head_dim] with q_stride; out[r] [rows, heads, head_dim];
+ * lse NULL, or N fp32 buffers [rows, heads].  out[r] is what rank r multiplies
+ * by its columns of the output projection.  window needs causal.  max_rows: no
+ * sequence has more rows than this (0: unknown); it chooses kernels and changes
+ * no result beyond the order of sums.  Sums, maxima and products with q are fp32
+ * or better; with AR_BF16 the weights exp(z - m) are rounded to bf16 before they
+ * are multiplied by v (a second term holds the rest where rows are few). */
+ar_status ar_cache_attention(const ar_kv_cache* cache, const void* const* q, size_t q_stride,
+                             const ar_paged_rows* rows, void* const* out, float* const* lse, size_t heads,
+                             float scale, int causal, size_t window, size_t max_rows, ar_dtype dtype,
+                             void* workspace, size_t workspace_bytes, ar_stream_t stream);
+
 /* Static description of a status code. */
 const char* ar_status_string(ar_status status);
 
