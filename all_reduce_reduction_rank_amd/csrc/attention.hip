@@ -25,8 +25,10 @@ using namespace ar;
 namespace {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
 
 constexpr uint32_t TOKENS = 64;  // of a step along the cache
 constexpr float LN2 = 0.69314718055994530942f, LOG2E = 1.44269504088896340736f;
@@ -44,9 +46,13 @@ struct AttnArgs {
   uint32_t kv_heads, heads, group;
   uint32_t splits, min_steps;  // shares of a tile's tokens: at most `splits`, of at least `min_steps` steps
   uint32_t tiles;              // row tiles of a head (bound)
-  float scale;                 // times log2(e)
+  // z in units of log2: factor * (q . k), factor > 0; a negative scale turns the
+  // queries' signs instead (a multiply-add from the raw product then gives the
+  // exponent, and the largest product is the largest z)
+  float factor;
+  uint32_t flip;
   int32_t causal;
-  uint32_t window;
+  int32_t window;
   float* part;   // [rank][kv head][tile][split][rows of a tile][dim]: sum p v of a share
   float2* stat;  // [rank][kv head][tile][split][rows of a tile]: its m (of log2) and sum p
 };
@@ -55,35 +61,35 @@ struct AttnArgs {
 struct Tile {
   uint32_t s, row0, n;  // sequence, its first row in the call, its rows
   uint32_t r0, rows;    // packed rows r0 .. r0 + rows - 1
-  int64_t length;       // cached tokens
-  int64_t lo, hi;       // tokens some row sees lie in [lo, hi)
+  int32_t length;       // cached tokens (below 2^31, as every position)
+  int32_t lo, hi;       // tokens some row sees lie in [lo, hi)
   uint32_t begin, steps;  // steps of TOKENS tokens from token `begin` on
 };
 
 __device__ __forceinline__ bool tile_of(const AttnArgs& a, uint32_t tile, uint32_t bm, Tile* t) {
   uint64_t local;
-  t->s = find_sequence(a.p, tile, a.group, bm, 1, &t->row0, &t->n, &local);
+  int32_t len;
+  t->s = find_sequence(a.p, tile, a.group, bm, 1, &t->row0, &t->n, &local, &len);
   if (t->s >= a.p.seqs) return false;
   const uint64_t rows = (uint64_t)t->n * a.group, r0 = local * bm;
   if (r0 >= rows) return false;
   t->r0 = (uint32_t)r0;
   t->rows = (uint32_t)(rows - r0 < bm ? rows - r0 : bm);
-  const int64_t cap = (int64_t)a.p.width << a.p.page_shift;
-  int64_t len = a.p.at[t->s];
+  const int32_t cap = (int32_t)(a.p.width << a.p.page_shift);
   len = len < 0 ? 0 : len < cap ? len : cap;
   t->length = len;
   t->lo = 0;
   t->hi = len;
   if (a.causal) {
-    const int64_t last = len - t->n + (t->r0 + t->rows - 1) / a.group + 1;
+    const int32_t n = (int32_t)t->n, last = len - n + (int32_t)((t->r0 + t->rows - 1) / a.group) + 1;
     t->hi = last < 0 ? 0 : last < len ? last : len;
     if (a.window) {
-      const int64_t first = len - t->n + t->r0 / a.group + 1 - (int64_t)a.window;
-      t->lo = first < 0 ? 0 : first < t->hi ? first : t->hi;
+      const int32_t end = len - n + (int32_t)(t->r0 / a.group) + 1, first = end > a.window ? end - a.window : 0;
+      t->lo = first < t->hi ? first : t->hi;
     }
   }
-  t->begin = (uint32_t)(t->lo & ~(int64_t)(TOKENS - 1));
-  t->steps = t->hi > t->lo ? (uint32_t)((t->hi - t->begin + TOKENS - 1) / TOKENS) : 0;
+  t->begin = (uint32_t)t->lo & ~(TOKENS - 1);
+  t->steps = t->hi > t->lo ? ((uint32_t)t->hi - t->begin + TOKENS - 1) / TOKENS : 0;
   return true;
 }
 
@@ -120,23 +126,27 @@ __device__ __forceinline__ void split8(float* x, v8bf* out) {
   }
 }
 
-// A bf16 pair's numbers that are not finite become 1 and the others 0
-// (count), or they become 0 and the others stay.
-__device__ __forceinline__ v8bf sift(v8bf x, bool count) {
-  v4u w = __builtin_bit_cast(v4u, x);
+// x rounded to bf16, and the sum of what that gives added to *sum.
+__device__ __forceinline__ v8bf rounded8(const float* x, float* sum) {
+  const v2bf one = {(__bf16)1.f, (__bf16)1.f};
+  v4u w;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = (w[i] & 0x7f80u) == 0x7f80u ? 0xffffu : 0u, hi = (w[i] & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u;
-    w[i] = count ? (0x3f803f80u & (lo | hi)) : (w[i] & ~(lo | hi));
+    w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+    *sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2bf, (uint32_t)w[i]), one, *sum, false);
   }
   return __builtin_bit_cast(v8bf, w);
 }
 
-__device__ __forceinline__ float byte_scale(uint32_t b) { return scale_of(b < SCALE_MIN ? SCALE_MIN : b > SCALE_MAX ? SCALE_MAX : b); }
+__device__ __forceinline__ uint4 flipped(const uint4& w, uint32_t f) { return make_uint4(w.x ^ f, w.y ^ f, w.z ^ f, w.w ^ f); }
+
+__device__ __forceinline__ uint32_t clamp_byte(uint32_t b) { return b < SCALE_MIN ? SCALE_MIN : b > SCALE_MAX ? SCALE_MAX : b; }
+__device__ __forceinline__ float byte_scale(uint32_t b) { return scale_of(clamp_byte(b)); }
+__device__ __forceinline__ float finite(float x) { return x < INFINITY ? x : 0.f; }  // x >= 0 or NaN
 
 // Bytes of a 16-token block of codes that lie outside tokens [lo, hi) become 0;
 // `at` is the block's first token.
-__device__ __forceinline__ uint4 clear_outside(uint4 w, int64_t at, int64_t lo, int64_t hi) {
+__device__ __forceinline__ uint4 clear_outside(uint4 w, int32_t at, int32_t lo, int32_t hi) {
   uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -144,6 +154,82 @@ __device__ __forceinline__ uint4 clear_outside(uint4 w, int64_t at, int64_t lo, 
     for (int e = 0; e < 4; ++e)
       if (at + 4 * i + e < lo || at + 4 * i + e >= hi) x[i] &= ~(0xffu << (8 * e));
   return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
+// A tile's rows over tokens [t0, t1), a row per wave, in plain loops: what a row
+// does not see is not touched.  For tiles that hold a NaN.
+template <int DT, int DIM>
+__device__ __forceinline__ void plain_rows(const AttnArgs& a, const Tile& t, uint32_t h, uint32_t r, uint32_t t0,
+                                           uint32_t t1, bool shared, uint64_t slot) {
+  constexpr int PER = DIM / 64;  // dimensions of a lane
+  const uint32_t lane = threadIdx.x & 63, in_page = (1u << a.p.page_shift) - 1, page_bytes = DIM << a.p.page_shift;
+#pragma nounroll
+  for (uint32_t row = threadIdx.x >> 6; row < t.rows; row += 4) {
+    const uint32_t packed = t.r0 + row, qr = packed / a.group, head = h * a.group + packed % a.group;
+    int32_t see0 = 0, see1 = t.length;
+    if (a.causal) {
+      const int32_t e = t.length - (int32_t)t.n + (int32_t)qr + 1;
+      see1 = e < 0 ? 0 : e;
+      if (a.window && e > a.window) see0 = e - a.window;
+    }
+    const char* q = a.q[r] + (uint64_t)(t.row0 + qr) * a.q_pitch + (uint64_t)head * DIM * Elem<DT>::size;
+    float m = -INFINITY, l = 0.f, o[PER] = {};
+#pragma nounroll
+    for (uint32_t base = t0; base < t1; base += 64) {
+      const uint32_t tok = base + lane, id = page_id(a.p, t.s, tok >> a.p.page_shift);
+      const bool seen = (int32_t)tok >= see0 && (int32_t)tok < see1 && id < a.p.pages;
+      float z = -INFINITY, vs = 0.f;
+      if (seen) {
+        const uint8_t* k = a.k[r] + page_at(id, a.kv_heads, h, page_bytes) + (tok & in_page) * DIM;
+        const float ks = byte_scale(a.k_scale[r][(uint64_t)id * a.kv_heads + h]);
+        vs = byte_scale(a.v_scale[r][(uint64_t)id * a.kv_heads + h]);
+        z = 0.f;
+#pragma nounroll
+        for (int d = 0; d < DIM; d += 4) {
+          float x[4];
+          values_of(*(const uint32_t*)(k + d), ks, x);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z += Elem<DT>::ldf(q + (d + e) * Elem<DT>::size) * x[e];
+        }
+        if (a.flip) z = -z;
+      }
+      float top = z;
+#pragma unroll
+      for (int s = 32; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
+      const float next = fmaxf(m, top), shift = next == -INFINITY ? 0.f : next * a.factor;
+      const float f = next == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - next) * a.factor);
+      m = next;
+      const float p = seen ? __builtin_amdgcn_exp2f(__builtin_fmaf(z, a.factor, -shift)) : 0.f;
+      l = l * f + p;
+#pragma unroll
+      for (int x = 0; x < PER; ++x) o[x] *= f;
+      const uint64_t who = __ballot(seen);
+#pragma nounroll
+      for (int j = 0; j < 64; ++j) {
+        if (!(who >> j & 1)) continue;
+        const float pj = __shfl(p, j), sj = __shfl(vs, j);
+        const uint8_t* v = a.v[r] + page_at(__shfl((int)id, j), a.kv_heads, h, page_bytes) + ((base + j) & in_page);
+#pragma unroll
+        for (int x = 0; x < PER; ++x) {
+          float y[4];
+          values_of(v[(lane + 64 * x) << a.p.page_shift], sj, y);
+          o[x] += pj * y[0];
+        }
+      }
+    }
+#pragma unroll
+    for (int s = 32; s > 0; s >>= 1) l += __shfl_xor(l, s);
+    const float inv = shared ? 1.f : l == 0.f ? 0.f : 1.f / l;
+    const uint64_t at = ((uint64_t)(t.row0 + qr) * a.heads + head);
+#pragma unroll
+    for (int x = 0; x < PER; ++x) {
+      if (shared) a.part[(slot + row) * DIM + lane + 64 * x] = o[x];
+      else Elem<DT>::stf(a.out[r] + (at * DIM + lane + 64 * x) * Elem<DT>::size, o[x] * inv);
+    }
+    if (lane) continue;
+    if (shared) a.stat[slot + row] = make_float2(m * a.factor, l);
+    else if (a.lse[r]) a.lse[r][at] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m * a.factor) + log2f(l)) * LN2;
+  }
 }
 
 // ---- few rows: 16 rows per workgroup, its four waves share the tokens ----
@@ -158,18 +244,17 @@ __device__ __forceinline__ uint4 clear_outside(uint4 w, int64_t at, int64_t lo, 
 // order of tokens; both are chosen so that lanes load contiguous bytes and
 // weights stay in the lanes that hold them.  With lane = 16 g + c:
 //   keys   step a (0..3), row c of the operand: token 16 (c / 4) + 4 a + c % 4,
-//          k: dim / 4 contiguous values from g dim / 4 on
+//          k: 16 contiguous values of every 64, from 16 g on, so that a load
+//          takes 64 contiguous bytes of each key
 //   S^T    lane (g, c) holds tokens 16 g + 4 a + i (i = 0..3) of row c
 //   values operand row c: dimension 16 t + c, k of group g: tokens 16 g ..
 //          16 g + 15, which are one 16-byte load (a page is whole blocks of 16)
 //   O^T    lane (g, c) holds dimensions 16 t + 4 g + i of row c
 //
 // What a row does not see must not reach it: its weight is 0, but 0 times a NaN
-// is not.  A wave that ends with a NaN goes over its tokens twice more, once to
-// count the numbers that are not finite among those that each row sees, once
-// without them.
+// is not.  A workgroup that ends with a NaN does its rows again, by plain_rows.
 template <int DT, int DIM>
-__global__ __launch_bounds__(256) void few_rows_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 || DIM == 64 ? 2 : 1) void few_rows_kernel(AttnArgs a) {
   constexpr int WAVES = 4, BM = 16;
   constexpr int KSTEPS = DIM / 32, KW = DIM / 64;  // instructions of q . k; 16-byte loads of a key
   constexpr int DT_TILES = DIM / 16;
@@ -179,6 +264,9 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttnArgs a) {
   constexpr int PITCH = DIM + 4;
   __shared__ float o_s[WAVES][BM][PITCH];
   __shared__ float m_s[WAVES][BM], l_s[WAVES][BM];
+  // One term of q stays in registers, three would not fit beside the rest.
+  constexpr bool Q_LDS = QT > 1;
+  __shared__ uint4 q_s[Q_LDS ? KSTEPS * QT * 64 : 1];
 
   const uint32_t split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits;
   const uint32_t h = blockIdx.y, r = blockIdx.z;
@@ -198,35 +286,43 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttnArgs a) {
   const uint32_t rho = t.r0 + c;
   const bool real = c < t.rows;
   const uint32_t qrow = real ? rho / a.group : 0, qhead = h * a.group + (real ? rho - qrow * a.group : 0);
-  int64_t see0 = 0, see1 = real ? t.length : 0;
+  int32_t see0 = 0, see1 = real ? t.length : 0;
   if (a.causal && real) {
-    const int64_t e = t.length - t.n + qrow + 1;
-    see1 = e < 0 ? 0 : e < t.length ? e : t.length;
-    if (a.window && e > (int64_t)a.window) see0 = e - a.window;
+    const int32_t e = t.length - (int32_t)t.n + (int32_t)qrow + 1;
+    see1 = e < 0 ? 0 : e;
+    if (a.window && e > a.window) see0 = e - a.window;
   }
-  v8bf q[KSTEPS][QT];
+  v8bf q[Q_LDS ? 1 : KSTEPS];
   {
-    const char* at = a.q[r] + (uint64_t)(t.row0 + qrow) * a.q_pitch + (uint64_t)qhead * (DIM * ES) + g * (DIM / 4) * ES;
+    const char* at = a.q[r] + (uint64_t)(t.row0 + qrow) * a.q_pitch + (uint64_t)qhead * (DIM * ES) + g * 16 * ES;
+    if constexpr (!Q_LDS) {
 #pragma unroll
-    for (int s = 0; s < KSTEPS; ++s) {
-      if (DT == DT_BF16) {
-        const uint4 w = real ? ld16(at + s * 16) : make_uint4(0, 0, 0, 0);
-        q[s][0] = __builtin_bit_cast(v8bf, w);
-      } else {
-        const uint4 w = real ? ld16(at + s * 32) : make_uint4(0, 0, 0, 0), u = real ? ld16(at + s * 32 + 16) : make_uint4(0, 0, 0, 0);
+      for (int s = 0; s < KSTEPS; ++s)
+        q[s] = __builtin_bit_cast(v8bf, flipped(real ? ld16(at + (s / 2 * 64 + s % 2 * 8) * 2) : make_uint4(0, 0, 0, 0), a.flip));
+    } else {
+      for (int s = wave; s < KSTEPS; s += WAVES) {
+        const char* from = at + (s / 2 * 64 + s % 2 * 8) * 4;
+        const uint4 w = real ? ld16(from) : make_uint4(0, 0, 0, 0), u = real ? ld16(from + 16) : make_uint4(0, 0, 0, 0);
         float x[8] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w),
                       __uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
-        split8<QT>(x, q[s]);
+        if (a.flip)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = -x[e];
+        v8bf terms[QT];
+        split8<QT>(x, terms);
+#pragma unroll
+        for (int y = 0; y < QT; ++y) q_s[(s * QT + y) * 64 + lane] = __builtin_bit_cast(uint4, terms[y]);
       }
+      __syncthreads();
     }
   }
   // Tokens that every row sees: no mask within [all0, all1).
-  int64_t all0 = 0, all1 = t.length;
+  int32_t all0 = 0, all1 = t.length;
   if (a.causal) {
-    const int64_t e = t.length - t.n + t.r0 / a.group + 1;
-    all1 = e < 0 ? 0 : e < t.length ? e : t.length;
-    const int64_t f = t.length - t.n + (t.r0 + t.rows - 1) / a.group + 1 - (int64_t)a.window;
-    if (a.window && f > 0) all0 = f;
+    const int32_t end = t.length - (int32_t)t.n + 1;
+    const int32_t e = end + (int32_t)(t.r0 / a.group), f = end + (int32_t)((t.r0 + t.rows - 1) / a.group);
+    all1 = e < 0 ? 0 : e;
+    if (a.window && f > a.window) all0 = f - a.window;
   }
 
   v4f o[DT_TILES];
@@ -246,12 +342,12 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttnArgs a) {
     const uint64_t base = (uint64_t)t.begin + (uint64_t)step * TOKENS + kb;
     const uint32_t off = (uint32_t)base & ((1u << a.p.page_shift) - 1);
     if (kid < a.p.pages) {
-      const uint8_t* at = kc + page_at(kid, a.kv_heads, h, page_bytes) + (off + koff) * DIM + g * (DIM / 4);
+      const uint8_t* at = kc + page_at(kid, a.kv_heads, h, page_bytes) + (off + koff) * DIM + g * 16;
       ks = byte_scale(a.k_scale[r][(uint64_t)kid * a.kv_heads + h]);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < KW; ++j) kw[i][j] = ld16((const char*)at + i * 4 * DIM + j * 16);
+        for (int j = 0; j < KW; ++j) kw[i][j] = ld16((const char*)at + i * 4 * DIM + j * 64);
     } else {
       ks = 1.f;
 #pragma unroll
@@ -276,85 +372,87 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttnArgs a) {
     }
   };
 
-  // One pass over this wave's steps.  MODE 0: the sums; 1: numbers that are not
-  // finite among the values a row sees; 2: the sums without those.
-  auto sweep = [&](auto mode) {
-    constexpr int MODE = decltype(mode)::value;
+  {
 #pragma unroll
     for (int i = 0; i < DT_TILES; ++i) o[i] = (v4f){0.f, 0.f, 0.f, 0.f};
     m = -INFINITY;
     l = 0.f;
     uint32_t step = step0 + wave;
-    if (step >= step1) return;
-    ids(step);
-    load_k(step);
-    load_v(step, vid);
+    if (step < step1) {
+      ids(step);
+      load_k(step);
+      load_v(step, vid);
+    }
     for (; step < step1; step += WAVES) {
-      const int64_t base = (int64_t)t.begin + (int64_t)step * TOKENS;
+      const int32_t base = (int32_t)(t.begin + step * TOKENS);
       const bool more = step + WAVES < step1;
       if (more) ids(step + WAVES);
       v4f s[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[i] = (v4f){0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < 4; ++i) s[i] = (v4f){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < KSTEPS; ++j) {
+      for (int j = 0; j < KSTEPS; ++j) {
+        v8bf qj[QT];
+#pragma unroll
+        for (int x = 0; x < QT; ++x) {
+          if constexpr (Q_LDS) qj[x] = __builtin_bit_cast(v8bf, q_s[(j * QT + x) * 64 + lane]);
+          else qj[x] = q[j];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
           const uint4 w = kw[i][j / 2];
           const v8bf k8 = j % 2 ? widen8(w.z, w.w, ks) : widen8(w.x, w.y, ks);
 #pragma unroll
-          for (int x = QT - 1; x >= 0; --x) s[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k8, q[j][x], s[i], 0, 0, 0);
+          for (int x = QT - 1; x >= 0; --x) s[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k8, qj[x], s[i], 0, 0, 0);
         }
       }
       if (more) load_k(step + WAVES);
-      const bool mask = base < all0 || base + TOKENS > all1 || __any(!there);
-      const int64_t first = base + 16 * g;
+      const bool mask = base < all0 || base > all1 - (int32_t)TOKENS || __any(!there);
+      const int32_t first = base + 16 * (int32_t)g;
       float p[16];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float z = s[i][e] * a.scale;
-          if (MODE == 1) z = 0.f;
+          float z = s[i][e];
           if (mask) {
-            const int64_t at = first + 4 * i + e;
+            const int32_t at = first + 4 * i + e;
             if (at < see0 || at >= see1 || !there) z = -INFINITY;
           }
           p[4 * i + e] = z;
         }
-      if (MODE == 1) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) p[i] = p[i] == 0.f ? 1.f : 0.f;
-      } else {
+      {
         float top = p[0];
 #pragma unroll
         for (int i = 1; i < 16; ++i) top = fmaxf(top, p[i]);
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
-        const float next = fmaxf(m, top), shift = next == -INFINITY ? 0.f : next;
-        if (__any(next > m)) {
-          const float f = __builtin_amdgcn_exp2f(m - shift);  // m -inf: 0
+        // The maximum follows only when it has grown by more than 2^8: weights of
+        // up to that are as good.
+        if (__any((top - m) * a.factor > 8.f)) {
+          const float next = fmaxf(m, top), f = next == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - next) * a.factor);
+          m = next;
           l *= f;
 #pragma unroll
           for (int i = 0; i < DT_TILES; ++i) o[i] *= f;
         }
-        m = next;
+        const float shift = m == -INFINITY ? 0.f : m * a.factor;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          p[i] = __builtin_amdgcn_exp2f(p[i] - shift);
+          p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[i], a.factor, -shift));
           l += p[i];
         }
       }
       v8bf w[2][PT];
       split8<PT>(p, w[0]);
       split8<PT>(p + 8, w[1]);
-      if (base < t.lo || base + TOKENS > t.hi) {
+      if (base < t.lo || base > t.hi - (int32_t)TOKENS) {
 #pragma unroll
         for (int i = 0; i < DT_TILES; ++i) vw[i] = clear_outside(vw[i], first, t.lo, t.hi);
       }
 #pragma unroll
       for (int i = 0; i < DT_TILES; ++i) {
-        v8bf lo = widen8(vw[i].x, vw[i].y, vs), hi = widen8(vw[i].z, vw[i].w, vs);
-        if (MODE) lo = sift(lo, MODE == 1), hi = sift(hi, MODE == 1);
+        const v8bf lo = widen8(vw[i].x, vw[i].y, vs), hi = widen8(vw[i].z, vw[i].w, vs);
 #pragma unroll
         for (int x = PT - 1; x >= 0; --x) {
           o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, w[0][x], o[i], 0, 0, 0);
@@ -363,33 +461,24 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttnArgs a) {
       }
       if (more) load_v(step + WAVES, vid);
     }
-  };
+  }
 
-  sweep(std::integral_constant<int, 0>{});
+  const uint64_t slot = (((uint64_t)r * a.kv_heads + h) * a.tiles + tile) * a.splits + split;
   float worst = 0.f;
 #pragma unroll
-  for (int i = 0; i < DT_TILES; ++i) worst += o[i][0] * 0.f + o[i][1] * 0.f + o[i][2] * 0.f + o[i][3] * 0.f;
-  if (__any(!(worst == 0.f))) {
-    uint32_t bad[(DT_TILES * 4 + 31) / 32];
-    sweep(std::integral_constant<int, 1>{});
-#pragma unroll
-    for (int i = 0; i < (DT_TILES * 4 + 31) / 32; ++i) bad[i] = 0;
-#pragma unroll
-    for (int i = 0; i < DT_TILES * 4; ++i) bad[i / 32] |= (o[i / 4][i % 4] > 0.f ? 1u : 0u) << (i % 32);
-    sweep(std::integral_constant<int, 2>{});
-#pragma unroll
-    for (int i = 0; i < DT_TILES * 4; ++i)
-      if (bad[i / 32] >> (i % 32) & 1) o[i / 4][i % 4] = NAN;
+  for (int i = 0; i < DT_TILES * 4; ++i) worst += o[i / 4][i % 4] * 0.f;
+  if (__syncthreads_or(!(worst == 0.f))) {
+    plain_rows<DT, DIM>(a, t, h, r, t.begin + step0 * TOKENS, t.begin + step1 * TOKENS, shared, slot * BM);
+    return;
   }
 
   // Join the waves (and the lane groups' sums of p).
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
-  if (g == 0) m_s[wave][c] = m, l_s[wave][c] = l;
+  if (g == 0) m_s[wave][c] = m * a.factor, l_s[wave][c] = l;
 #pragma unroll
   for (int i = 0; i < DT_TILES; ++i) *(v4f*)&o_s[wave][c][16 * i + 4 * g] = o[i];
   __syncthreads();
-  const uint64_t slot = (((uint64_t)r * a.kv_heads + h) * a.tiles + tile) * a.splits + split;
   for (uint32_t i = threadIdx.x; i < BM * (DIM / 4); i += 256) {
     const uint32_t row = i / (DIM / 4), d = i % (DIM / 4) * 4;
     if (row >= t.rows) break;
@@ -420,19 +509,378 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttnArgs a) {
   }
 }
 
-// Joins the shares of a tile, BM rows of DIM: one workgroup per row tile, four
-// dimensions per thread.
+// ---- many rows: 128 rows per workgroup, 32 per wave, the codes shared in LDS ----
+//
+// bf16 queries meet the keys' codes as they are, in 32x32x64 instructions with
+// scales: a query is 8 significant bits, so two e4m3 terms of 4 hold it (hi, and
+// 16 times what hi left), over a power of two of its row's largest value.  What
+// is smaller than 2^-14 of that is off by at most 2^-22 of it.  The same matrix
+// time as one bf16 product, and no key is widened.
+//
+// Bound by the matrix cores and, beside them, by the vector units, which widen
+// the values and compute the softmax.  A step of 64 tokens is loaded to
+// registers one step ahead and stored to the other of two LDS buffers.
+//
+// Matrix instructions 32x32x16, keys as the first operand, with lane = 32 h + c:
+//   S^T    operand row i of step a (0, 1) is token 32 ((i >> 2) & 1) + 16 a +
+//          4 (i >> 3) + (i & 3): lane (h, c) then holds tokens 32 h + 16 a +
+//          0 .. 15 of row c, which is the order the weights enter the second
+//          product in, without leaving their lane
+//   keys   fp32: k of half h: dim / 2 contiguous values from h dim / 2 on
+//   values operand row: dimension 32 t + c, k of half h: tokens 32 h .. + 31
+// LDS rows (a token's key, a dimension's 64 values) hold their 16-byte chunks
+// permuted by the row's number, so that the lanes of a read spread over the banks.
+template <int DT, int DIM>
+__global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 ? 2 : 1) void many_rows_kernel(AttnArgs a) {
+  constexpr int WAVES = 4, THREADS = 64 * WAVES, BM = 32 * WAVES;
+  constexpr int KSTEPS = DIM / 16, DT_TILES = DIM / 32;
+  constexpr int KCHUNKS = DIM / 16;               // 16-byte chunks of a key
+  constexpr int NC = 4 * DIM / THREADS;           // chunks a thread moves, of keys and of values
+  constexpr int QT = DT == DT_BF16 ? 1 : 3, PT = DT == DT_BF16 ? 1 : 3;
+  constexpr uint32_t ES = DT == DT_BF16 ? 2 : 4;
+  __shared__ uint4 k_s[2][4 * DIM], v_s[2][8 * DIM];  // keys as codes, values as bf16
+  __shared__ uint32_t sc_s[2][4];  // scale bytes of the keys' 16-token blocks, 0: on no page
+
+  const uint32_t columns = a.kv_heads * gridDim.y;  // (gridDim.y: ranks)
+  const uint32_t b = blockIdx.x + gridDim.x * blockIdx.y, column = b % columns, item = b / columns;
+  const uint32_t h = column % a.kv_heads, r = column / a.kv_heads;
+  const uint32_t split = item % a.splits, tile = a.tiles - 1 - item / a.splits;
+  Tile t;
+  if (!tile_of(a, tile, BM, &t)) return;
+  const uint32_t per = share_steps(a, t.steps), step0 = split * per;
+  if (split && step0 >= t.steps) return;
+  const uint32_t step1 = step0 + per < t.steps ? step0 + per : t.steps;
+  const bool shared = t.steps > per;
+
+  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, hf = lane >> 5, c = lane & 31;
+  const uint32_t page_bytes = DIM << a.p.page_shift;
+
+  // This lane's row, the tokens it sees and those its wave's rows see.
+  const uint32_t wr = wave * 32, row = wr + c, rho = t.r0 + row;
+  const bool real = row < t.rows;
+  const uint32_t qrow = real ? rho / a.group : 0, qhead = h * a.group + (real ? rho - qrow * a.group : 0);
+  int32_t see0 = 0, see1 = real ? t.length : 0, some0 = 0, some1 = wr < t.rows ? t.length : 0, all0 = 0, all1 = t.length;
+  if (a.causal && wr < t.rows) {
+    const int32_t end = t.length - (int32_t)t.n + 1;
+    const uint32_t last = t.r0 + (wr + 31 < t.rows ? wr + 31 : t.rows - 1);
+    const int32_t e = end + (int32_t)qrow, e0 = end + (int32_t)((t.r0 + wr) / a.group), e1 = end + (int32_t)(last / a.group);
+    if (real) see1 = e < 0 ? 0 : e;
+    all1 = e0 < 0 ? 0 : e0;
+    some1 = e1 < 0 ? 0 : e1;
+    if (a.window) {
+      see0 = e > a.window ? e - a.window : 0;
+      some0 = e0 > a.window ? e0 - a.window : 0;
+      all0 = e1 > a.window ? e1 - a.window : 0;
+    }
+  }
+  // This lane's half of its row: bf16 queries in two e4m3 terms, fp32 ones in
+  // three bf16 terms.
+  constexpr bool F8 = DT == DT_BF16;
+  v8i q8[F8 ? DIM / 64 : 1][2];
+  int q_scale[2] = {127, 127};
+  v8bf q[F8 ? 1 : KSTEPS][QT];
+  {
+    const char* at = a.q[r] + (uint64_t)(t.row0 + qrow) * a.q_pitch + (uint64_t)qhead * (DIM * ES) + hf * (F8 ? 32 : DIM / 2) * ES;
+    if constexpr (F8) {
+      uint4 w[DIM / 64][4];
+      float top = 0.f;
+#pragma unroll
+      for (int s = 0; s < DIM / 64; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          w[s][i] = flipped(real ? ld16(at + s * 128 + i * 16) : make_uint4(0, 0, 0, 0), a.flip);
+          const uint32_t u[4] = {w[s][i].x, w[s][i].y, w[s][i].z, w[s][i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(finite(fabsf(low_of(u[e]))), finite(fabsf(high_of(u[e])))));
+        }
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const uint32_t byte = scale_byte(top) < 8 ? 8 : scale_byte(top);
+      q_scale[0] = (int)byte, q_scale[1] = (int)byte - 4;
+      const float inv = scale_of(254 - byte);
+#pragma unroll
+      for (int s = 0; s < DIM / 64; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t u[4] = {w[s][i].x, w[s][i].y, w[s][i].z, w[s][i].w};
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x[4] = {low_of(u[2 * e]), high_of(u[2 * e]), low_of(u[2 * e + 1]), high_of(u[2 * e + 1])}, y[4];
+            const uint32_t hi = codes_of(x, inv);
+            values_of(hi, 1.f, y);
+#pragma unroll
+            for (int z = 0; z < 4; ++z) x[z] = __builtin_fmaf(x[z], inv, -y[z]);
+            q8[s][0][2 * i + e] = (int)hi;
+            q8[s][1][2 * i + e] = (int)codes_of(x, 16.f);
+          }
+        }
+    } else {
+#pragma unroll
+      for (int s = 0; s < KSTEPS; ++s) {
+        const uint4 w = real ? ld16(at + s * 32) : make_uint4(0, 0, 0, 0), u = real ? ld16(at + s * 32 + 16) : make_uint4(0, 0, 0, 0);
+        float x[8] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w),
+                      __uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
+        if (a.flip)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = -x[e];
+        split8<QT>(x, q[s]);
+      }
+    }
+  }
+
+  v16f o[DT_TILES];
+  // l: sum of the weights; lr: of the weights as they are multiplied.  One bf16
+  // term is off by up to 2^-9 of it; over lr a row that one token dominates has
+  // that error in both and loses it.  lse goes by l.
+  float m, l, lr;
+  uint32_t kid[NC], vid;  // pages of the step to load next
+  uint4 kx[NC], vx[NC];
+  uint32_t scales[2];     // of this thread's block of values, tid % 4; 0: on no page
+  // A page of 64 tokens or more holds a whole step: one page, the same for
+  // every thread, whose address scalar registers keep.
+  const bool whole = a.p.page_shift >= 6;
+  auto ids = [&](uint32_t step) {
+    const uint64_t base = (uint64_t)t.begin + (uint64_t)step * TOKENS;
+    vid = page_id(a.p, t.s, (whole ? base : base + 16 * (tid & 3)) >> a.p.page_shift);
+    if (whole) return;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) kid[i] = page_id(a.p, t.s, (base + (tid + i * THREADS) / KCHUNKS) >> a.p.page_shift);
+  };
+  auto load = [&](uint32_t step) {
+    const uint32_t base = t.begin + step * TOKENS, in_page = (1u << a.p.page_shift) - 1;
+    if (whole) {
+      const uint32_t id = __builtin_amdgcn_readfirstlane(vid);
+      if (id < a.p.pages) {
+        const uint64_t at = page_at(id, a.kv_heads, h, page_bytes);
+        const uint8_t* kp = a.k[r] + at + (base & in_page) * DIM;
+        const uint8_t* vp = a.v[r] + at + (base & in_page);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          kx[i] = ld16((const char*)kp + (tid + i * THREADS) * 16);
+          vx[i] = ld16((const char*)vp + (((tid + i * THREADS) / 4) << a.p.page_shift) + 16 * (tid & 3));
+        }
+        scales[0] = clamp_byte(a.k_scale[r][(uint64_t)id * a.kv_heads + h]);
+        scales[1] = clamp_byte(a.v_scale[r][(uint64_t)id * a.kv_heads + h]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) kx[i] = vx[i] = make_uint4(0, 0, 0, 0);
+        scales[0] = scales[1] = 0;
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const uint32_t ch = tid + i * THREADS;
+      kx[i] = make_uint4(0, 0, 0, 0);
+      if (kid[i] < a.p.pages)
+        kx[i] = ld16((const char*)a.k[r] + page_at(kid[i], a.kv_heads, h, page_bytes) +
+                     ((base + ch / KCHUNKS) & in_page) * DIM + ch % KCHUNKS * 16);
+    }
+    const bool there = vid < a.p.pages;
+    const uint8_t* at = a.v[r] + page_at(there ? vid : 0, a.kv_heads, h, page_bytes) + ((base + 16 * (tid & 3)) & in_page);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      vx[i] = make_uint4(0, 0, 0, 0);
+      if (there) vx[i] = ld16((const char*)at + (((tid + i * THREADS) / 4) << a.p.page_shift));
+    }
+    scales[0] = scales[1] = 0;
+    if (there) {
+      scales[0] = clamp_byte(a.k_scale[r][(uint64_t)vid * a.kv_heads + h]);
+      scales[1] = clamp_byte(a.v_scale[r][(uint64_t)vid * a.kv_heads + h]);
+    }
+  };
+  auto store = [&](uint32_t step, uint32_t buf) {
+    const int32_t base = (int32_t)(t.begin + step * TOKENS);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const uint32_t ch = tid + i * THREADS, kr = ch / KCHUNKS, vr = ch / 4;
+      k_s[buf][kr * KCHUNKS + ((ch % KCHUNKS) ^ (kr & (KCHUNKS - 1) & 7))] = kx[i];
+      uint4 w = vx[i];
+      if (base < t.lo || base > t.hi - (int32_t)TOKENS) w = clear_outside(w, base + 16 * (int32_t)(tid & 3), t.lo, t.hi);
+      uint4* vt = v_s[buf] + vr * 8;
+      vt[(2 * (tid & 3)) ^ (vr & 7)] = __builtin_bit_cast(uint4, widen8(w.x, w.y, scale_of(scales[1])));
+      vt[(2 * (tid & 3) + 1) ^ (vr & 7)] = __builtin_bit_cast(uint4, widen8(w.z, w.w, scale_of(scales[1])));
+    }
+    if (tid < 4) sc_s[buf][tid] = scales[0];
+  };
+
+  const uint32_t kt = 32 * ((c >> 2) & 1) + 4 * (c >> 3) + (c & 3);  // this lane's key of x = 0
+  // where its chunks lie in LDS: the chunk's number is exclusive-ored in
+  const uint32_t ka0 = kt * KCHUNKS + ((F8 ? 2 * hf : hf * (KCHUNKS / 2)) ^ (kt & (KCHUNKS - 1) & 7));
+  const uint32_t va0 = c * 8 + ((4 * hf) ^ (c & 7));
+  {
+#pragma unroll
+    for (int i = 0; i < DT_TILES; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[i][e] = 0.f;
+    m = -INFINITY;
+    l = lr = 0.f;
+    if (step0 < step1) {
+      ids(step0);
+      load(step0);
+      if (step0 + 1 < step1) ids(step0 + 1);
+      store(step0, 0);
+    }
+    __syncthreads();
+    for (uint32_t step = step0; step < step1; ++step) {
+      const uint32_t buf = (step - step0) & 1;
+      const bool more = step + 1 < step1;
+      if (more) {
+        load(step + 1);
+        if (step + 2 < step1) ids(step + 2);
+      }
+      const int32_t base = (int32_t)(t.begin + step * TOKENS);
+      if (base < some1 && base > some0 - (int32_t)TOKENS) {
+        const bool gap = !sc_s[buf][2 * hf] || !sc_s[buf][2 * hf + 1];
+        const bool mask = base < all0 || base > all1 - (int32_t)TOKENS || __any(gap);
+        float p[2][16];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          v16f s;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[e] = 0.f;
+          const uint32_t key = kt + 16 * x;
+          const uint32_t byte = sc_s[buf][key >> 4];
+          const uint32_t ka = ka0 + x * 16 * KCHUNKS;
+          if constexpr (F8) {
+#pragma unroll
+            for (int j = 0; j < DIM / 64; ++j) {
+              const uint4 w0 = k_s[buf][ka ^ (4 * j)], w1 = k_s[buf][ka ^ (4 * j + 1)];
+              const v8i k8 = {(int)w0.x, (int)w0.y, (int)w0.z, (int)w0.w, (int)w1.x, (int)w1.y, (int)w1.z, (int)w1.w};
+              s = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k8, q8[j][1], s, 0, 0, 0, (int)byte, 0, q_scale[1]);
+              s = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k8, q8[j][0], s, 0, 0, 0, (int)byte, 0, q_scale[0]);
+            }
+          } else {
+            const float ks = scale_of(byte);
+#pragma unroll
+            for (int j = 0; j < KSTEPS; j += 2) {
+              const uint4 w = k_s[buf][ka ^ (j / 2)];
+              const v8bf lo = widen8(w.x, w.y, ks), hi = widen8(w.z, w.w, ks);
+#pragma unroll
+              for (int y = QT - 1; y >= 0; --y) {
+                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lo, q[j][y], s, 0, 0, 0);
+                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hi, q[j + 1][y], s, 0, 0, 0);
+              }
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) p[x][e] = s[e];
+          if (mask) {
+            // tokens first + e with from <= e < to
+            const int32_t first = base + 32 * (int32_t)hf + 16 * x, from = see0 - first;
+            const int32_t to = sc_s[buf][2 * hf + x] ? see1 - first : -1;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (e < from || e >= to) p[x][e] = -INFINITY;
+          }
+        }
+        {
+          float top = p[0][0];
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) top = fmaxf(top, p[x][e]);
+          top = fmaxf(top, __shfl_xor(top, 32));
+          // The maximum follows only when it has grown by more than 2^8: weights
+          // of up to that are as good, and rescaling the sums costs as much as
+          // the rest of the softmax.
+          if (__any((top - m) * a.factor > 8.f)) {
+            const float next = fmaxf(m, top), f = next == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - next) * a.factor);
+            m = next;
+            l *= f;
+            lr *= f;
+#pragma unroll
+            for (int i = 0; i < DT_TILES; ++i) o[i] *= f;
+          }
+        }
+        const float shift = m == -INFINITY ? 0.f : m * a.factor;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            p[x][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[x][e], a.factor, -shift));
+            l += p[x][e];
+          }
+          v8bf w[2][PT];
+          if (PT == 1) {
+            w[0][0] = rounded8(p[x], &lr);
+            w[1][0] = rounded8(p[x] + 8, &lr);
+          } else {
+            split8<PT>(p[x], w[0]);
+            split8<PT>(p[x] + 8, w[1]);
+          }
+#pragma unroll
+          for (int i = 0; i < DT_TILES; ++i) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const v8bf v = __builtin_bit_cast(v8bf, v_s[buf][(va0 ^ (2 * x + u)) + 256 * i]);
+#pragma unroll
+              for (int y = PT - 1; y >= 0; --y) o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w[u][y], o[i], 0, 0, 0);
+            }
+          }
+        }
+      }
+      if (more) store(step + 1, buf ^ 1);
+      __syncthreads();
+    }
+  }
+
+  const uint64_t slot = ((((uint64_t)r * a.kv_heads + h) * a.tiles + tile) * a.splits + split) * BM;
+  float worst = 0.f;
+#pragma unroll
+  for (int i = 0; i < DT_TILES * 16; ++i) worst += o[i / 16][i % 16] * 0.f;
+  if (__syncthreads_or(!(worst == 0.f))) {
+    plain_rows<DT, DIM>(a, t, h, r, t.begin + step0 * TOKENS, t.begin + step1 * TOKENS, shared, slot);
+    return;
+  }
+
+  l += __shfl_xor(l, 32);
+  if (PT == 1) lr += __shfl_xor(lr, 32);
+  else lr = l;
+  if (!real) return;
+  if (shared) {
+    const float f = lr == 0.f ? 0.f : l / lr;  // sums that go with l
+#pragma unroll
+    for (int i = 0; i < DT_TILES; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const v4f x = (v4f){o[i][4 * e], o[i][4 * e + 1], o[i][4 * e + 2], o[i][4 * e + 3]} * f;
+        *(v4f*)(a.part + (slot + row) * DIM + 32 * i + 8 * e + 4 * hf) = x;
+      }
+    if (hf == 0) a.stat[slot + row] = make_float2(m * a.factor, l);
+    return;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / lr;
+  const uint64_t at = ((uint64_t)(t.row0 + qrow) * a.heads + qhead) * DIM;
+#pragma unroll
+  for (int i = 0; i < DT_TILES; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const v4f x = (v4f){o[i][4 * e], o[i][4 * e + 1], o[i][4 * e + 2], o[i][4 * e + 3]} * inv;
+      const uint64_t d = at + 32 * i + 8 * e + 4 * hf;
+      if (DT == DT_BF16) *(uint2*)(a.out[r] + d * 2) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+      else *(v4f*)(a.out[r] + d * 4) = x;
+    }
+  if (hf == 0 && a.lse[r])
+    a.lse[r][(uint64_t)(t.row0 + qrow) * a.heads + qhead] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m * a.factor) + log2f(l)) * LN2;
+}
+
+// Joins the shares of a tile, 16 rows per workgroup, four dimensions per thread.
+constexpr uint32_t JOIN_ROWS = 16;
+
 template <int DT, int DIM>
 __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, uint32_t bm) {
-  const uint32_t tile = blockIdx.x, h = blockIdx.y, r = blockIdx.z;
+  const uint32_t parts = bm / JOIN_ROWS, tile = blockIdx.x / parts, row0 = blockIdx.x % parts * JOIN_ROWS;
+  const uint32_t h = blockIdx.y, r = blockIdx.z;
   Tile t;
   if (!tile_of(a, tile, bm, &t)) return;
   const uint32_t per = share_steps(a, t.steps);
   if (t.steps <= per) return;  // one share: stored whole
   const uint32_t shares = (t.steps + per - 1) / per;
   const uint64_t slot = (((uint64_t)r * a.kv_heads + h) * a.tiles + tile) * a.splits;
-  for (uint32_t i = threadIdx.x; i < t.rows * (DIM / 4); i += 256) {
-    const uint32_t row = i / (DIM / 4), d = i % (DIM / 4) * 4;
+#pragma unroll
+  for (uint32_t i = threadIdx.x; i < JOIN_ROWS * (DIM / 4); i += 256) {
+    const uint32_t row = row0 + i / (DIM / 4), d = i % (DIM / 4) * 4;
+    if (row >= t.rows) break;
     float top = -INFINITY, total = 0.f;
     for (uint32_t s = 0; s < shares; ++s) top = fmaxf(top, a.stat[(slot + s) * bm + row].x);
     const float shift = top == -INFINITY ? 0.f : top;
@@ -454,23 +902,39 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, uint32_t bm) {
 
 // How a call is cut.
 struct AttnPlan {
+  bool few;
   uint32_t bm, tiles, splits, min_steps;
   uint64_t part_bytes, stat_bytes;
   uint64_t bytes() const { return part_bytes + stat_bytes; }
 };
 
-AttnPlan plan_of(int n, uint64_t seqs, uint64_t rows, uint64_t tokens, uint64_t heads, uint64_t kv_heads, uint64_t dim) {
+AttnPlan plan_of(const ar_kv_cache* c, uint64_t seqs, uint64_t rows, uint64_t width, uint64_t heads, uint64_t max_rows) {
   AttnPlan p;
-  const uint64_t group = heads / kv_heads;
-  p.bm = 16;
+  const uint64_t group = heads / c->kv_heads, columns = c->kv_heads * c->nranks;
+  // Rows of a sequence: the caller's word, or the mean.  Either kernel is right
+  // for any number.
+  const uint64_t most = max_rows ? umin(max_rows, rows) : (rows + seqs - 1) / seqs;
+  p.few = most * group <= 32;
+  p.bm = p.few ? 16 : 128;
   p.tiles = (uint32_t)item_count(rows, seqs, group, p.bm, 1);
   // Tiles that may be real: a sequence's last one is counted twice above.
-  const uint64_t real = umax(1, umin(p.tiles, (rows * group + p.bm - 1) / p.bm + seqs - 1));
-  const uint64_t steps = (tokens + TOKENS - 1) / TOKENS;
-  p.min_steps = 16;
-  p.splits = (uint32_t)umax(1, umin((steps + p.min_steps - 1) / p.min_steps, (1024 + real * n * kv_heads - 1) / (real * n * kv_heads)));
-  const uint64_t slots = p.splits > 1 ? (uint64_t)n * kv_heads * p.tiles * p.splits : 0;
-  p.part_bytes = layer_align(slots * p.bm * dim * 4);
+  const uint64_t real = umax(1, umin(p.tiles, (rows * group + p.bm - 1) / p.bm + seqs - 1)) * columns;
+  const uint64_t steps = (width * c->page + TOKENS - 1) / TOKENS;
+  p.min_steps = 8;
+  const uint64_t most_splits = umax(1, (steps + p.min_steps - 1) / p.min_steps);
+  if (p.few) {
+    p.splits = (uint32_t)umin(most_splits, (512 + real - 1) / real);
+  } else {
+    // Rounds of 512 workgroups (two per CU) over the work of each.
+    p.splits = 1;
+    uint64_t best = (real + 511) / 512 * 840;
+    for (uint32_t k = 2; k <= 8 && k <= most_splits && real < 512; ++k) {
+      const uint64_t cost = (real * k + 511) / 512 * (840 / k) + 20;
+      if (cost < best) best = cost, p.splits = k;
+    }
+  }
+  const uint64_t slots = p.splits > 1 ? columns * p.tiles * p.splits : 0;
+  p.part_bytes = layer_align(slots * p.bm * c->head_dim * 4);
   p.stat_bytes = layer_align(slots * p.bm * 8);
   return p;
 }
@@ -492,8 +956,7 @@ size_t ar_cache_attention_workspace(const ar_kv_cache* cache, size_t seqs, size_
   if (check_cache(cache) != AR_OK || rows > LAYER_MAX_ROWS || seqs > (1ull << 20) || width > (1ull << 31) ||
       width * cache->page >= (1ull << 31) || check_heads(cache, rows, heads, (int)dtype) != AR_OK || !rows || !seqs)
     return 0;
-  (void)max_rows;
-  return (size_t)plan_of(cache->nranks, seqs, rows, width * cache->page, heads, cache->kv_heads, cache->head_dim).bytes();
+  return (size_t)plan_of(cache, seqs, rows, width, heads, max_rows).bytes();
 }
 
 ar_status ar_cache_attention(const ar_kv_cache* cache, const void* const* q, size_t q_stride,
@@ -504,13 +967,12 @@ ar_status ar_cache_attention(const ar_kv_cache* cache, const void* const* q, siz
   if (st == AR_OK) st = check_rows(cache, rows);
   if (st == AR_OK) st = check_heads(cache, rows->rows, heads, (int)dtype);
   if (st != AR_OK) return st;
-  if (!q || !out || causal < 0 || causal > 1 || (window && !causal) || !(fabsf(scale) < INFINITY)) return AR_ERR_INVALID;
+  if (!q || !out || causal < 0 || causal > 1 || (window && !causal) || !(fabsf(scale) < 1e38f)) return AR_ERR_INVALID;
   if (rows->rows == 0 || rows->seqs == 0) return AR_OK;
   const uint64_t es = dtype == AR_BF16 ? 2 : 4, width = heads * cache->head_dim;
   if (!stride_ok(q_stride, width, es)) return AR_ERR_INVALID;
   const int n = cache->nranks;
-  const AttnPlan plan = plan_of(n, rows->seqs, rows->rows, rows->width * cache->page, heads, cache->kv_heads, cache->head_dim);
-  (void)max_rows;
+  const AttnPlan plan = plan_of(cache, rows->seqs, rows->rows, rows->width, heads, max_rows);
   AttnArgs a;
   LayerBuffers b;
   for (int r = 0; r < n; ++r) {
@@ -538,15 +1000,19 @@ ar_status ar_cache_attention(const ar_kv_cache* cache, const void* const* q, siz
   a.splits = plan.splits;
   a.min_steps = plan.min_steps;
   a.tiles = plan.tiles;
-  a.scale = scale * LOG2E;
+  // (a factor of 0 would make NaN of what is masked; the smallest does the same to the rest)
+  a.factor = fmaxf(fabsf(scale * LOG2E), 1.17549435e-38f);
+  a.flip = scale < 0.f ? 0x80008000u : 0u;
   a.causal = causal;
-  a.window = (uint32_t)umin(window, 0x7fffffff);
+  a.window = (int32_t)umin(window, 0x7fffffff);
   a.part = (float*)workspace;
   a.stat = (float2*)((char*)workspace + plan.part_bytes);
-  const dim3 grid(plan.tiles * plan.splits, a.kv_heads, n), joins(plan.tiles, a.kv_heads, n);
+  const dim3 grid(plan.tiles * plan.splits, a.kv_heads, n), joins(plan.tiles * (plan.bm / JOIN_ROWS), a.kv_heads, n);
+  const dim3 wide(plan.tiles * plan.splits * a.kv_heads, n);
   by_head_dim((int)dtype, cache->head_dim, [&](auto dt, auto dim) {
     constexpr int DT = decltype(dt)::value, DIM = decltype(dim)::value;
-    few_rows_kernel<DT, DIM><<<grid, 256, 0, (hipStream_t)stream>>>(a);
+    if (plan.few) few_rows_kernel<DT, DIM><<<grid, 256, 0, (hipStream_t)stream>>>(a);
+    else many_rows_kernel<DT, DIM><<<wide, 256, 0, (hipStream_t)stream>>>(a);
     if (plan.splits > 1) join_kernel<DT, DIM><<<joins, 256, 0, (hipStream_t)stream>>>(a, plan.bm);
   });
   return hipGetLastError() == hipSuccess ? AR_OK : AR_ERR_HIP;

@@ -46,9 +46,9 @@ struct Piece {
 __device__ __forceinline__ bool piece_of(const Paged& p, uint64_t item, Piece* out) {
   uint32_t row0, n;
   uint64_t local;
-  const uint32_t s = find_sequence(p, item, 1, 1u << p.page_shift, 2, &row0, &n, &local);
+  int32_t at;
+  const uint32_t s = find_sequence(p, item, 1, 1u << p.page_shift, 2, &row0, &n, &local, &at);
   if (s >= p.seqs) return false;
-  const int32_t at = p.at[s];
   const uint64_t start = at < 0 ? 0 : (uint64_t)at, end = start + n;
   const uint64_t j = (start >> p.page_shift) + local, t0 = j << p.page_shift;
   if (t0 >= end) return false;
