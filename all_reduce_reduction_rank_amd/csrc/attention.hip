@@ -28,7 +28,6 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-typedef int v8i __attribute__((ext_vector_type(8)));
 
 constexpr uint32_t TOKENS = 64;  // of a step along the cache
 constexpr float LN2 = 0.69314718055994530942f, LOG2E = 1.44269504088896340736f;
@@ -142,7 +141,6 @@ __device__ __forceinline__ uint4 flipped(const uint4& w, uint32_t f) { return ma
 
 __device__ __forceinline__ uint32_t clamp_byte(uint32_t b) { return b < SCALE_MIN ? SCALE_MIN : b > SCALE_MAX ? SCALE_MAX : b; }
 __device__ __forceinline__ float byte_scale(uint32_t b) { return scale_of(clamp_byte(b)); }
-__device__ __forceinline__ float finite(float x) { return x < INFINITY ? x : 0.f; }  // x >= 0 or NaN
 
 // Bytes of a 16-token block of codes that lie outside tokens [lo, hi) become 0;
 // `at` is the block's first token.
@@ -511,22 +509,21 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 || DIM == 64 ? 2 :
 
 // ---- many rows: 128 rows per workgroup, 32 per wave, the codes shared in LDS ----
 //
-// bf16 queries meet the keys' codes as they are, in 32x32x64 instructions with
-// scales: a query is 8 significant bits, so two e4m3 terms of 4 hold it (hi, and
-// 16 times what hi left), over a power of two of its row's largest value.  What
-// is smaller than 2^-14 of that is off by at most 2^-22 of it.  The same matrix
-// time as one bf16 product, and no key is widened.
-//
-// Bound by the matrix cores and, beside them, by the vector units, which widen
-// the values and compute the softmax.  A step of 64 tokens is loaded to
-// registers one step ahead and stored to the other of two LDS buffers.
+// Bound by the vector units and the matrix cores in turn: the softmax, and the
+// waits of two waves per SIMD that share both.  The codes are widened once, on
+// their way into LDS; widened by every wave from codes in LDS they cost more
+// than the larger LDS reads (prompt of 8192 tokens, 40 heads of 128: 941 us, PUT
+// us now).  The e4m3 instructions with block scales would take the keys' codes
+// as they are, but their sums over 64 products keep fewer than fp32's bits
+// (scores off by 2^-18 of their terms' size, measured).  A step of 64 tokens is
+// loaded to registers one step ahead and stored to the other of two LDS buffers.
 //
 // Matrix instructions 32x32x16, keys as the first operand, with lane = 32 h + c:
-//   S^T    operand row i of step a (0, 1) is token 32 ((i >> 2) & 1) + 16 a +
-//          4 (i >> 3) + (i & 3): lane (h, c) then holds tokens 32 h + 16 a +
+//   S^T    operand row i of x (0, 1) is token 32 ((i >> 2) & 1) + 16 x +
+//          4 (i >> 3) + (i & 3): lane (h, c) then holds tokens 32 h + 16 x +
 //          0 .. 15 of row c, which is the order the weights enter the second
 //          product in, without leaving their lane
-//   keys   fp32: k of half h: dim / 2 contiguous values from h dim / 2 on
+//   keys   k of half h: 8 contiguous values of every 16, from 8 h on
 //   values operand row: dimension 32 t + c, k of half h: tokens 32 h .. + 31
 // LDS rows (a token's key, a dimension's 64 values) hold their 16-byte chunks
 // permuted by the row's number, so that the lanes of a read spread over the banks.
@@ -538,8 +535,9 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 ? 2 : 1) void many
   constexpr int NC = 4 * DIM / THREADS;           // chunks a thread moves, of keys and of values
   constexpr int QT = DT == DT_BF16 ? 1 : 3, PT = DT == DT_BF16 ? 1 : 3;
   constexpr uint32_t ES = DT == DT_BF16 ? 2 : 4;
-  __shared__ uint4 k_s[2][4 * DIM], v_s[2][8 * DIM];  // keys as codes, values as bf16
-  __shared__ uint32_t sc_s[2][4];  // scale bytes of the keys' 16-token blocks, 0: on no page
+  constexpr int KROW = DIM / 8;                   // LDS chunks of a key
+  __shared__ uint4 k_s[2][8 * DIM], v_s[2][8 * DIM];  // bf16
+  __shared__ uint32_t there_s[2][4];                  // the 16-token blocks: on a page
 
   const uint32_t columns = a.kv_heads * gridDim.y;  // (gridDim.y: ranks)
   const uint32_t b = blockIdx.x + gridDim.x * blockIdx.y, column = b % columns, item = b / columns;
@@ -573,50 +571,15 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 ? 2 : 1) void many
       all0 = e1 > a.window ? e1 - a.window : 0;
     }
   }
-  // This lane's half of its row: bf16 queries in two e4m3 terms, fp32 ones in
-  // three bf16 terms.
-  constexpr bool F8 = DT == DT_BF16;
-  v8i q8[F8 ? DIM / 64 : 1][2];
-  int q_scale[2] = {127, 127};
-  v8bf q[F8 ? 1 : KSTEPS][QT];
+  v8bf q[KSTEPS][QT];
   {
-    const char* at = a.q[r] + (uint64_t)(t.row0 + qrow) * a.q_pitch + (uint64_t)qhead * (DIM * ES) + hf * (F8 ? 32 : DIM / 2) * ES;
-    if constexpr (F8) {
-      uint4 w[DIM / 64][4];
-      float top = 0.f;
+    const char* at = a.q[r] + (uint64_t)(t.row0 + qrow) * a.q_pitch + (uint64_t)qhead * (DIM * ES) + hf * 8 * ES;
 #pragma unroll
-      for (int s = 0; s < DIM / 64; ++s)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[s][i] = flipped(real ? ld16(at + s * 128 + i * 16) : make_uint4(0, 0, 0, 0), a.flip);
-          const uint32_t u[4] = {w[s][i].x, w[s][i].y, w[s][i].z, w[s][i].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(finite(fabsf(low_of(u[e]))), finite(fabsf(high_of(u[e])))));
-        }
-      top = fmaxf(top, __shfl_xor(top, 32));
-      const uint32_t byte = scale_byte(top) < 8 ? 8 : scale_byte(top);
-      q_scale[0] = (int)byte, q_scale[1] = (int)byte - 4;
-      const float inv = scale_of(254 - byte);
-#pragma unroll
-      for (int s = 0; s < DIM / 64; ++s)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t u[4] = {w[s][i].x, w[s][i].y, w[s][i].z, w[s][i].w};
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x[4] = {low_of(u[2 * e]), high_of(u[2 * e]), low_of(u[2 * e + 1]), high_of(u[2 * e + 1])}, y[4];
-            const uint32_t hi = codes_of(x, inv);
-            values_of(hi, 1.f, y);
-#pragma unroll
-            for (int z = 0; z < 4; ++z) x[z] = __builtin_fmaf(x[z], inv, -y[z]);
-            q8[s][0][2 * i + e] = (int)hi;
-            q8[s][1][2 * i + e] = (int)codes_of(x, 16.f);
-          }
-        }
-    } else {
-#pragma unroll
-      for (int s = 0; s < KSTEPS; ++s) {
-        const uint4 w = real ? ld16(at + s * 32) : make_uint4(0, 0, 0, 0), u = real ? ld16(at + s * 32 + 16) : make_uint4(0, 0, 0, 0);
+    for (int s = 0; s < KSTEPS; ++s) {
+      if (DT == DT_BF16) {
+        q[s][0] = __builtin_bit_cast(v8bf, flipped(real ? ld16(at + s * 32) : make_uint4(0, 0, 0, 0), a.flip));
+      } else {
+        const uint4 w = real ? ld16(at + s * 64) : make_uint4(0, 0, 0, 0), u = real ? ld16(at + s * 64 + 16) : make_uint4(0, 0, 0, 0);
         float x[8] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w),
                       __uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
         if (a.flip)
@@ -634,7 +597,8 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 ? 2 : 1) void many
   float m, l, lr;
   uint32_t kid[NC], vid;  // pages of the step to load next
   uint4 kx[NC], vx[NC];
-  uint32_t scales[2];     // of this thread's block of values, tid % 4; 0: on no page
+  float ks[NC], vs;       // their scales
+  bool there;             // block tid % 4 is on a page
   // A page of 64 tokens or more holds a whole step: one page, the same for
   // every thread, whose address scalar registers keep.
   const bool whole = a.p.page_shift >= 6;
@@ -658,54 +622,58 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 ? 2 : 1) void many
           kx[i] = ld16((const char*)kp + (tid + i * THREADS) * 16);
           vx[i] = ld16((const char*)vp + (((tid + i * THREADS) / 4) << a.p.page_shift) + 16 * (tid & 3));
         }
-        scales[0] = clamp_byte(a.k_scale[r][(uint64_t)id * a.kv_heads + h]);
-        scales[1] = clamp_byte(a.v_scale[r][(uint64_t)id * a.kv_heads + h]);
+        ks[0] = byte_scale(a.k_scale[r][(uint64_t)id * a.kv_heads + h]);
+        vs = byte_scale(a.v_scale[r][(uint64_t)id * a.kv_heads + h]);
       } else {
 #pragma unroll
         for (int i = 0; i < NC; ++i) kx[i] = vx[i] = make_uint4(0, 0, 0, 0);
-        scales[0] = scales[1] = 0;
+        ks[0] = vs = 1.f;
       }
+#pragma unroll
+      for (int i = 1; i < NC; ++i) ks[i] = ks[0];
+      there = id < a.p.pages;
       return;
     }
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const uint32_t ch = tid + i * THREADS;
       kx[i] = make_uint4(0, 0, 0, 0);
-      if (kid[i] < a.p.pages)
+      ks[i] = 1.f;
+      if (kid[i] < a.p.pages) {
+        ks[i] = byte_scale(a.k_scale[r][(uint64_t)kid[i] * a.kv_heads + h]);
         kx[i] = ld16((const char*)a.k[r] + page_at(kid[i], a.kv_heads, h, page_bytes) +
                      ((base + ch / KCHUNKS) & in_page) * DIM + ch % KCHUNKS * 16);
+      }
     }
-    const bool there = vid < a.p.pages;
+    there = vid < a.p.pages;
     const uint8_t* at = a.v[r] + page_at(there ? vid : 0, a.kv_heads, h, page_bytes) + ((base + 16 * (tid & 3)) & in_page);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       vx[i] = make_uint4(0, 0, 0, 0);
       if (there) vx[i] = ld16((const char*)at + (((tid + i * THREADS) / 4) << a.p.page_shift));
     }
-    scales[0] = scales[1] = 0;
-    if (there) {
-      scales[0] = clamp_byte(a.k_scale[r][(uint64_t)vid * a.kv_heads + h]);
-      scales[1] = clamp_byte(a.v_scale[r][(uint64_t)vid * a.kv_heads + h]);
-    }
+    vs = there ? byte_scale(a.v_scale[r][(uint64_t)vid * a.kv_heads + h]) : 1.f;
   };
   auto store = [&](uint32_t step, uint32_t buf) {
     const int32_t base = (int32_t)(t.begin + step * TOKENS);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const uint32_t ch = tid + i * THREADS, kr = ch / KCHUNKS, vr = ch / 4;
-      k_s[buf][kr * KCHUNKS + ((ch % KCHUNKS) ^ (kr & (KCHUNKS - 1) & 7))] = kx[i];
+      uint4* kt = k_s[buf] + kr * KROW;
+      kt[(ch % KCHUNKS * 2) ^ (kr & 7)] = __builtin_bit_cast(uint4, widen8(kx[i].x, kx[i].y, ks[i]));
+      kt[(ch % KCHUNKS * 2 + 1) ^ (kr & 7)] = __builtin_bit_cast(uint4, widen8(kx[i].z, kx[i].w, ks[i]));
       uint4 w = vx[i];
       if (base < t.lo || base > t.hi - (int32_t)TOKENS) w = clear_outside(w, base + 16 * (int32_t)(tid & 3), t.lo, t.hi);
       uint4* vt = v_s[buf] + vr * 8;
-      vt[(2 * (tid & 3)) ^ (vr & 7)] = __builtin_bit_cast(uint4, widen8(w.x, w.y, scale_of(scales[1])));
-      vt[(2 * (tid & 3) + 1) ^ (vr & 7)] = __builtin_bit_cast(uint4, widen8(w.z, w.w, scale_of(scales[1])));
+      vt[(2 * (tid & 3)) ^ (vr & 7)] = __builtin_bit_cast(uint4, widen8(w.x, w.y, vs));
+      vt[(2 * (tid & 3) + 1) ^ (vr & 7)] = __builtin_bit_cast(uint4, widen8(w.z, w.w, vs));
     }
-    if (tid < 4) sc_s[buf][tid] = scales[0];
+    if (tid < 4) there_s[buf][tid] = there;
   };
 
   const uint32_t kt = 32 * ((c >> 2) & 1) + 4 * (c >> 3) + (c & 3);  // this lane's key of x = 0
   // where its chunks lie in LDS: the chunk's number is exclusive-ored in
-  const uint32_t ka0 = kt * KCHUNKS + ((F8 ? 2 * hf : hf * (KCHUNKS / 2)) ^ (kt & (KCHUNKS - 1) & 7));
+  const uint32_t ka0 = kt * KROW + (hf ^ (kt & 7));
   const uint32_t va0 = c * 8 + ((4 * hf) ^ (c & 7));
   {
 #pragma unroll
@@ -730,7 +698,7 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 ? 2 : 1) void many
       }
       const int32_t base = (int32_t)(t.begin + step * TOKENS);
       if (base < some1 && base > some0 - (int32_t)TOKENS) {
-        const bool gap = !sc_s[buf][2 * hf] || !sc_s[buf][2 * hf + 1];
+        const bool gap = !there_s[buf][2 * hf] || !there_s[buf][2 * hf + 1];
         const bool mask = base < all0 || base > all1 - (int32_t)TOKENS || __any(gap);
         float p[2][16];
 #pragma unroll
@@ -738,36 +706,18 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 ? 2 : 1) void many
           v16f s;
 #pragma unroll
           for (int e = 0; e < 16; ++e) s[e] = 0.f;
-          const uint32_t key = kt + 16 * x;
-          const uint32_t byte = sc_s[buf][key >> 4];
-          const uint32_t ka = ka0 + x * 16 * KCHUNKS;
-          if constexpr (F8) {
 #pragma unroll
-            for (int j = 0; j < DIM / 64; ++j) {
-              const uint4 w0 = k_s[buf][ka ^ (4 * j)], w1 = k_s[buf][ka ^ (4 * j + 1)];
-              const v8i k8 = {(int)w0.x, (int)w0.y, (int)w0.z, (int)w0.w, (int)w1.x, (int)w1.y, (int)w1.z, (int)w1.w};
-              s = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k8, q8[j][1], s, 0, 0, 0, (int)byte, 0, q_scale[1]);
-              s = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k8, q8[j][0], s, 0, 0, 0, (int)byte, 0, q_scale[0]);
-            }
-          } else {
-            const float ks = scale_of(byte);
+          for (int j = 0; j < KSTEPS; ++j) {
+            const v8bf k8 = __builtin_bit_cast(v8bf, k_s[buf][(ka0 ^ (2 * j)) + x * 16 * KROW]);
 #pragma unroll
-            for (int j = 0; j < KSTEPS; j += 2) {
-              const uint4 w = k_s[buf][ka ^ (j / 2)];
-              const v8bf lo = widen8(w.x, w.y, ks), hi = widen8(w.z, w.w, ks);
-#pragma unroll
-              for (int y = QT - 1; y >= 0; --y) {
-                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lo, q[j][y], s, 0, 0, 0);
-                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hi, q[j + 1][y], s, 0, 0, 0);
-              }
-            }
+            for (int y = QT - 1; y >= 0; --y) s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k8, q[j][y], s, 0, 0, 0);
           }
 #pragma unroll
           for (int e = 0; e < 16; ++e) p[x][e] = s[e];
           if (mask) {
             // tokens first + e with from <= e < to
             const int32_t first = base + 32 * (int32_t)hf + 16 * x, from = see0 - first;
-            const int32_t to = sc_s[buf][2 * hf + x] ? see1 - first : -1;
+            const int32_t to = there_s[buf][2 * hf + x] ? see1 - first : -1;
 #pragma unroll
             for (int e = 0; e < 16; ++e)
               if (e < from || e >= to) p[x][e] = -INFINITY;
