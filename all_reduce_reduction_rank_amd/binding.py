@@ -123,7 +123,7 @@ def _declare(lib):
                                               P, S, P])
     lib.ar_cache_write.argtypes = [C, PP, S, PP, S, R, I, P]
     lib.ar_cache_read.argtypes = [C, PP, PP, R, I, P]
-    lib.ar_cache_attention_workspace.argtypes = [C, S, S, S, S, S, I]
+    lib.ar_cache_attention_workspace.argtypes = [C, S, S, S, S, S, S, I]
     lib.ar_cache_attention.argtypes = [C, PP, S, R, PP, PP, S, F, I, S, S, I, P, S, P]
     lib.ar_status_string.argtypes = [I]
     lib.ar_status_string.restype = ctypes.c_char_p
@@ -914,10 +914,10 @@ def cache_read(cache, table, first, start, k, v, stream=None):
 
 
 @functools.lru_cache(maxsize=1024)
-def _attention_workspace(n, pages, page, kv, dim, seqs, rows, width, heads, max_rows, dt):
+def _attention_workspace(n, pages, page, kv, dim, seqs, rows, width, heads, window, max_rows, dt):
     ptr = ctypes.cast(_PTRS[n](*[16] * n), ctypes.c_void_p)  # the sizes do not depend on the buffers
     rec = CacheRecord(ptr, ptr, ptr, ptr, pages, page, kv, dim, n)
-    return _lib().ar_cache_attention_workspace(rec, seqs, rows, width, heads, max_rows, DTYPES[dt])
+    return _lib().ar_cache_attention_workspace(rec, seqs, rows, width, heads, window, max_rows, DTYPES[dt])
 
 
 def cache_attention(q, cache, table, first, length, scale=None, causal=True, window=0, max_rows=0, out=None, lse=None,
@@ -958,7 +958,7 @@ def cache_attention(q, cache, table, first, length, scale=None, causal=True, win
         out = scratch.ranks(n, (rows, heads, dim), dtype)
         op = _PTRS[n](*[t.data_ptr() for t in out])
     nbytes = _attention_workspace(n, cache.pages, cache.page, cache.kv_heads, dim, paged.seqs, rows, paged.width, heads,
-                                  max_rows, dt)
+                                  window, max_rows, dt)
     ws, ws_ptr = scratch.workspace(nbytes) if nbytes else (None, None)
     _check(_lib().ar_cache_attention(cache.record, qp, qs, paged, op, lp, heads,
                                      dim ** -0.5 if scale is None else scale, bool(causal), window, max_rows, DTYPES[dt],

@@ -326,8 +326,10 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 || DIM == 64 ? 2 :
   v4f o[DT_TILES];
   float m, l;
   uint4 kw[4][KW], vw[DT_TILES];
-  uint32_t kid, vid;      // pages of the step to load next
-  float ks, vs;
+  // What a load brings is not touched before its step, so that nothing waits:
+  // the table's entries of the step to load next, the scales' bytes of the one
+  // that is loaded.
+  uint32_t kid, vid, kbyte, vbyte;
   bool there;             // this lane's block of values is on a page
   const uint32_t kb = 16 * (c >> 2), koff = c & 3;  // this lane's key block, row in a group of four
 
@@ -341,30 +343,30 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 || DIM == 64 ? 2 :
     const uint32_t off = (uint32_t)base & ((1u << a.p.page_shift) - 1);
     if (kid < a.p.pages) {
       const uint8_t* at = kc + page_at(kid, a.kv_heads, h, page_bytes) + (off + koff) * DIM + g * 16;
-      ks = byte_scale(a.k_scale[r][(uint64_t)kid * a.kv_heads + h]);
+      kbyte = a.k_scale[r][(uint64_t)kid * a.kv_heads + h];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < KW; ++j) kw[i][j] = ld16((const char*)at + i * 4 * DIM + j * 64);
     } else {
-      ks = 1.f;
+      kbyte = 127;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < KW; ++j) kw[i][j] = make_uint4(0, 0, 0, 0);
     }
   };
-  auto load_v = [&](uint32_t step, uint32_t id) {
+  auto load_v = [&](uint32_t step) {
     const uint64_t base = (uint64_t)t.begin + (uint64_t)step * TOKENS + 16 * g;
     const uint32_t off = (uint32_t)base & ((1u << a.p.page_shift) - 1);
-    there = id < a.p.pages;
+    there = vid < a.p.pages;
     if (there) {
-      const uint8_t* at = vc + page_at(id, a.kv_heads, h, page_bytes) + (c << a.p.page_shift) + off;
-      vs = byte_scale(a.v_scale[r][(uint64_t)id * a.kv_heads + h]);
+      const uint8_t* at = vc + page_at(vid, a.kv_heads, h, page_bytes) + (c << a.p.page_shift) + off;
+      vbyte = a.v_scale[r][(uint64_t)vid * a.kv_heads + h];
 #pragma unroll
       for (int i = 0; i < DT_TILES; ++i) vw[i] = ld16((const char*)at + ((16 * i) << a.p.page_shift));
     } else {
-      vs = 1.f;
+      vbyte = 127;
 #pragma unroll
       for (int i = 0; i < DT_TILES; ++i) vw[i] = make_uint4(0, 0, 0, 0);
     }
@@ -379,12 +381,13 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 || DIM == 64 ? 2 :
     if (step < step1) {
       ids(step);
       load_k(step);
-      load_v(step, vid);
+      load_v(step);
+      ids(step + WAVES);
     }
     for (; step < step1; step += WAVES) {
       const int32_t base = (int32_t)(t.begin + step * TOKENS);
       const bool more = step + WAVES < step1;
-      if (more) ids(step + WAVES);
+      const float ks = byte_scale(kbyte);
       v4f s[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[i] = (v4f){0.f, 0.f, 0.f, 0.f};
@@ -448,6 +451,7 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 || DIM == 64 ? 2 :
 #pragma unroll
         for (int i = 0; i < DT_TILES; ++i) vw[i] = clear_outside(vw[i], first, t.lo, t.hi);
       }
+      const float vs = byte_scale(vbyte);
 #pragma unroll
       for (int i = 0; i < DT_TILES; ++i) {
         const v8bf lo = widen8(vw[i].x, vw[i].y, vs), hi = widen8(vw[i].z, vw[i].w, vs);
@@ -457,7 +461,10 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 || DIM == 64 ? 2 :
           o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, w[1][x], o[i], 0, 0, 0);
         }
       }
-      if (more) load_v(step + WAVES, vid);
+      if (more) {
+        load_v(step + WAVES);
+        ids(step + 2 * WAVES);
+      }
     }
   }
 
@@ -597,8 +604,8 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 ? 2 : 1) void many
   float m, l, lr;
   uint32_t kid[NC], vid;  // pages of the step to load next
   uint4 kx[NC], vx[NC];
-  float ks[NC], vs;       // their scales
-  bool there;             // block tid % 4 is on a page
+  uint32_t kbyte[NC], vbyte;  // their scales; as the entries, not touched before their step
+  bool there;                 // block tid % 4 is on a page
   // A page of 64 tokens or more holds a whole step: one page, the same for
   // every thread, whose address scalar registers keep.
   const bool whole = a.p.page_shift >= 6;
@@ -622,15 +629,15 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 ? 2 : 1) void many
           kx[i] = ld16((const char*)kp + (tid + i * THREADS) * 16);
           vx[i] = ld16((const char*)vp + (((tid + i * THREADS) / 4) << a.p.page_shift) + 16 * (tid & 3));
         }
-        ks[0] = byte_scale(a.k_scale[r][(uint64_t)id * a.kv_heads + h]);
-        vs = byte_scale(a.v_scale[r][(uint64_t)id * a.kv_heads + h]);
+        kbyte[0] = a.k_scale[r][(uint64_t)id * a.kv_heads + h];
+        vbyte = a.v_scale[r][(uint64_t)id * a.kv_heads + h];
       } else {
 #pragma unroll
         for (int i = 0; i < NC; ++i) kx[i] = vx[i] = make_uint4(0, 0, 0, 0);
-        ks[0] = vs = 1.f;
+        kbyte[0] = vbyte = 127;
       }
 #pragma unroll
-      for (int i = 1; i < NC; ++i) ks[i] = ks[0];
+      for (int i = 1; i < NC; ++i) kbyte[i] = kbyte[0];
       there = id < a.p.pages;
       return;
     }
@@ -638,9 +645,9 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 ? 2 : 1) void many
     for (int i = 0; i < NC; ++i) {
       const uint32_t ch = tid + i * THREADS;
       kx[i] = make_uint4(0, 0, 0, 0);
-      ks[i] = 1.f;
+      kbyte[i] = 127;
       if (kid[i] < a.p.pages) {
-        ks[i] = byte_scale(a.k_scale[r][(uint64_t)kid[i] * a.kv_heads + h]);
+        kbyte[i] = a.k_scale[r][(uint64_t)kid[i] * a.kv_heads + h];
         kx[i] = ld16((const char*)a.k[r] + page_at(kid[i], a.kv_heads, h, page_bytes) +
                      ((base + ch / KCHUNKS) & in_page) * DIM + ch % KCHUNKS * 16);
       }
@@ -652,16 +659,18 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 ? 2 : 1) void many
       vx[i] = make_uint4(0, 0, 0, 0);
       if (there) vx[i] = ld16((const char*)at + (((tid + i * THREADS) / 4) << a.p.page_shift));
     }
-    vs = there ? byte_scale(a.v_scale[r][(uint64_t)vid * a.kv_heads + h]) : 1.f;
+    vbyte = 127;
+    if (there) vbyte = a.v_scale[r][(uint64_t)vid * a.kv_heads + h];
   };
   auto store = [&](uint32_t step, uint32_t buf) {
     const int32_t base = (int32_t)(t.begin + step * TOKENS);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const uint32_t ch = tid + i * THREADS, kr = ch / KCHUNKS, vr = ch / 4;
+      const float ks = byte_scale(kbyte[i]), vs = byte_scale(vbyte);
       uint4* kt = k_s[buf] + kr * KROW;
-      kt[(ch % KCHUNKS * 2) ^ (kr & 7)] = __builtin_bit_cast(uint4, widen8(kx[i].x, kx[i].y, ks[i]));
-      kt[(ch % KCHUNKS * 2 + 1) ^ (kr & 7)] = __builtin_bit_cast(uint4, widen8(kx[i].z, kx[i].w, ks[i]));
+      kt[(ch % KCHUNKS * 2) ^ (kr & 7)] = __builtin_bit_cast(uint4, widen8(kx[i].x, kx[i].y, ks));
+      kt[(ch % KCHUNKS * 2 + 1) ^ (kr & 7)] = __builtin_bit_cast(uint4, widen8(kx[i].z, kx[i].w, ks));
       uint4 w = vx[i];
       if (base < t.lo || base > t.hi - (int32_t)TOKENS) w = clear_outside(w, base + 16 * (int32_t)(tid & 3), t.lo, t.hi);
       uint4* vt = v_s[buf] + vr * 8;
@@ -858,7 +867,8 @@ struct AttnPlan {
   uint64_t bytes() const { return part_bytes + stat_bytes; }
 };
 
-AttnPlan plan_of(const ar_kv_cache* c, uint64_t seqs, uint64_t rows, uint64_t width, uint64_t heads, uint64_t max_rows) {
+AttnPlan plan_of(const ar_kv_cache* c, uint64_t seqs, uint64_t rows, uint64_t width, uint64_t heads, uint64_t window,
+                 uint64_t max_rows, int dtype) {
   AttnPlan p;
   const uint64_t group = heads / c->kv_heads, columns = c->kv_heads * c->nranks;
   // Rows of a sequence: the caller's word, or the mean.  Either kernel is right
@@ -869,11 +879,20 @@ AttnPlan plan_of(const ar_kv_cache* c, uint64_t seqs, uint64_t rows, uint64_t wi
   p.tiles = (uint32_t)item_count(rows, seqs, group, p.bm, 1);
   // Tiles that may be real: a sequence's last one is counted twice above.
   const uint64_t real = umax(1, umin(p.tiles, (rows * group + p.bm - 1) / p.bm + seqs - 1)) * columns;
-  const uint64_t steps = (width * c->page + TOKENS - 1) / TOKENS;
+  // Steps of a tile, at most; a window's rows start and end inside one.
+  uint64_t steps = (width * c->page + TOKENS - 1) / TOKENS;
+  if (window) steps = umin(steps, (window + p.bm / group) / TOKENS + 2);
   p.min_steps = 8;
   const uint64_t most_splits = umax(1, (steps + p.min_steps - 1) / p.min_steps);
   if (p.few) {
-    p.splits = (uint32_t)umin(most_splits, (512 + real - 1) / real);
+    // Workgroups that are resident together: two per CU, one where registers are
+    // short.  One round of them if the tiles are few, else two: shares that fill a
+    // round exactly leave CUs with one share too many (64 sequences of 8192 tokens,
+    // 8 key heads of 128: one share each 234 us, two 198; 4 sequences of 32768: 16
+    // shares 56 us, 32 69).
+    const uint64_t round = c->head_dim == 64 || (c->head_dim == 128 && dtype == DT_BF16) ? 512 : 256;
+    const uint64_t want = real < round / 2 ? round : 2 * round;
+    p.splits = (uint32_t)umin(most_splits, (want + real - 1) / real);
   } else {
     // Rounds of 512 workgroups (two per CU) over the work of each.
     p.splits = 1;
@@ -902,11 +921,11 @@ ar_status check_heads(const ar_kv_cache* c, size_t rows, size_t heads, int dtype
 extern "C" {
 
 size_t ar_cache_attention_workspace(const ar_kv_cache* cache, size_t seqs, size_t rows, size_t width, size_t heads,
-                                    size_t max_rows, ar_dtype dtype) {
+                                    size_t window, size_t max_rows, ar_dtype dtype) {
   if (check_cache(cache) != AR_OK || rows > LAYER_MAX_ROWS || seqs > (1ull << 20) || width > (1ull << 31) ||
       width * cache->page >= (1ull << 31) || check_heads(cache, rows, heads, (int)dtype) != AR_OK || !rows || !seqs)
     return 0;
-  return (size_t)plan_of(cache, seqs, rows, width, heads, max_rows).bytes();
+  return (size_t)plan_of(cache, seqs, rows, width, heads, window, max_rows, (int)dtype).bytes();
 }
 
 ar_status ar_cache_attention(const ar_kv_cache* cache, const void* const* q, size_t q_stride,
@@ -922,7 +941,7 @@ ar_status ar_cache_attention(const ar_kv_cache* cache, const void* const* q, siz
   const uint64_t es = dtype == AR_BF16 ? 2 : 4, width = heads * cache->head_dim;
   if (!stride_ok(q_stride, width, es)) return AR_ERR_INVALID;
   const int n = cache->nranks;
-  const AttnPlan plan = plan_of(cache, rows->seqs, rows->rows, rows->width, heads, max_rows);
+  const AttnPlan plan = plan_of(cache, rows->seqs, rows->rows, rows->width, heads, window, max_rows, (int)dtype);
   AttnArgs a;
   LayerBuffers b;
   for (int r = 0; r < n; ++r) {

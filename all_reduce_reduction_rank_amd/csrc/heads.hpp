@@ -64,11 +64,13 @@ __device__ __forceinline__ uint64_t page_at(uint32_t id, uint32_t kv_heads, uint
   return ((uint64_t)id * kv_heads + head) * bytes;
 }
 
-// Page of tokens j << page_shift on of sequence s, or `pages` where there is none.
+// Entry of the table for tokens j << page_shift on of sequence s: a page if it
+// is below p.pages.  (Compared where it is used and not here, so that a loop may
+// ask for it ahead of time without waiting for it.)
 __device__ __forceinline__ uint32_t page_id(const Paged& p, uint32_t s, uint64_t j) {
-  if (j >= p.width) return p.pages;
-  const uint32_t id = (uint32_t)p.table[s * p.table_stride + j];
-  return id < p.pages ? id : p.pages;
+  uint32_t id = ~0u;
+  if (j < p.width) id = (uint32_t)p.table[s * p.table_stride + j];
+  return id;
 }
 
 __device__ __forceinline__ uint32_t first_row(const Paged& p, uint32_t s) {

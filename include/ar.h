@@ -561,7 +561,7 @@ ar_status ar_cache_read(const ar_kv_cache* cache, void* const* k, void* const* v
 /* Workspace bytes of ar_cache_attention; 0 for arguments it refuses, and where
  * it needs none. */
 size_t ar_cache_attention_workspace(const ar_kv_cache* cache, size_t seqs, size_t rows, size_t width, size_t heads,
-                                    size_t max_rows, ar_dtype dtype);
+                                    size_t window, size_t max_rows, ar_dtype dtype);
 
 /* Attention over the cache.  Sequence s has L = min(at[s], width * page) cached
  * tokens, and n = first[s + 1] - first[s] query rows; row i of them stands at

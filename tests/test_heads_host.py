@@ -302,8 +302,8 @@ def test_c_abi_attention_argument_errors():
     assert att(causal=2) == 1 and att(causal=0, window=5) == 1 and att(window=5) == 5
     assert att(out=_ptrs(5)) == 1 and att(out=_ptrs(1)) == 1 and att(lse=_ptrs(6)) == 1
     long = _paged(width=4096, stride=4096)
-    need = LIB.ar_cache_attention_workspace(_record(), 3, 10, 4096, 4, 0, 1)
+    need = LIB.ar_cache_attention_workspace(_record(), 3, 10, 4096, 4, 0, 0, 1)
     assert need > 0 and att(rows=long, nbytes=need - 1) == 4 and att(rows=long, nbytes=need) == 5 and att(rows=long, ws=0) == 1
-    assert LIB.ar_cache_attention_workspace(_record(), 3, 10, 8, 4, 0, 1) == 0   # short: not shared
+    assert LIB.ar_cache_attention_workspace(_record(), 3, 10, 8, 4, 0, 0, 1) == 0   # short: not shared
     assert att(ws=0, nbytes=0) == 5
-    assert LIB.ar_cache_attention_workspace(_record(dim=80), 3, 10, 4096, 4, 0, 1) == 0
+    assert LIB.ar_cache_attention_workspace(_record(dim=80), 3, 10, 4096, 4, 0, 0, 1) == 0
