@@ -156,13 +156,13 @@ __device__ __forceinline__ uint4 clear_outside(uint4 w, int32_t at, int32_t lo, 
 
 // A tile's rows over tokens [t0, t1), a row per wave, in plain loops: what a row
 // does not see is not touched.  For tiles that hold a NaN.
-template <int DT, int DIM>
+template <int DT, int DIM, int WAVES>
 __device__ __forceinline__ void plain_rows(const AttnArgs& a, const Tile& t, uint32_t h, uint32_t r, uint32_t t0,
                                            uint32_t t1, bool shared, uint64_t slot) {
   constexpr int PER = DIM / 64;  // dimensions of a lane
   const uint32_t lane = threadIdx.x & 63, in_page = (1u << a.p.page_shift) - 1, page_bytes = DIM << a.p.page_shift;
 #pragma nounroll
-  for (uint32_t row = threadIdx.x >> 6; row < t.rows; row += 4) {
+  for (uint32_t row = threadIdx.x >> 6; row < t.rows; row += WAVES) {
     const uint32_t packed = t.r0 + row, qr = packed / a.group, head = h * a.group + packed % a.group;
     int32_t see0 = 0, see1 = t.length;
     if (a.causal) {
@@ -251,9 +251,9 @@ __device__ __forceinline__ void plain_rows(const AttnArgs& a, const Tile& t, uin
 //
 // What a row does not see must not reach it: its weight is 0, but 0 times a NaN
 // is not.  A workgroup that ends with a NaN does its rows again, by plain_rows.
-template <int DT, int DIM>
-__global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 || DIM == 64 ? 2 : 1) void few_rows_kernel(AttnArgs a) {
-  constexpr int WAVES = 4, BM = 16;
+template <int DT, int DIM, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, WAVES == 8 || DT == DT_BF16 && DIM <= 128 || DIM == 64 ? 2 : 1) void few_rows_kernel(AttnArgs a) {
+  constexpr int BM = 16;
   constexpr int KSTEPS = DIM / 32, KW = DIM / 64;  // instructions of q . k; 16-byte loads of a key
   constexpr int DT_TILES = DIM / 16;
   constexpr int QT = DT == DT_BF16 ? 1 : 3;  // terms of q
@@ -473,7 +473,7 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 || DIM == 64 ? 2 :
 #pragma unroll
   for (int i = 0; i < DT_TILES * 4; ++i) worst += o[i / 4][i % 4] * 0.f;
   if (__syncthreads_or(!(worst == 0.f))) {
-    plain_rows<DT, DIM>(a, t, h, r, t.begin + step0 * TOKENS, t.begin + step1 * TOKENS, shared, slot * BM);
+    plain_rows<DT, DIM, WAVES>(a, t, h, r, t.begin + step0 * TOKENS, t.begin + step1 * TOKENS, shared, slot * BM);
     return;
   }
 
@@ -484,7 +484,7 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 || DIM == 64 ? 2 :
 #pragma unroll
   for (int i = 0; i < DT_TILES; ++i) *(v4f*)&o_s[wave][c][16 * i + 4 * g] = o[i];
   __syncthreads();
-  for (uint32_t i = threadIdx.x; i < BM * (DIM / 4); i += 256) {
+  for (uint32_t i = threadIdx.x; i < BM * (DIM / 4); i += 64 * WAVES) {
     const uint32_t row = i / (DIM / 4), d = i % (DIM / 4) * 4;
     if (row >= t.rows) break;
     float top = m_s[0][row];
@@ -788,7 +788,7 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 ? 2 : 1) void many
 #pragma unroll
   for (int i = 0; i < DT_TILES * 16; ++i) worst += o[i / 16][i % 16] * 0.f;
   if (__syncthreads_or(!(worst == 0.f))) {
-    plain_rows<DT, DIM>(a, t, h, r, t.begin + step0 * TOKENS, t.begin + step1 * TOKENS, shared, slot);
+    plain_rows<DT, DIM, WAVES>(a, t, h, r, t.begin + step0 * TOKENS, t.begin + step1 * TOKENS, shared, slot);
     return;
   }
 
@@ -862,7 +862,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, uint32_t bm) {
 // How a call is cut.
 struct AttnPlan {
   bool few;
-  uint32_t bm, tiles, splits, min_steps;
+  uint32_t bm, tiles, splits, min_steps, waves;
   uint64_t part_bytes, stat_bytes;
   uint64_t bytes() const { return part_bytes + stat_bytes; }
 };
@@ -883,6 +883,7 @@ AttnPlan plan_of(const ar_kv_cache* c, uint64_t seqs, uint64_t rows, uint64_t wi
   uint64_t steps = (width * c->page + TOKENS - 1) / TOKENS;
   if (window) steps = umin(steps, (window + p.bm / group) / TOKENS + 2);
   p.min_steps = 8;
+  p.waves = 4;
   const uint64_t most_splits = umax(1, (steps + p.min_steps - 1) / p.min_steps);
   if (p.few) {
     // Workgroups that are resident together: two per CU, one where registers are
@@ -893,6 +894,11 @@ AttnPlan plan_of(const ar_kv_cache* c, uint64_t seqs, uint64_t rows, uint64_t wi
     const uint64_t round = c->head_dim == 64 || (c->head_dim == 128 && dtype == DT_BF16) ? 512 : 256;
     const uint64_t want = real < round / 2 ? round : 2 * round;
     p.splits = (uint32_t)umin(most_splits, (want + real - 1) / real);
+    // Half a GPU's worth of tiles over not many tokens: eight waves of one workgroup
+    // instead of a few workgroups and a second kernel to join them (16 sequences of
+    // up to 2000 tokens, 8 key heads of 128: 25 us shared, 20 so; with 8 tiles the
+    // CUs' own bandwidth is short: 15 us shared, 19 so).
+    if (p.splits > 1 && c->head_dim <= 128 && real > 64 && real <= 256 && steps <= 48) p.waves = 8, p.splits = 1;
   } else {
     // Rounds of 512 workgroups (two per CU) over the work of each.
     p.splits = 1;
@@ -980,8 +986,14 @@ ar_status ar_cache_attention(const ar_kv_cache* cache, const void* const* q, siz
   const dim3 wide(plan.tiles * plan.splits * a.kv_heads, n);
   by_head_dim((int)dtype, cache->head_dim, [&](auto dt, auto dim) {
     constexpr int DT = decltype(dt)::value, DIM = decltype(dim)::value;
-    if (plan.few) few_rows_kernel<DT, DIM><<<grid, 256, 0, (hipStream_t)stream>>>(a);
-    else many_rows_kernel<DT, DIM><<<wide, 256, 0, (hipStream_t)stream>>>(a);
+    if (plan.few) {
+      if constexpr (DIM <= 128) {
+        if (plan.waves == 8) few_rows_kernel<DT, DIM, 8><<<grid, 512, 0, (hipStream_t)stream>>>(a);
+        else few_rows_kernel<DT, DIM, 4><<<grid, 256, 0, (hipStream_t)stream>>>(a);
+      } else {
+        few_rows_kernel<DT, DIM, 4><<<grid, 256, 0, (hipStream_t)stream>>>(a);
+      }
+    } else many_rows_kernel<DT, DIM><<<wide, 256, 0, (hipStream_t)stream>>>(a);
     if (plan.splits > 1) join_kernel<DT, DIM><<<joins, 256, 0, (hipStream_t)stream>>>(a, plan.bm);
   });
   return hipGetLastError() == hipSuccess ? AR_OK : AR_ERR_HIP;
