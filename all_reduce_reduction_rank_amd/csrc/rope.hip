@@ -7,10 +7,11 @@
 //             dw = sum g n
 //
 // Both are bound by memory: every value is read once and written once
-// (backward: two reads, one write), 16 bytes per lane.  head_dim / E lanes (E
-// elements of 16 bytes) hold one head of one row; its sums go through lane
-// exchanges, and so does a rotation's other half, which lies rot / 2 elements
-// away in the same head.
+// (backward: two reads, one write).  head_dim / 8 lanes hold one head of one row,
+// 8 values each in two pieces of 4 that lie rot / 2 apart, so that both values
+// of a rotation's pair are in one lane (with neighbours in pairs, and in what is
+// not rotated, the pieces are side by side); the sums over a head go through
+// lane exchanges within rows of 16 lanes, which cost no LDS access.
 //
 // The angle of a far position needs more than fp32: pos * freq is formed in
 // fp64 in turns, only its fraction goes on in fp32.  That costs far more than
@@ -30,6 +31,7 @@ using namespace ar;
 namespace {
 
 constexpr int THREADS = 256;
+constexpr int PASSES = 1;
 
 struct RopeArgs {
   const char* x[2][MAX_RANKS];   // queries, keys
@@ -63,150 +65,167 @@ __device__ void angles(const RopeArgs& a, uint32_t t0, uint32_t n, float2* table
   }
 }
 
-template <int DT> constexpr int elems() { return DT == DT_BF16 ? 8 : 4; }
+constexpr int E = 8;  // values of a lane
+
+// Four values of a row, and back.
+template <int DT>
+struct Piece {
+  uint32_t w[DT == DT_BF16 ? 2 : 4];
+};
 
 template <int DT>
-__device__ __forceinline__ void widen(const uint4& v, float* f) {
-  if (DT == DT_BF16) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+__device__ __forceinline__ Piece<DT> load4(const char* p) {
+  Piece<DT> r;
+  if constexpr (DT == DT_BF16) {
+    const uint2 v = *(const uint2*)p;
+    r.w[0] = v.x, r.w[1] = v.y;
   } else {
-    f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+    const uint4 v = *(const uint4*)p;
+    r.w[0] = v.x, r.w[1] = v.y, r.w[2] = v.z, r.w[3] = v.w;
+  }
+  return r;
+}
+
+template <int DT>
+__device__ __forceinline__ void widen(const Piece<DT>& v, float* f) {
+  if constexpr (DT == DT_BF16) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) f[2 * i] = __uint_as_float(v.w[i] << 16), f[2 * i + 1] = __uint_as_float(v.w[i] & 0xffff0000u);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(v.w[i]);
   }
 }
 
+// Results are not read again by this call: stored past the caches' turn
+// (prompt of 4096 tokens, 8 x 6 heads of 128: 30.4 us stored plainly, 28.2 so).
 template <int DT>
-__device__ __forceinline__ uint4 narrow(const float* f) {
-  if (DT == DT_BF16)
-    return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+__device__ __forceinline__ void store4(char* p, const float* f) {
+  typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+  if constexpr (DT == DT_BF16) {
+    const v2u v = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])};
+    __builtin_nontemporal_store(v, (v2u*)p);
+  } else {
+    st16_hint<true>(p, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
+  }
 }
 
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xf, 0xf, false));
+}
+
+// The sum over L neighbouring lanes, in each of them.
 template <int L>
 __device__ __forceinline__ float sum_lanes(float v) {
-#pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  v = add_dpp<0xb1>(v);   // quad_perm 1 0 3 2
+  v = add_dpp<0x4e>(v);   // quad_perm 2 3 0 1
+  v = add_dpp<0x141>(v);  // the other four of eight (row_half_mirror)
+  if (L > 8) v = add_dpp<0x140>(v);  // the other eight of sixteen (row_mirror)
+  if (L > 16) v += __shfl_xor(v, 16);
   return v;
 }
 
-__device__ __forceinline__ uint4 from_lane(const uint4& v, int lane) {
-  return make_uint4(__shfl((int)v.x, lane), __shfl((int)v.y, lane), __shfl((int)v.z, lane), __shfl((int)v.w, lane));
-}
-
-// Where chunk c of a head finds the other half of its rotation.
-struct Turn {
-  int partner;      // lane that holds the other half (the lane itself: none, or in pairs)
-  float sign;       // of the sine term of a rotation: -1 in the first half, +1 in the second, 0 not rotated
-  uint32_t at;      // first entry of the chunk in its token's table
+// What a lane holds of a head.
+struct Share {
+  uint32_t at[2];  // first values of its pieces
+  uint32_t turn;   // first entry of its token's table
   bool rotated;
 };
 
-template <int DT, int DIM>
-__device__ __forceinline__ Turn turn_of(uint32_t chunk, uint32_t rot, int pairs) {
-  constexpr int E = elems<DT>();
-  const uint32_t rc = rot / E, hc = rc / 2, lane = threadIdx.x & 63;
-  Turn t;
-  t.rotated = chunk < rc;
-  t.partner = (int)lane;
-  t.sign = 0.f;
-  t.at = 0;
-  if (!t.rotated) return t;
-  if (pairs) {
-    t.at = chunk * (E / 2);
-    return t;
-  }
-  t.partner = (int)(chunk < hc ? lane + hc : lane - hc);
-  t.sign = chunk < hc ? -1.f : 1.f;
-  t.at = (chunk < hc ? chunk : chunk - hc) * E;
-  return t;
+__device__ __forceinline__ Share share_of(uint32_t lane, uint32_t rot, int pairs) {
+  Share s;
+  s.rotated = lane * E < rot;
+  s.at[0] = lane * E, s.at[1] = lane * E + 4, s.turn = lane * 4;
+  if (s.rotated && !pairs) s.at[0] = lane * 4, s.at[1] = rot / 2 + lane * 4;
+  return s;
 }
 
-// y turned by the angles in cs (dir +1) or back (dir -1); other: the partner's y.
-template <int DT>
-__device__ __forceinline__ void rotate(const Turn& t, int pairs, const float2* cs, float dir, const float* other, float* y) {
-  constexpr int E = elems<DT>();
-  if (!t.rotated) return;
-  if (pairs) {
+// y turned by the angles in cs (dir +1) or back (dir -1).
+__device__ __forceinline__ void rotate(bool rotated, int pairs, const float2* cs, float dir, float* y) {
+  if (!rotated) return;
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-      const float2 v = cs[i];
-      const float p = y[2 * i], q = y[2 * i + 1], s = dir * v.y;
-      y[2 * i] = p * v.x - q * s;
-      y[2 * i + 1] = q * v.x + p * s;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const float2 v = cs[i];
-      y[i] = y[i] * v.x + other[i] * (dir * t.sign * v.y);
-    }
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = cs[i];
+    const int j = pairs ? 2 * i : i, k = pairs ? 2 * i + 1 : i + 4;
+    const float p = y[j], q = y[k], s = dir * v.y;
+    y[j] = p * v.x - q * s;
+    y[k] = q * v.x + p * s;
   }
 }
 
 // Forward.  A workgroup takes `tokens` rows of every rank: thread (row, head,
-// chunk) keeps its cosines, sines and weights over the ranks, whose loads go
-// out together.
-template <int DT, int DIM>
+// lane) keeps its cosines, sines and weights over the ranks, whose loads go
+// out together, the first ones before the cosines are made.
+template <int DT, int DIM, bool PAIRS>
 __global__ __launch_bounds__(THREADS) void rope_kernel(RopeArgs a) {
-  constexpr int E = elems<DT>(), L = DIM / E;
+  constexpr int L = DIM / E, ES = DT == DT_BF16 ? 2 : 4;
   extern __shared__ float2 table[];
   const uint32_t t0 = blockIdx.x * a.tokens, half = a.rot / 2;
   const uint32_t n = min(a.tokens, a.rows - t0);
+  const uint32_t heads = a.heads[0] + a.heads[1];
+  const Share sh = share_of(threadIdx.x % L, a.rot, PAIRS);
+  constexpr int R = MAX_RANKS;  // ranks whose loads are in flight together: all
+  // every lane of a head takes part in its sums: whole heads per pass
+  const uint32_t step = gridDim.y * (THREADS / L);
+  uint32_t i = threadIdx.x / L + blockIdx.y * (THREADS / L);
+  uint32_t t, hh;
+  int kind;
+  Piece<DT> v[R][2];
+  auto load = [&] {
+    t = i / heads, hh = i - t * heads;
+    kind = hh >= a.heads[0];
+    if (kind) hh -= a.heads[0];
+    const uint64_t from = (uint64_t)(t0 + t) * a.x_pitch[kind] + (uint64_t)hh * (DIM * ES);
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+      if (j < a.nranks) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) v[j][p] = load4<DT>(a.x[kind][j] + from + sh.at[p] * ES);
+      }
+  };
+  if (i < n * heads) load();
   angles(a, t0, n, table);
   __syncthreads();
-  const uint32_t heads = a.heads[0] + a.heads[1], chunk = threadIdx.x % L;
-  const Turn turn = turn_of<DT, DIM>(chunk, a.rot, a.pairs);
-  const uint32_t other_chunk = chunk + turn.partner - (threadIdx.x & 63);
-  // every lane of a head takes part in its exchanges: whole heads per pass
-  for (uint32_t i = threadIdx.x / L + blockIdx.y * (THREADS / L); i < n * heads; i += gridDim.y * (THREADS / L)) {
-    const uint32_t t = i / heads, h = i - t * heads;
-    const int kind = h >= a.heads[0];
-    const uint32_t hh = kind ? h - a.heads[0] : h;
-    float w[E], wo[E];
-    widen<DT>(ld16(a.weight[kind] + chunk * 16), w);
-    widen<DT>(ld16(a.weight[kind] + other_chunk * 16), wo);
-    const float2* cs = table + t * half + turn.at;
-    const uint64_t from = (uint64_t)(t0 + t) * a.x_pitch[kind] + (uint64_t)hh * (L * 16) + chunk * 16;
-    const uint64_t to = ((uint64_t)(t0 + t) * a.heads[kind] + hh) * (L * 16) + chunk * 16;
-    constexpr int R = 4;  // ranks whose loads are in flight together
-    for (int r0 = 0; r0 < a.nranks; r0 += R) {
-      uint4 v[R];
+  while (i < n * heads) {
+    float w[E];
+    float2 cs[4];
 #pragma unroll
-      for (int j = 0; j < R; ++j)
-        if (r0 + j < a.nranks) v[j] = ld16(a.x[kind][r0 + j] + from);
+    for (int p = 0; p < 2; ++p) widen<DT>(load4<DT>(a.weight[kind] + sh.at[p] * ES), w + 4 * p);
+    if (sh.rotated)
 #pragma unroll
-      for (int j = 0; j < R; ++j)
-        if (r0 + j < a.nranks) {
-          float x[E], o[E];
-          widen<DT>(v[j], x);
-          widen<DT>(from_lane(v[j], turn.partner), o);
-          float q = 0.f;
+      for (int p = 0; p < 4; ++p) cs[p] = table[t * half + sh.turn + p];
+    const uint64_t to = (((uint64_t)(t0 + t) * a.heads[kind] + hh) * DIM) * ES;
 #pragma unroll
-          for (int e = 0; e < E; ++e) q += x[e] * x[e];
-          const float inv = 1.0f / sqrtf(sum_lanes<L>(q) * (1.0f / DIM) + a.eps);
+    for (int j = 0; j < R; ++j)
+      if (j < a.nranks) {
+        float x[E], q = 0.f;
 #pragma unroll
-          for (int e = 0; e < E; ++e) x[e] = x[e] * inv * w[e], o[e] = o[e] * inv * wo[e];
-          rotate<DT>(turn, a.pairs, cs, 1.f, o, x);
-          st16(a.out[kind][r0 + j] + to, narrow<DT>(x));
-        }
-    }
+        for (int p = 0; p < 2; ++p) widen<DT>(v[j][p], x + 4 * p);
+#pragma unroll
+        for (int e = 0; e < E; ++e) q += x[e] * x[e];
+        const float inv = rsqrtf(sum_lanes<L>(q) * (1.0f / DIM) + a.eps);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = x[e] * inv * w[e];
+        rotate(sh.rotated, PAIRS, cs, 1.f, x);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) store4<DT>(a.out[kind][j] + to + sh.at[p] * ES, x + 4 * p);
+      }
+    i += step;
+    if (i < n * heads) load();
   }
 }
 
 // Backward.  A workgroup takes every `blocks`-th group of `tokens` rows of one
-// rank; a thread's chunk is the same for all of them, so its share of dw stays
-// in registers until the end, one sum for queries and one for keys.
-template <int DT, int DIM>
+// rank; a thread's values of a head are the same for all of them, so its share
+// of dw stays in registers until the end, one sum for queries and one for keys.
+template <int DT, int DIM, bool PAIRS>
 __global__ __launch_bounds__(THREADS) void rope_backward_kernel(RopeArgs a) {
-  constexpr int E = elems<DT>(), L = DIM / E, PER = THREADS / L;
+  constexpr int L = DIM / E, PER = THREADS / L, ES = DT == DT_BF16 ? 2 : 4;
   extern __shared__ float2 table[];
-  const uint32_t half = a.rot / 2, chunk = threadIdx.x % L;
+  const uint32_t half = a.rot / 2;
   const int r = blockIdx.y;
-  const Turn turn = turn_of<DT, DIM>(chunk, a.rot, a.pairs);
+  const Share sh = share_of(threadIdx.x % L, a.rot, PAIRS);
   float dw[2][E] = {};
   for (uint64_t t0 = (uint64_t)blockIdx.x * a.tokens; t0 < a.rows; t0 += (uint64_t)a.blocks * a.tokens) {
     const uint32_t n = (uint32_t)min((uint64_t)a.tokens, a.rows - t0);
@@ -217,22 +236,29 @@ __global__ __launch_bounds__(THREADS) void rope_backward_kernel(RopeArgs a) {
       const uint32_t heads = a.heads[kind];
       if (!heads) continue;
       float w[E];
-      widen<DT>(ld16(a.weight[kind] + chunk * 16), w);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) widen<DT>(load4<DT>(a.weight[kind] + sh.at[p] * ES), w + 4 * p);
       for (uint32_t i = threadIdx.x / L; i < n * heads; i += PER) {
         const uint32_t t = i / heads, h = i - t * heads;
-        const uint64_t row = t0 + t, at = (uint64_t)h * (L * 16) + chunk * 16;
-        const uint4 xv = ld16(a.x[kind][r] + row * a.x_pitch[kind] + at);
-        const uint4 gv = ld16(a.dy[kind][r] + row * a.dy_pitch[kind] + at);
-        float x[E], g[E], o[E];
-        widen<DT>(xv, x);
-        widen<DT>(gv, g);
-        widen<DT>(from_lane(gv, turn.partner), o);
-        rotate<DT>(turn, a.pairs, table + t * half + turn.at, -1.f, o, g);
-        float q = 0.f;
+        const uint64_t row = t0 + t, at = (uint64_t)h * (DIM * ES);
+        float x[E], g[E];
+        float2 cs[4];
+        Piece<DT> xv[2], gv[2];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          xv[p] = load4<DT>(a.x[kind][r] + row * a.x_pitch[kind] + at + sh.at[p] * ES);
+          gv[p] = load4<DT>(a.dy[kind][r] + row * a.dy_pitch[kind] + at + sh.at[p] * ES);
+        }
+        if (sh.rotated)
+#pragma unroll
+          for (int p = 0; p < 4; ++p) cs[p] = table[t * half + sh.turn + p];
+        float q = 0.f, dot = 0.f;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) widen<DT>(xv[p], x + 4 * p), widen<DT>(gv[p], g + 4 * p);
 #pragma unroll
         for (int e = 0; e < E; ++e) q += x[e] * x[e];
-        const float inv = 1.0f / sqrtf(sum_lanes<L>(q) * (1.0f / DIM) + a.eps);
-        float dot = 0.f;
+        const float inv = rsqrtf(sum_lanes<L>(q) * (1.0f / DIM) + a.eps);
+        rotate(sh.rotated, PAIRS, cs, -1.f, g);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           x[e] *= inv;
@@ -243,12 +269,14 @@ __global__ __launch_bounds__(THREADS) void rope_backward_kernel(RopeArgs a) {
         dot = sum_lanes<L>(dot) * (1.0f / DIM);
 #pragma unroll
         for (int e = 0; e < E; ++e) g[e] = inv * (g[e] - x[e] * dot);
-        st16(a.out[kind][r] + row * a.out_pitch[kind] + at, narrow<DT>(g));
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          store4<DT>(a.out[kind][r] + row * a.out_pitch[kind] + at + sh.at[p] * ES, g + 4 * p);
       }
     }
     __syncthreads();  // the table is written again
   }
-  // The lanes of a chunk, then the waves, join their shares.
+  // The lanes with the same values, then the waves, join their shares.
   __shared__ float s[2][THREADS / 64][DIM];
 #pragma unroll
   for (int kind = 0; kind < 2; ++kind)
@@ -257,7 +285,7 @@ __global__ __launch_bounds__(THREADS) void rope_backward_kernel(RopeArgs a) {
       float v = dw[kind][e];
 #pragma unroll
       for (int o = 32; o >= L; o >>= 1) v += __shfl_xor(v, o);
-      if ((threadIdx.x & 63) < L) s[kind][threadIdx.x >> 6][chunk * E + e] = v;
+      if ((threadIdx.x & 63) < L) s[kind][threadIdx.x >> 6][sh.at[e / 4] + e % 4] = v;
     }
   __syncthreads();
   for (uint32_t i = threadIdx.x; i < 2 * DIM; i += THREADS) {
@@ -275,20 +303,23 @@ struct SumArgs {
   uint32_t blocks, dim;
 };
 
-// dw of one rank and kind: the workgroups' shares added in order, by
-// 1024 / dim slices of them.
+// 32 values of one rank's and kind's dw: the workgroups' shares added in a fixed
+// order, 32 slices of them side by side, eight loads of a slice in flight.
+constexpr uint32_t SUM_DIMS = 32, SUM_SLICES = 32;
+
 template <int DT>
-__global__ __launch_bounds__(1024) void rope_weight_kernel(SumArgs a) {
-  __shared__ float s[1024];
-  const uint32_t kind = blockIdx.x, r = blockIdx.y, d = threadIdx.x % a.dim, slice = threadIdx.x / a.dim;
-  const uint32_t slices = 1024 / a.dim;
-  const float* p = a.part + ((uint64_t)r * 2 + kind) * a.blocks * a.dim;
+__global__ __launch_bounds__(SUM_DIMS * SUM_SLICES) void rope_weight_kernel(SumArgs a) {
+  __shared__ float s[SUM_SLICES][SUM_DIMS];
+  const uint32_t kind = blockIdx.x, r = blockIdx.y, lane = threadIdx.x % SUM_DIMS, slice = threadIdx.x / SUM_DIMS;
+  const uint32_t d = blockIdx.z * SUM_DIMS + lane;
+  const float* p = a.part + ((uint64_t)r * 2 + kind) * a.blocks * a.dim + d;
   float v = 0.f;
-  for (uint32_t b = slice; b < a.blocks; b += slices) v += p[(uint64_t)b * a.dim + d];
-  s[threadIdx.x] = v;
+#pragma unroll 8
+  for (uint32_t b = slice; b < a.blocks; b += SUM_SLICES) v += p[(uint64_t)b * a.dim];
+  s[slice][lane] = v;
   __syncthreads();
-  if (slice == 0 && a.out[kind][r]) {
-    for (uint32_t i = 1; i < slices; ++i) v += s[i * a.dim + d];
+  if (slice == 0) {
+    for (uint32_t i = 1; i < SUM_SLICES; ++i) v += s[i][lane];
     Elem<DT>::stf(a.out[kind][r] + (uint64_t)d * Elem<DT>::size, v);
   }
 }
@@ -317,12 +348,14 @@ ar_status check_shape(int n, size_t rows, size_t heads, size_t kv_heads, size_t 
 
 template <int DT, int DIM>
 void launch_forward(const RopeArgs& a, dim3 grid, uint32_t lds, hipStream_t stream) {
-  rope_kernel<DT, DIM><<<grid, THREADS, lds, stream>>>(a);
+  if (a.pairs) rope_kernel<DT, DIM, true><<<grid, THREADS, lds, stream>>>(a);
+  else rope_kernel<DT, DIM, false><<<grid, THREADS, lds, stream>>>(a);
 }
 
 template <int DT, int DIM>
 void launch_backward(const RopeArgs& a, dim3 grid, uint32_t lds, hipStream_t stream) {
-  rope_backward_kernel<DT, DIM><<<grid, THREADS, lds, stream>>>(a);
+  if (a.pairs) rope_backward_kernel<DT, DIM, true><<<grid, THREADS, lds, stream>>>(a);
+  else rope_backward_kernel<DT, DIM, false><<<grid, THREADS, lds, stream>>>(a);
 }
 
 }  // namespace
@@ -373,10 +406,10 @@ ar_status ar_qk_norm_rope(int nranks, const void* const* q, size_t q_stride, con
   a.nranks = nranks;
   a.pairs = pairs;
   a.eps = eps;
-  // Two passes of 16-byte chunks a thread, or one token's heads shared by
+  // One pass a thread, or one token's heads shared by
   // several workgroups where there are few tokens.
-  const uint64_t per_token = (heads + kv_heads) * head_dim * es / 16;  // threads
-  a.tokens = (uint32_t)umin(umax(2 * THREADS / per_token, 1), 16);
+  const uint64_t per_token = (heads + kv_heads) * head_dim / E;  // threads
+  a.tokens = (uint32_t)umin(umax(PASSES * THREADS / per_token, 1), 16);
   const uint32_t groups = (uint32_t)((rows + a.tokens - 1) / a.tokens);
   const uint64_t passes = (a.tokens * per_token + THREADS - 1) / THREADS;
   const uint32_t split = (uint32_t)umax(1, umin(passes, 512 / groups));
@@ -471,9 +504,9 @@ ar_status ar_qk_norm_rope_backward(int nranks, const void* const* dq_out, const 
   s.part = a.part;
   s.blocks = a.blocks;
   s.dim = (uint32_t)head_dim;
-  const dim3 grid(kv_heads ? 2 : 1, nranks);
-  if (dtype == AR_BF16) rope_weight_kernel<DT_BF16><<<grid, 1024, 0, (hipStream_t)stream>>>(s);
-  else rope_weight_kernel<DT_F32><<<grid, 1024, 0, (hipStream_t)stream>>>(s);
+  const dim3 grid(kv_heads ? 2 : 1, nranks, (uint32_t)head_dim / SUM_DIMS);
+  if (dtype == AR_BF16) rope_weight_kernel<DT_BF16><<<grid, SUM_DIMS * SUM_SLICES, 0, (hipStream_t)stream>>>(s);
+  else rope_weight_kernel<DT_F32><<<grid, SUM_DIMS * SUM_SLICES, 0, (hipStream_t)stream>>>(s);
   return hipGetLastError() == hipSuccess ? AR_OK : AR_ERR_HIP;
 }
 
