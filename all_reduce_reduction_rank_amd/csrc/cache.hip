@@ -60,19 +60,30 @@ __device__ __forceinline__ bool piece_of(const Paged& p, uint64_t item, Piece* o
   return true;
 }
 
-// Eight elements of a row.
+// Eight elements of a row, as they are stored.
 template <int DT>
-__device__ __forceinline__ void load8(const char* p, float* f) {
-  const uint4 v = ld16(p);
-  if (DT == DT_BF16) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+struct Eight {
+  uint4 w[DT == DT_BF16 ? 1 : 2];
+};
+
+template <int DT>
+__device__ __forceinline__ Eight<DT> load8(const char* p) {
+  Eight<DT> r;
+  r.w[0] = ld16(p);
+  if constexpr (DT != DT_BF16) r.w[1] = ld16(p + 16);
+  return r;
+}
+
+template <int DT>
+__device__ __forceinline__ void widen(const Eight<DT>& v, float* f) {
+  const uint32_t w[4] = {v.w[0].x, v.w[0].y, v.w[0].z, v.w[0].w};
+  if constexpr (DT == DT_BF16) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   } else {
-    const uint4 u = ld16(p + 16);
-    const uint32_t w[8] = {v.x, v.y, v.z, v.w, u.x, u.y, u.z, u.w};
+    const uint32_t u[4] = {v.w[1].x, v.w[1].y, v.w[1].z, v.w[1].w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(w[i]), f[4 + i] = __uint_as_float(u[i]);
   }
 }
 
@@ -86,6 +97,14 @@ __device__ __forceinline__ void store8(char* p, const float* f) {
       st16(p + 16 * i, make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]),
                                   __float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3])));
   }
+}
+
+// Four words of four bytes, turned: byte i of word j becomes byte j of word i.
+__device__ __forceinline__ void turn4(uint32_t* w) {
+  const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x05010400), b = __builtin_amdgcn_perm(w[1], w[0], 0x07030602);
+  const uint32_t c = __builtin_amdgcn_perm(w[3], w[2], 0x05010400), d = __builtin_amdgcn_perm(w[3], w[2], 0x07030602);
+  w[0] = __builtin_amdgcn_perm(c, a, 0x05040100), w[1] = __builtin_amdgcn_perm(c, a, 0x07060302);
+  w[2] = __builtin_amdgcn_perm(d, b, 0x05040100), w[3] = __builtin_amdgcn_perm(d, b, 0x07060302);
 }
 
 // Four codes at another scale: what they stand for, rounded again.
@@ -109,32 +128,71 @@ __device__ float block_max(float m, float* s, uint32_t* byte) {
   return m;
 }
 
+// Tokens a workgroup has in registers at a time: BATCH of each thread.  A page of
+// 64 tokens of 128 values is one batch and read once; what is longer is read a
+// second time, from L2.
+constexpr int BATCH = 4;
+
+// Bytes of the tokens [lo, hi) in a word that holds tokens 4 q .. 4 q + 3.
+__device__ __forceinline__ uint32_t bytes_of(uint32_t q, uint32_t lo, uint32_t hi) {
+  uint32_t m = 0;
+#pragma unroll
+  for (uint32_t e = 0; e < 4; ++e)
+    if (4 * q + e >= lo && 4 * q + e < hi) m |= 0xffu << (8 * e);
+  return m;
+}
+
 template <int DT, int DIM>
 __global__ __launch_bounds__(THREADS) void write_kernel(CacheArgs a) {
-  constexpr uint32_t ES = DT == DT_BF16 ? 2 : 4, LANES = DIM / 8;  // lanes of a token
-  constexpr uint32_t PITCH = DIM + 4;                              // of a token's codes in LDS
-  extern __shared__ uint8_t tile[];                                // values: [page][PITCH]
+  constexpr uint32_t ES = DT == DT_BF16 ? 2 : 4, LANES = DIM / 8, ROWS = THREADS / LANES;  // lanes of a token, tokens a pass
+  constexpr uint32_t PITCH = DIM + 4;                                                      // of a token's codes in LDS
+  extern __shared__ uint8_t tile[];                                                        // values: [page][PITCH]
   __shared__ float maxima[THREADS / 64 + 1];
   const uint32_t kind = blockIdx.y & 1, r = blockIdx.z, head = blockIdx.y >> 1;
   Piece pc;
   if (!piece_of(a.p, blockIdx.x, &pc) || pc.id >= a.p.pages) return;
   const uint32_t page = 1u << a.p.page_shift, count = pc.hi - pc.lo;
-  const char* x = a.x[kind][r] + (uint64_t)pc.row * a.pitch[kind] + (uint64_t)head * (DIM * ES);
+  const uint32_t lane = threadIdx.x % LANES, row = threadIdx.x / LANES;
+  const char* x = a.x[kind][r] + (uint64_t)pc.row * a.pitch[kind] + (uint64_t)head * (DIM * ES) + lane * 8 * ES;
   uint8_t* codes = a.codes[kind][r] + page_at(pc.id, a.kv_heads, head, page * DIM);
   uint8_t* scale = a.scale[kind][r] + (uint64_t)pc.id * a.kv_heads + head;
   // one thread reads the byte and writes it, in that order
   uint32_t held = threadIdx.x == 0 ? *scale : 0;
-  const uint32_t lane = threadIdx.x % LANES;
+
+  Eight<DT> v[BATCH];
+  auto load = [&](uint32_t i0) {
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) {
+      const uint32_t i = i0 + row + j * ROWS;
+      if (i < count) v[j] = load8<DT>(x + (uint64_t)i * a.pitch[kind]);
+    }
+  };
+  load(0);
+  // Values: words q0 .. of every dimension change.  A thread's first ones are asked
+  // for here where some of their bytes stay.
+  const uint32_t q1 = (pc.hi + 3) / 4, q0 = pc.lo / 4;
+  uint32_t old[4] = {};
+  if (kind == 1 && threadIdx.x < (q1 - q0) * (DIM / 4)) {
+    const uint32_t words = q1 - q0, dq = threadIdx.x / words, q = q0 + threadIdx.x - dq * words;
+    if (bytes_of(q, pc.lo, pc.hi) != ~0u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) old[e] = *(const uint32_t*)(codes + (4 * dq + e) * page + q * 4);
+  }
 
   float m = 0.f;
-  for (uint32_t i = threadIdx.x / LANES; i < count; i += THREADS / LANES) {
-    float f[8];
-    load8<DT>(x + i * a.pitch[kind] + lane * 8 * ES, f);
+  for (uint32_t i0 = 0; i0 < count; i0 += BATCH * ROWS) {
+    if (i0) load(i0);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float v = fabsf(f[e]);
-      m = fmaxf(m, v < __builtin_inff() ? v : 0.f);
-    }
+    for (int j = 0; j < BATCH; ++j)
+      if (i0 + row + j * ROWS < count) {
+        float f[8];
+        widen<DT>(v[j], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float w = fabsf(f[e]);
+          m = fmaxf(m, w < __builtin_inff() ? w : 0.f);
+        }
+      }
   }
   uint32_t byte = scale_byte(block_max(m, maxima, &held));
   const uint32_t before = held < SCALE_MIN ? SCALE_MIN : held > SCALE_MAX ? SCALE_MAX : held;
@@ -144,17 +202,23 @@ __global__ __launch_bounds__(THREADS) void write_kernel(CacheArgs a) {
   const float half = 254 - byte < SCALE_MIN ? 0.5f : 1.f;  // 2^-127 is not a normal number
   if (threadIdx.x == 0) *scale = (uint8_t)byte;
 
-  for (uint32_t i = threadIdx.x / LANES; i < count; i += THREADS / LANES) {
-    float f[8];
-    load8<DT>(x + i * a.pitch[kind] + lane * 8 * ES, f);
+  for (uint32_t i0 = 0; i0 < count; i0 += BATCH * ROWS) {
+    if (count > BATCH * ROWS) load(i0);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] *= half;
-    const uint2 w = make_uint2(codes_of(f, inv), codes_of(f + 4, inv));
-    if (kind == 0) {
-      *(uint2*)(codes + (pc.lo + i) * DIM + lane * 8) = w;
-    } else {
-      uint32_t* t = (uint32_t*)(tile + i * PITCH + lane * 8);
-      t[0] = w.x, t[1] = w.y;
+    for (int j = 0; j < BATCH; ++j) {
+      const uint32_t i = i0 + row + j * ROWS;
+      if (i >= count) continue;
+      float f[8];
+      widen<DT>(v[j], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] *= half;
+      const uint2 w = make_uint2(codes_of(f, inv), codes_of(f + 4, inv));
+      if (kind == 0) {
+        *(uint2*)(codes + (pc.lo + i) * DIM + lane * 8) = w;
+      } else {
+        uint32_t* t = (uint32_t*)(tile + i * PITCH + lane * 8);
+        t[0] = w.x, t[1] = w.y;
+      }
     }
   }
   if (kind == 0) {
@@ -166,71 +230,98 @@ __global__ __launch_bounds__(THREADS) void write_kernel(CacheArgs a) {
     return;
   }
   __syncthreads();
-  // Values: dword q of dimension d holds tokens 4 q .. 4 q + 3.
-  const uint32_t q0 = grows ? 0 : pc.lo / 4, q1 = (pc.hi + 3) / 4, words = q1 - q0;
-  for (uint32_t i = threadIdx.x; i < words * DIM; i += THREADS) {
-    const uint32_t d = i / words, q = q0 + i - d * words;
-    uint32_t* at = (uint32_t*)(codes + d * page + q * 4);
-    uint32_t w = 0;
-    const bool whole = q * 4 >= pc.lo && q * 4 + 4 <= pc.hi;
-    if (!whole) {
-      w = *at;
-      const uint32_t old = grows ? rescaled(w, from * half, inv) : w;
-      // tokens before lo are the page's, those from hi on stay as they are
-#pragma unroll
-      for (uint32_t e = 0; e < 4; ++e)
-        if (q * 4 + e < pc.lo) w = (w & ~(0xffu << (8 * e))) | (old & (0xffu << (8 * e)));
-    }
+  // Four dimensions of four tokens per item, turned in registers.
+  const uint32_t words = q1 - q0;
+  for (uint32_t i = threadIdx.x; i < words * (DIM / 4); i += THREADS) {
+    const uint32_t dq = i / words, q = q0 + i - dq * words, fresh = bytes_of(q, pc.lo, pc.hi);
+    uint32_t w[4];
 #pragma unroll
     for (uint32_t e = 0; e < 4; ++e) {
-      const uint32_t t = q * 4 + e;
-      if (t >= pc.lo && t < pc.hi) w = (w & ~(0xffu << (8 * e))) | ((uint32_t)tile[(t - pc.lo) * PITCH + d] << (8 * e));
+      const uint32_t t = 4 * q + e;
+      w[e] = t >= pc.lo && t < pc.hi ? *(const uint32_t*)(tile + (t - pc.lo) * PITCH + 4 * dq) : 0;
     }
-    *at = w;
+    turn4(w);
+    if (fresh != ~0u) {
+      // tokens before lo are the page's (at its new scale), those from hi on stay as they are
+      const uint32_t first = bytes_of(q, 0, pc.lo);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (i >= THREADS) old[e] = *(const uint32_t*)(codes + (4 * dq + e) * page + q * 4);
+        const uint32_t moved = grows ? rescaled(old[e], from * half, inv) : old[e];
+        w[e] = (w[e] & fresh) | (moved & first) | (old[e] & ~(fresh | first));
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) *(uint32_t*)(codes + (4 * dq + e) * page + q * 4) = w[e];
   }
+  if (grows)  // whole words of earlier tokens
+    for (uint32_t i = threadIdx.x; i < q0 * DIM; i += THREADS) {
+      uint32_t* at = (uint32_t*)(codes + i / q0 * page + i % q0 * 4);
+      *at = rescaled(*at, from * half, inv);
+    }
 }
 
 template <int DT, int DIM>
 __global__ __launch_bounds__(THREADS) void read_kernel(CacheArgs a) {
-  constexpr uint32_t ES = DT == DT_BF16 ? 2 : 4, LANES = DIM / 8, PITCH = DIM + 4;
+  constexpr uint32_t ES = DT == DT_BF16 ? 2 : 4, LANES = DIM / 8, ROWS = THREADS / LANES, PITCH = DIM + 4;
   extern __shared__ uint8_t tile[];
   const uint32_t kind = blockIdx.y & 1, r = blockIdx.z, head = blockIdx.y >> 1;
   Piece pc;
   if (!piece_of(a.p, blockIdx.x, &pc)) return;
   const uint32_t page = 1u << a.p.page_shift, count = pc.hi - pc.lo;
   const bool there = pc.id < a.p.pages;
-  char* x = (char*)a.x[kind][r] + (uint64_t)pc.row * a.pitch[kind] + (uint64_t)head * (DIM * ES);
+  const uint32_t lane = threadIdx.x % LANES, row = threadIdx.x / LANES;
+  char* x = (char*)a.x[kind][r] + (uint64_t)pc.row * a.pitch[kind] + (uint64_t)head * (DIM * ES) + lane * 8 * ES;
   const uint8_t* codes = a.codes[kind][r] + page_at(there ? pc.id : 0, a.kv_heads, head, page * DIM);
-  float scale = 0.f;
-  if (there) {
-    const uint32_t byte = a.scale[kind][r][(uint64_t)pc.id * a.kv_heads + head];
-    scale = scale_of(byte < SCALE_MIN ? SCALE_MIN : byte > SCALE_MAX ? SCALE_MAX : byte);
-  }
+  uint32_t byte = 127;
+  if (there) byte = a.scale[kind][r][(uint64_t)pc.id * a.kv_heads + head];
+  const uint32_t q0 = pc.lo / 4, words = (pc.hi + 3) / 4 - q0;
   if (kind == 1 && there) {
-    const uint32_t q0 = pc.lo / 4, words = (pc.hi + 3) / 4 - q0;
-    for (uint32_t i = threadIdx.x; i < words * DIM; i += THREADS) {
-      const uint32_t d = i / words, q = i - d * words;
-      const uint32_t w = *(const uint32_t*)(codes + d * page + (q0 + q) * 4);
+    // Four dimensions of four tokens per item, BATCH items of a thread in flight.
+    for (uint32_t i0 = threadIdx.x; i0 < words * (DIM / 4); i0 += BATCH * THREADS) {
+      uint32_t w[BATCH][4];
 #pragma unroll
-      for (uint32_t e = 0; e < 4; ++e) tile[(q * 4 + e) * PITCH + d] = (uint8_t)(w >> (8 * e));
+      for (int j = 0; j < BATCH; ++j) {
+        const uint32_t i = i0 + j * THREADS, dq = i / words, q = i - dq * words;
+        if (i < words * (DIM / 4))
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[j][e] = *(const uint32_t*)(codes + (4 * dq + e) * page + (q0 + q) * 4);
+      }
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j) {
+        const uint32_t i = i0 + j * THREADS, dq = i / words, q = i - dq * words;
+        if (i >= words * (DIM / 4)) continue;
+        turn4(w[j]);
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e) *(uint32_t*)(tile + (4 * q + e) * PITCH + 4 * dq) = w[j][e];
+      }
     }
     __syncthreads();
   }
-  const uint32_t lane = threadIdx.x % LANES;
-  for (uint32_t i = threadIdx.x / LANES; i < count; i += THREADS / LANES) {
-    uint2 w = make_uint2(0, 0);
-    if (there) {
+  const float scale = scale_of(byte < SCALE_MIN ? SCALE_MIN : byte > SCALE_MAX ? SCALE_MAX : byte);
+  for (uint32_t i0 = row; i0 < count; i0 += BATCH * ROWS) {
+    uint2 w[BATCH];
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) {
+      const uint32_t i = i0 + j * ROWS;
+      w[j] = make_uint2(0, 0);
+      if (i >= count || !there) continue;
       if (kind == 0) {
-        w = *(const uint2*)(codes + (pc.lo + i) * DIM + lane * 8);
+        w[j] = *(const uint2*)(codes + (pc.lo + i) * DIM + lane * 8);
       } else {
         const uint32_t* t = (const uint32_t*)(tile + (i + pc.lo % 4) * PITCH + lane * 8);
-        w = make_uint2(t[0], t[1]);
+        w[j] = make_uint2(t[0], t[1]);
       }
     }
-    float f[8];
-    values_of(w.x, scale, f);
-    values_of(w.y, scale, f + 4);
-    store8<DT>(x + i * a.pitch[kind] + lane * 8 * ES, f);
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) {
+      const uint32_t i = i0 + j * ROWS;
+      if (i >= count) continue;
+      float f[8];
+      values_of(w[j].x, scale, f);
+      values_of(w[j].y, scale, f + 4);
+      store8<DT>(x + (uint64_t)i * a.pitch[kind], f);
+    }
   }
 }
 
