@@ -116,15 +116,16 @@ def _declare(lib):
     lib.ar_linear_cross_entropy_workspace.argtypes = [I, S, S, S, I, I, S]
     lib.ar_linear_cross_entropy.argtypes = [I, PP, PP, P, PP, PP, S, S, S, I, P, S, P]
     lib.ar_linear_cross_entropy_backward.argtypes = [I, P, PP, PP, P, PP, PP, PP, S, S, S, I, S, P, S, P]
+    # (pointer arrays as ctypes arrays or as bytes)
     F, C, R = ctypes.c_float, ctypes.POINTER(CacheRecord), ctypes.POINTER(PagedRows)
-    lib.ar_qk_norm_rope.argtypes = [I, PP, S, PP, S, P, P, P, P, PP, PP, S, S, S, S, S, I, F, I, P]
+    lib.ar_qk_norm_rope.argtypes = [I, P, S, P, S, P, P, P, P, P, P, S, S, S, S, S, I, F, I, P]
     lib.ar_qk_norm_rope_workspace.argtypes = [I, S, S, S, S]
-    lib.ar_qk_norm_rope_backward.argtypes = ([I, PP, PP, PP, S, PP, S, P, P, P, P, PP, S, PP, S, PP, PP, S, S, S, S, S, I, F, I,
+    lib.ar_qk_norm_rope_backward.argtypes = ([I, P, P, P, S, P, S, P, P, P, P, P, S, P, S, P, P, S, S, S, S, S, I, F, I,
                                               P, S, P])
-    lib.ar_cache_write.argtypes = [C, PP, S, PP, S, R, I, P]
-    lib.ar_cache_read.argtypes = [C, PP, PP, R, I, P]
+    lib.ar_cache_write.argtypes = [C, P, S, P, S, R, I, P]
+    lib.ar_cache_read.argtypes = [C, P, P, R, I, P]
     lib.ar_cache_attention_workspace.argtypes = [C, S, S, S, S, S, S, I]
-    lib.ar_cache_attention.argtypes = [C, PP, S, R, PP, PP, S, F, I, S, S, I, P, S, P]
+    lib.ar_cache_attention.argtypes = [C, P, S, R, P, P, S, F, I, S, S, I, P, S, P]
     lib.ar_status_string.argtypes = [I]
     lib.ar_status_string.restype = ctypes.c_char_p
     for name in SYMBOLS:
@@ -164,14 +165,19 @@ def _proto(name):
 
 
 _TORCH = None
+_MARSHAL = None  # the checks of the attention operators' tensors in C++ (csrc/marshal.cpp), where built
 _DT_NAMES = None  # torch dtype -> "f32" / "bf16" / "i32"
 
 
 def _torch():
-    global _TORCH, _DT_NAMES
+    global _TORCH, _DT_NAMES, _MARSHAL
     if _TORCH is None:
         import torch
 
+        try:
+            from . import _marshal as _MARSHAL  # noqa: N812
+        except ImportError:
+            pass  # the same checks in Python
         _DT_NAMES = {torch.float32: "f32", torch.bfloat16: "bf16", torch.int32: "i32"}
         _TORCH = torch
     return _TORCH
@@ -687,6 +693,10 @@ def _head_list(ts, n, rows, width, dtype, device, what):
     """(pointer array, stride) of N rank tensors [rows, heads, head_dim] whose
     rows are contiguous and all the same distance apart (views of a wider
     matrix are fine); `width` = (heads, head_dim) or None for the first one's."""
+    if _MARSHAL is not None and width is not None and len(ts) == n:
+        found = _MARSHAL.rows(ts, dtype, device, rows, *width)
+        if found is not None:
+            return found
     if len(ts) != n:
         raise ValueError(f"{what} holds {len(ts)} rank buffers; the call needs {n}")
     first = ts[0]
@@ -710,6 +720,24 @@ def _head_list(ts, n, rows, width, dtype, device, what):
     return _PTRS[n](*ptrs), strides[0] if rows > 1 else shape[1] * dim
 
 
+def _rank_list(ts, n, shape, dtype, device, what):
+    """``_layer_list`` of one shape, in C++ where that is built."""
+    if _MARSHAL is not None and len(ts) == n:
+        found = _MARSHAL.contiguous(ts, dtype, device, shape)
+        if found is not None:
+            return found
+    return _layer_list(ts, n, shape, dtype, device, what)
+
+
+def _shared_vector(t, n, dtype, device, what):
+    """``_layer_vector``, in C++ where that is built."""
+    if _MARSHAL is not None:
+        found = _MARSHAL.vector(t, dtype, device, n)
+        if found is not None:
+            return found
+    return _layer_vector(t, n, dtype, device, what)
+
+
 def _rope_inputs(q, k, q_weight, k_weight, pos, freq):
     """(n, device, dtype, name, sizes, pointers and strides) of a qk_norm_rope call."""
     torch = _torch()
@@ -718,20 +746,20 @@ def _rope_inputs(q, k, q_weight, k_weight, pos, freq):
     if q[0].dim() != 3:
         raise ValueError("q must be [rows, heads, head_dim] on every rank")
     rows, heads, dim = q[0].shape
-    qp, qs = _head_list(q, n, rows, None, dtype, device, "q")
+    qp, qs = _head_list(q, n, rows, (heads, dim), dtype, device, "q")
     kp, ks, kw, kv = None, 0, None, 0
     if (k is None) != (k_weight is None):
         raise ValueError("k and k_weight are given together or not at all")
     if k is not None:
         kp, ks = _head_list(k, n, rows, (k[0].shape[1] if k[0].dim() == 3 else 0, dim), dtype, device, "k")
         kv = k[0].shape[1]
-        kw = _layer_vector(k_weight, dim, dtype, device, "k_weight")
+        kw = _shared_vector(k_weight, dim, dtype, device, "k_weight")
     rot = 0 if freq is None else 2 * freq.numel()
     if rot and pos is None:
         raise ValueError("freq needs pos")
-    args = [_layer_vector(q_weight, dim, dtype, device, "q_weight"), kw,
-            _layer_vector(pos, rows, torch.int64, device, "pos") if rot else None,
-            _layer_vector(freq, rot // 2, torch.float32, device, "freq") if rot else None]
+    args = [_shared_vector(q_weight, dim, dtype, device, "q_weight"), kw,
+            _shared_vector(pos, rows, torch.int64, device, "pos") if rot else None,
+            _shared_vector(freq, rot // 2, torch.float32, device, "freq") if rot else None]
     return n, device, dtype, dt, (rows, heads, kv, dim, rot), (qp, qs, kp, ks), args
 
 
@@ -747,10 +775,10 @@ def qk_norm_rope(q, k, q_weight, k_weight, pos, freq, eps=1e-6, pairs=False, q_o
     no rotation).  k and k_weight None: queries alone, k_out is None.  q_out,
     k_out: contiguous, allocated when None.  head_dim 64, 128 or 256; fp32 and bf16."""
     n, device, dtype, dt, (rows, heads, kv, dim, rot), x, shared = _rope_inputs(q, k, q_weight, k_weight, pos, freq)
-    qo = _layer_list(q_out, n, (rows, heads, dim), dtype, device, "q_out") if q_out is not None else None
+    qo = _rank_list(q_out, n, (rows, heads, dim), dtype, device, "q_out") if q_out is not None else None
     if k is None and k_out is not None:
         raise ValueError("k_out needs k")
-    ko = _layer_list(k_out, n, (rows, kv, dim), dtype, device, "k_out") if k_out is not None else None
+    ko = _rank_list(k_out, n, (rows, kv, dim), dtype, device, "k_out") if k_out is not None else None
     _on_device(device, stream)
     scratch = _Scratch(stream, device)
     if qo is None:
@@ -781,11 +809,11 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, pos, freq, e
     n, device, dtype, dt, (rows, heads, kv, dim, rot), x, shared = _rope_inputs(q, k, q_weight, k_weight, pos, freq)
     if k is None and not dk_out is dk is dk_weight is None:
         raise ValueError("dk_out, dk and dk_weight need k")
-    go = [_layer_list(dq_out, n, (rows, heads, dim), dtype, device, "dq_out"),
-          _layer_list(dk_out, n, (rows, kv, dim), dtype, device, "dk_out") if k is not None else None]
+    go = [_rank_list(dq_out, n, (rows, heads, dim), dtype, device, "dq_out"),
+          _rank_list(dk_out, n, (rows, kv, dim), dtype, device, "dk_out") if k is not None else None]
     given = [_head_list(dq, n, rows, (heads, dim), dtype, device, "dq") if dq is not None else None,
              _head_list(dk, n, rows, (kv, dim), dtype, device, "dk") if dk is not None else None]
-    sums = [_layer_list(t, n, (dim,), dtype, device, what) if t is not None else None
+    sums = [_rank_list(t, n, (dim,), dtype, device, what) if t is not None else None
             for what, t in (("dq_weight", dq_weight), ("dk_weight", dk_weight))]
     _on_device(device, stream)
     scratch = _Scratch(stream, device)
@@ -848,6 +876,10 @@ class KVCache:
 
 def _paged_rows(cache, table, first, at, rows, what):
     """ar_paged_rows of a call's sequences."""
+    if _MARSHAL is not None:
+        found = _MARSHAL.sequences(table, first, at, cache.device)
+        if found is not None:
+            return PagedRows(*found, rows)
     torch = _TORCH
     for name, t, dim in (("table", table, 2), ("first", first, 1), (what, at, 1)):
         if t.dtype is not torch.int32:
@@ -905,8 +937,8 @@ def cache_read(cache, table, first, start, k, v, stream=None):
     if k[0].dim() != 3:
         raise ValueError("k must be [rows, kv_heads, head_dim] on every rank")
     shape, dtype = (k[0].shape[0], cache.kv_heads, cache.head_dim), k[0].dtype
-    kp = _layer_list(k, n, shape, dtype, device, "k")
-    vp = _layer_list(v, n, shape, dtype, device, "v")
+    kp = _rank_list(k, n, shape, dtype, device, "k")
+    vp = _rank_list(v, n, shape, dtype, device, "v")
     paged = _paged_rows(cache, table, first, start, shape[0], "start")
     _on_device(device, stream)
     _check(_lib().ar_cache_read(cache.record, kp, vp, paged, DTYPES[dt], _stream_handle(stream, device)), "ar_cache_read")
@@ -949,8 +981,8 @@ def cache_attention(q, cache, table, first, length, scale=None, causal=True, win
         raise ValueError("window and max_rows must not be negative")
     if window and not causal:
         raise ValueError("window needs causal")
-    op = _layer_list(out, n, (rows, heads, dim), dtype, device, "out") if out is not None else None
-    lp = _layer_list(lse, n, (rows, heads), _TORCH.float32, device, "lse") if lse is not None else None
+    op = _rank_list(out, n, (rows, heads, dim), dtype, device, "out") if out is not None else None
+    lp = _rank_list(lse, n, (rows, heads), _TORCH.float32, device, "lse") if lse is not None else None
     paged = _paged_rows(cache, table, first, length, rows, "length")
     _on_device(device, stream)
     scratch = _Scratch(stream, device)

@@ -7,12 +7,14 @@ file so it travels with the source tree.
 import os
 import subprocess
 import sys
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libar.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 SOURCES = ("api.hip", "kernels.hip", "rmsnorm.hip", "noalloc.hip", "ceiling.hip", "ffn.hip", "xent.hip", "rope.hip", "cache.hip", "attention.hip",
            "products.hip", "products_bf16.hip", "products_f32.hip")
 
@@ -30,9 +32,26 @@ def _hipcc():
     return path if os.path.exists(path) else "hipcc"
 
 
+def build_marshal(out: str = MARSHAL) -> str:
+    """Compile the binding's argument checks (host code against torch's headers)."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"]]
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-I{i}" for i in inc], os.path.join(CSRC, "marshal.cpp"), "-L" + os.path.join(root, "lib"), "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-o", out + ".tmp"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on marshal.cpp:\n{res.stderr}")
+    os.replace(out + ".tmp", out)
+    return out
+
+
 def build(verbose: bool = False, out: str = LIB, defines=()) -> str:
     """Compile every source and link the library (libar.so next to this file
-    unless `out` says otherwise); `defines` are extra -D options."""
+    unless `out` says otherwise); `defines` are extra -D options.  With the
+    library goes the binding's compiled half (_marshal.so)."""
     hipcc = _hipcc()
     with tempfile.TemporaryDirectory(prefix="ar_build_") as tmp:
         def compile_one(src):
@@ -45,8 +64,11 @@ def build(verbose: bool = False, out: str = LIB, defines=()) -> str:
                 sys.stderr.write(res.stderr)
             return obj
 
-        with ThreadPoolExecutor(len(SOURCES)) as pool:
+        with ThreadPoolExecutor(len(SOURCES) + 1) as pool:
+            checks = pool.submit(build_marshal) if out == LIB else None
             objs = list(pool.map(compile_one, SOURCES))
+            if checks:
+                checks.result()
         tmp_lib = out + ".tmp"
         cmd = [hipcc, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp_lib]
         res = subprocess.run(cmd, capture_output=True, text=True)

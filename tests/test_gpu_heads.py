@@ -264,6 +264,8 @@ ATT = [  # ranks, heads, kv_heads, dim, page, cached tokens, query rows, causal,
     (2, 1, 1, 128, 64, [1500], [40], True, 0, "bf16", 40),       # shared among workgroups
     (1, 2, 2, 128, 64, [2000], [1], False, 0, "f32", 1),
     (1, 64, 1, 128, 64, [300], [1], True, 0, "bf16", 1),          # 64 heads to one key
+    (8, 3, 1, 128, 64, [700, 1, 640, 90, 513, 1100, 2, 64, 800], [1] * 9, True, 0, "bf16", 1),  # eight waves a tile
+    (4, 4, 4, 64, 16, [600, 70, 515, 540, 580], [1, 2, 1, 1, 1], True, 0, "f32", 2),
 ]
 
 

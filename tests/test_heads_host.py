@@ -197,6 +197,40 @@ def test_cache_refuses_shapes_and_types():
             ar.cache_attention(**args)
 
 
+def test_compiled_checks_agree_with_pythons():
+    """The checks in C++ pass what those in Python pass, with the same addresses
+    and strides, and leave to Python whatever they do not pass."""
+    m = binding._MARSHAL
+    if m is None:
+        pytest.skip("built with the library")
+    wide = [torch.zeros(3, 7, 64) for _ in range(2)]
+    views = [t[:, 1:3] for t in wide]
+    addresses = lambda ts: b"".join(t.data_ptr().to_bytes(8, "little") for t in ts)  # noqa: E731
+    f32, i32 = torch.float32, torch.int32
+    assert m.rows(views, f32, -1, 3, 2, 64) == (addresses(views), 7 * 64)
+    assert m.rows([t[:1] for t in views], f32, -1, 1, 2, 64) == (addresses(views), 2 * 64)
+    assert m.contiguous(wide, f32, -1, (3, 7, 64)) == addresses(wide)
+    assert m.contiguous(tuple(wide), f32, -1, wide[0].shape) == addresses(wide)
+    vec = torch.arange(5)
+    assert m.vector(vec, torch.int64, -1, 5) == vec.data_ptr()
+    table, first, at = torch.zeros(2, 9, dtype=i32)[:, :4], _ints(0, 1, 2), _ints(5, 6)
+    assert m.sequences(table, first, at, -1) == (table.data_ptr(), first.data_ptr(), at.data_ptr(), 9, 4, 2)
+    for refused in (m.rows(views, torch.bfloat16, -1, 3, 2, 64), m.rows(views, f32, 0, 3, 2, 64), m.rows(views, f32, -1, 4, 2, 64),
+                    m.rows([views[0], views[1].contiguous()], f32, -1, 3, 2, 64), m.rows([], f32, -1, 3, 2, 64),
+                    m.rows(views * 5, f32, -1, 3, 2, 64), m.rows([t.transpose(1, 2) for t in wide], f32, -1, 3, 64, 7),
+                    m.rows([None, 3], f32, -1, 3, 2, 64), m.rows(views, "f32", -1, 3, 2, 64), m.rows(iter(views), f32, -1, 3, 2, 64),
+                    m.contiguous(views, f32, -1, (3, 2, 64)), m.contiguous(wide, f32, -1, (3, 7)), m.contiguous(wide, f32, -1, 3),
+                    m.vector(vec[::2], torch.int64, -1, 3),
+                    m.vector(vec, torch.int64, -1, 4), m.vector(vec.to_sparse(), torch.int64, -1, 5), m.vector(None, f32, -1, 5),
+                    m.sequences(table.long(), first, at, -1), m.sequences(table, first[:2], at, -1), m.sequences(table, first, table, -1),
+                    m.sequences(table[:1].expand(2, 4), first, at, -1), m.sequences(table.t(), first, at, -1)):
+        assert refused is None
+    meta = [t.to("meta") for t in wide]  # no device and no address: Python passes them on too
+    assert m.contiguous(meta, f32, -1, (3, 7, 64)) == bytes(binding._layer_list(meta, 2, (3, 7, 64), f32, -1, "x"))
+    with pytest.raises((TypeError, OverflowError)):
+        m.rows(views, f32, -1, "3", 2, 64)
+
+
 # ---- the C ABI (argument errors come before any HIP call) ----
 
 P8 = ctypes.c_void_p * 8
