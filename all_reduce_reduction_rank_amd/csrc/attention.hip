@@ -455,11 +455,15 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 || DT == DT_BF16 && DIM <= 1
 #pragma unroll
       for (int i = 0; i < DT_TILES; ++i) {
         const v8bf lo = widen8(vw[i].x, vw[i].y, vs), hi = widen8(vw[i].z, vw[i].w, vs);
+        // fp32 payloads: a step's sum on its own, so that a long sequence rounds the
+        // whole sum once a step and not once an instruction
+        v4f sum = PT == 3 ? (v4f){0.f, 0.f, 0.f, 0.f} : o[i];
 #pragma unroll
         for (int x = PT - 1; x >= 0; --x) {
-          o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, w[0][x], o[i], 0, 0, 0);
-          o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, w[1][x], o[i], 0, 0, 0);
+          sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, w[0][x], sum, 0, 0, 0);
+          sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, w[1][x], sum, 0, 0, 0);
         }
+        o[i] = PT == 3 ? o[i] + sum : sum;
       }
       if (more) {
         load_v(step + WAVES);
@@ -519,8 +523,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 || DT == DT_BF16 && DIM <= 1
 // Bound by the vector units and the matrix cores in turn: the softmax, and the
 // waits of two waves per SIMD that share both.  The codes are widened once, on
 // their way into LDS; widened by every wave from codes in LDS they cost more
-// than the larger LDS reads (prompt of 8192 tokens, 40 heads of 128: 941 us, PUT
-// us now).  The e4m3 instructions with block scales would take the keys' codes
+// than the larger LDS reads (prompt of 8192 tokens, 40 heads of 128: 941 us, 830
+// now).  The e4m3 instructions with block scales would take the keys' codes
 // as they are, but their sums over 64 products keep fewer than fp32's bits
 // (scores off by 2^-18 of their terms' size, measured).  A step of 64 tokens is
 // loaded to registers one step ahead and stored to the other of two LDS buffers.
@@ -769,12 +773,18 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 ? 2 : 1) void many
           }
 #pragma unroll
           for (int i = 0; i < DT_TILES; ++i) {
+            v16f sum;  // (as above: half a step's sum on its own)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const v8bf v = __builtin_bit_cast(v8bf, v_s[buf][(va0 ^ (2 * x + u)) + 256 * i]);
+            for (int e = 0; e < 16; ++e) sum[e] = PT == 3 ? 0.f : o[i][e];
+            const v8bf v0 = __builtin_bit_cast(v8bf, v_s[buf][(va0 ^ (2 * x)) + 256 * i]);
+            const v8bf v1 = __builtin_bit_cast(v8bf, v_s[buf][(va0 ^ (2 * x + 1)) + 256 * i]);
 #pragma unroll
-              for (int y = PT - 1; y >= 0; --y) o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w[u][y], o[i], 0, 0, 0);
+            for (int y = PT - 1; y >= 0; --y) {
+              sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v0, w[0][y], sum, 0, 0, 0);
+              sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v1, w[1][y], sum, 0, 0, 0);
             }
+            if (PT == 3) o[i] += sum;
+            else o[i] = sum;
           }
         }
       }
@@ -885,13 +895,13 @@ AttnPlan plan_of(const ar_kv_cache* c, uint64_t seqs, uint64_t rows, uint64_t wi
   p.min_steps = 8;
   p.waves = 4;
   const uint64_t most_splits = umax(1, (steps + p.min_steps - 1) / p.min_steps);
+  // Workgroups that are resident together: two per CU, one where registers are short.
+  const uint64_t round = c->head_dim == 64 || (c->head_dim == 128 && dtype == DT_BF16) ? 512 : 256;
   if (p.few) {
-    // Workgroups that are resident together: two per CU, one where registers are
-    // short.  One round of them if the tiles are few, else two: shares that fill a
-    // round exactly leave CUs with one share too many (64 sequences of 8192 tokens,
-    // 8 key heads of 128: one share each 234 us, two 198; 4 sequences of 32768: 16
-    // shares 56 us, 32 69).
-    const uint64_t round = c->head_dim == 64 || (c->head_dim == 128 && dtype == DT_BF16) ? 512 : 256;
+    // One round of them if the tiles are few, else two: shares that fill a round
+    // exactly leave CUs with one share too many (64 sequences of 8192 tokens, 8 key
+    // heads of 128: one share each 234 us, two 198; 4 sequences of 32768: 16 shares
+    // 56 us, 32 69).
     const uint64_t want = real < round / 2 ? round : 2 * round;
     p.splits = (uint32_t)umin(most_splits, (want + real - 1) / real);
     // Half a GPU's worth of tiles over not many tokens: eight waves of one workgroup
@@ -900,12 +910,14 @@ AttnPlan plan_of(const ar_kv_cache* c, uint64_t seqs, uint64_t rows, uint64_t wi
     // CUs' own bandwidth is short: 15 us shared, 19 so).
     if (p.splits > 1 && c->head_dim <= 128 && real > 64 && real <= 256 && steps <= 48) p.waves = 8, p.splits = 1;
   } else {
-    // Rounds of 512 workgroups (two per CU) over the work of each.
+    // Rounds of workgroups times the steps of each, where starting costs about four
+    // steps more, and what joining costs, about six and more with the shares (42
+    // fp32 rows of 256 over 20260 tokens, 8 tiles: 8 shares 550 us, 32 145).
     p.splits = 1;
-    uint64_t best = (real + 511) / 512 * 840;
-    for (uint32_t k = 2; k <= 8 && k <= most_splits && real < 512; ++k) {
-      const uint64_t cost = (real * k + 511) / 512 * (840 / k) + 20;
-      if (cost < best) best = cost, p.splits = k;
+    uint64_t best = (real + round - 1) / round * (steps + 4);
+    for (uint64_t k = 2; k <= most_splits && k <= 64 && real < round; ++k) {
+      const uint64_t cost = (real * k + round - 1) / round * ((steps + k - 1) / k + 4) + 6 + k / 8;
+      if (cost < best) best = cost, p.splits = (uint32_t)k;
     }
   }
   const uint64_t slots = p.splits > 1 ? columns * p.tiles * p.splits : 0;
