@@ -250,7 +250,8 @@ __device__ __forceinline__ void plain_rows(const AttnArgs& a, const Tile& t, uin
 //   O^T    lane (g, c) holds dimensions 16 t + 4 g + i of row c
 //
 // What a row does not see must not reach it: its weight is 0, but 0 times a NaN
-// is not.  A workgroup that ends with a NaN does its rows again, by plain_rows.
+// is not.  A workgroup that ends with a NaN in a row whose sum of weights is none
+// (there the whole row is NaN by itself) does its rows again, by plain_rows.
 template <int DT, int DIM, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, WAVES == 8 || DT == DT_BF16 && DIM <= 128 || DIM == 64 ? 2 : 1) void few_rows_kernel(AttnArgs a) {
   constexpr int BM = 16;
@@ -473,17 +474,17 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 || DT == DT_BF16 && DIM <= 1
   }
 
   const uint64_t slot = (((uint64_t)r * a.kv_heads + h) * a.tiles + tile) * a.splits + split;
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
   float worst = 0.f;
 #pragma unroll
   for (int i = 0; i < DT_TILES * 4; ++i) worst += o[i / 4][i % 4] * 0.f;
-  if (__syncthreads_or(!(worst == 0.f))) {
+  if (__syncthreads_or(!(worst == 0.f) && l == l)) {
     plain_rows<DT, DIM, WAVES>(a, t, h, r, t.begin + step0 * TOKENS, t.begin + step1 * TOKENS, shared, slot * BM);
     return;
   }
 
-  // Join the waves (and the lane groups' sums of p).
-  l += __shfl_xor(l, 16);
-  l += __shfl_xor(l, 32);
+  // Join the waves.
   if (g == 0) m_s[wave][c] = m * a.factor, l_s[wave][c] = l;
 #pragma unroll
   for (int i = 0; i < DT_TILES; ++i) *(v4f*)&o_s[wave][c][16 * i + 4 * g] = o[i];
@@ -794,15 +795,15 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 ? 2 : 1) void many
   }
 
   const uint64_t slot = ((((uint64_t)r * a.kv_heads + h) * a.tiles + tile) * a.splits + split) * BM;
+  l += __shfl_xor(l, 32);
   float worst = 0.f;
 #pragma unroll
   for (int i = 0; i < DT_TILES * 16; ++i) worst += o[i / 16][i % 16] * 0.f;
-  if (__syncthreads_or(!(worst == 0.f))) {
+  if (__syncthreads_or(!(worst == 0.f) && l == l)) {
     plain_rows<DT, DIM, WAVES>(a, t, h, r, t.begin + step0 * TOKENS, t.begin + step1 * TOKENS, shared, slot);
     return;
   }
 
-  l += __shfl_xor(l, 32);
   if (PT == 1) lr += __shfl_xor(lr, 32);
   else lr = l;
   if (!real) return;
@@ -869,6 +870,8 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, uint32_t bm) {
   }
 }
 
+constexpr bool eight_waves_fit(int dtype, uint64_t dim) { return dim == 64 || (dim == 128 && dtype == DT_BF16); }
+
 // How a call is cut.
 struct AttnPlan {
   bool few;
@@ -896,7 +899,7 @@ AttnPlan plan_of(const ar_kv_cache* c, uint64_t seqs, uint64_t rows, uint64_t wi
   p.waves = 4;
   const uint64_t most_splits = umax(1, (steps + p.min_steps - 1) / p.min_steps);
   // Workgroups that are resident together: two per CU, one where registers are short.
-  const uint64_t round = c->head_dim == 64 || (c->head_dim == 128 && dtype == DT_BF16) ? 512 : 256;
+  const uint64_t round = eight_waves_fit(dtype, c->head_dim) ? 512 : 256;
   if (p.few) {
     // One round of them if the tiles are few, else two: shares that fill a round
     // exactly leave CUs with one share too many (64 sequences of 8192 tokens, 8 key
@@ -908,7 +911,9 @@ AttnPlan plan_of(const ar_kv_cache* c, uint64_t seqs, uint64_t rows, uint64_t wi
     // instead of a few workgroups and a second kernel to join them (16 sequences of
     // up to 2000 tokens, 8 key heads of 128: 25 us shared, 20 so; with 8 tiles the
     // CUs' own bandwidth is short: 15 us shared, 19 so).
-    if (p.splits > 1 && c->head_dim <= 128 && real > 64 && real <= 256 && steps <= 48) p.waves = 8, p.splits = 1;
+    // Not where eight waves would be short of registers.
+    const bool fits = eight_waves_fit(dtype, c->head_dim);
+    if (p.splits > 1 && fits && real > 64 && real <= 256 && steps <= 48) p.waves = 8, p.splits = 1;
   } else {
     // Rounds of workgroups times the steps of each, where starting costs about four
     // steps more, and what joining costs, about six and more with the shares (42
@@ -999,7 +1004,7 @@ ar_status ar_cache_attention(const ar_kv_cache* cache, const void* const* q, siz
   by_head_dim((int)dtype, cache->head_dim, [&](auto dt, auto dim) {
     constexpr int DT = decltype(dt)::value, DIM = decltype(dim)::value;
     if (plan.few) {
-      if constexpr (DIM <= 128) {
+      if constexpr (eight_waves_fit(DT, DIM)) {
         if (plan.waves == 8) few_rows_kernel<DT, DIM, 8><<<grid, 512, 0, (hipStream_t)stream>>>(a);
         else few_rows_kernel<DT, DIM, 4><<<grid, 256, 0, (hipStream_t)stream>>>(a);
       } else {

@@ -357,6 +357,23 @@ def test_attention_nan_reaches_only_who_sees_it(most, count, dt, dim):
 
 
 @pytest.mark.parametrize("most", [1, 100])
+def test_attention_nan_queries(most):
+    """A row of NaN, and one that holds an infinity: NaN themselves, and no other row."""
+    length, count = [90, 700], [4, 40]
+    ref, cache, table, first, q = att_case(1, 2, 1, 128, 16, length, count, "bf16")
+    q = [q[0].clone()]
+    a, b = int(first[0]), int(first[-1])
+    clean = [q[0].clone()]
+    q[0][a + 1] = float("nan")
+    q[0][b - 3, 1, 7] = float("inf")
+    got = ar.cache_attention(q, cache, ints(table), ints(first), ints(length), max_rows=most)
+    want = ar.cache_attention(clean, cache, ints(table), ints(first), ints(length), max_rows=most)
+    assert got[0][a + 1].isnan().all() and got[0][b - 3, 1].isnan().all()
+    got[0][a + 1], got[0][b - 3, 1] = want[0][a + 1], want[0][b - 3, 1]
+    assert torch.equal(got[0][a:b], want[0][a:b])
+
+
+@pytest.mark.parametrize("most", [1, 100])
 @pytest.mark.parametrize("scale", [-0.2, 0.0, 1.0])
 def test_attention_scales(most, scale):
     length, count = [90, 41], [4, 33]
