@@ -538,7 +538,14 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 || DT == DT_BF16 && DIM <= 1
 //   keys   k of half h: 8 contiguous values of every 16, from 8 h on
 //   values operand row: dimension 32 t + c, k of half h: tokens 32 h .. + 31
 // LDS rows (a token's key, a dimension's 64 values) hold their 16-byte chunks
-// permuted by the row's number, so that the lanes of a read spread over the banks.
+// permuted, so that the 16 rows that 16 neighbouring lanes read lie on 16 chunks
+// of the 256 bytes of banks: values two rows to 256 bytes, hence by the row's
+// number over 2; keys, whose rows a wave reads in the order above, by the bits
+// that differ there.
+__device__ __forceinline__ uint32_t key_turn(uint32_t key, uint32_t row_chunks) {
+  return ((key & 3) | (key >> 3 & 4) | (key << 1 & 8)) & (row_chunks - 1);
+}
+
 template <int DT, int DIM>
 __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 ? 2 : 1) void many_rows_kernel(AttnArgs a) {
   constexpr int WAVES = 4, THREADS = 64 * WAVES, BM = 32 * WAVES;
@@ -674,21 +681,21 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 ? 2 : 1) void many
       const uint32_t ch = tid + i * THREADS, kr = ch / KCHUNKS, vr = ch / 4;
       const float ks = byte_scale(kbyte[i]), vs = byte_scale(vbyte);
       uint4* kt = k_s[buf] + kr * KROW;
-      kt[(ch % KCHUNKS * 2) ^ (kr & 7)] = __builtin_bit_cast(uint4, widen8(kx[i].x, kx[i].y, ks));
-      kt[(ch % KCHUNKS * 2 + 1) ^ (kr & 7)] = __builtin_bit_cast(uint4, widen8(kx[i].z, kx[i].w, ks));
+      kt[(ch % KCHUNKS * 2) ^ key_turn(kr, KROW)] = __builtin_bit_cast(uint4, widen8(kx[i].x, kx[i].y, ks));
+      kt[(ch % KCHUNKS * 2 + 1) ^ key_turn(kr, KROW)] = __builtin_bit_cast(uint4, widen8(kx[i].z, kx[i].w, ks));
       uint4 w = vx[i];
       if (base < t.lo || base > t.hi - (int32_t)TOKENS) w = clear_outside(w, base + 16 * (int32_t)(tid & 3), t.lo, t.hi);
       uint4* vt = v_s[buf] + vr * 8;
-      vt[(2 * (tid & 3)) ^ (vr & 7)] = __builtin_bit_cast(uint4, widen8(w.x, w.y, vs));
-      vt[(2 * (tid & 3) + 1) ^ (vr & 7)] = __builtin_bit_cast(uint4, widen8(w.z, w.w, vs));
+      vt[(2 * (tid & 3)) ^ ((vr >> 1) & 7)] = __builtin_bit_cast(uint4, widen8(w.x, w.y, vs));
+      vt[(2 * (tid & 3) + 1) ^ ((vr >> 1) & 7)] = __builtin_bit_cast(uint4, widen8(w.z, w.w, vs));
     }
     if (tid < 4) there_s[buf][tid] = there;
   };
 
   const uint32_t kt = 32 * ((c >> 2) & 1) + 4 * (c >> 3) + (c & 3);  // this lane's key of x = 0
   // where its chunks lie in LDS: the chunk's number is exclusive-ored in
-  const uint32_t ka0 = kt * KROW + (hf ^ (kt & 7));
-  const uint32_t va0 = c * 8 + ((4 * hf) ^ (c & 7));
+  const uint32_t ka0 = kt * KROW + (hf ^ key_turn(kt, KROW));
+  const uint32_t va0 = c * 8 + ((4 * hf) ^ ((c >> 1) & 7));
   {
 #pragma unroll
     for (int i = 0; i < DT_TILES; ++i)
@@ -715,20 +722,26 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 ? 2 : 1) void many
         const bool gap = !there_s[buf][2 * hf] || !there_s[buf][2 * hf + 1];
         const bool mask = base < all0 || base > all1 - (int32_t)TOKENS || __any(gap);
         float p[2][16];
+        v16f s[2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          v16f s;
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) s[e] = 0.f;
+          for (int e = 0; e < 16; ++e) s[x][e] = 0.f;
 #pragma unroll
-          for (int j = 0; j < KSTEPS; ++j) {
+        for (int j = 0; j < KSTEPS; ++j)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
             const v8bf k8 = __builtin_bit_cast(v8bf, k_s[buf][(ka0 ^ (2 * j)) + x * 16 * KROW]);
 #pragma unroll
-            for (int y = QT - 1; y >= 0; --y) s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k8, q[j][y], s, 0, 0, 0);
+            for (int y = QT - 1; y >= 0; --y) s[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k8, q[j][y], s[x], 0, 0, 0);
           }
 #pragma unroll
-          for (int e = 0; e < 16; ++e) p[x][e] = s[e];
-          if (mask) {
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) p[x][e] = s[x][e];
+        if (mask) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
             // tokens first + e with from <= e < to
             const int32_t first = base + 32 * (int32_t)hf + 16 * x, from = see0 - first;
             const int32_t to = there_s[buf][2 * hf + x] ? see1 - first : -1;

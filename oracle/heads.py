@@ -187,9 +187,9 @@ def attention(q, cache, table, first, length, scale, causal, window, dt, terms):
                     continue
                 z = kk @ x * scale
                 size = np.abs(kk) @ np.abs(x) * abs(scale)
-                # a product of dim terms in any order; queries in terms are off by
-                # at most 2^-22 of their largest value (e4m3) or 2^-24 (bf16)
-                ez = size * (dim + 6) * E + np.abs(kk).sum(1) * np.abs(x).max() * abs(scale) * 2.0 ** -22
+                # a product of dim terms, each in up to three parts, in any order; what
+                # three bf16 terms leave of a query is at most 2^-24 of it
+                ez = size * (3 * dim + 6) * E
                 m = z.max()
                 w = np.exp(z - m)
                 w /= w.sum()
