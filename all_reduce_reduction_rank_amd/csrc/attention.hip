@@ -897,10 +897,15 @@ AttnPlan plan_of(const ar_kv_cache* c, uint64_t seqs, uint64_t rows, uint64_t wi
                  uint64_t max_rows, int dtype) {
   AttnPlan p;
   const uint64_t group = heads / c->kv_heads, columns = c->kv_heads * c->nranks;
-  // Rows of a sequence: the caller's word, or the mean.  Either kernel is right
-  // for any number.
-  const uint64_t most = max_rows ? umin(max_rows, rows) : (rows + seqs - 1) / seqs;
-  p.few = most * group <= 32;
+  // Packed rows of a sequence: by the caller's word, or the mean.  Either kernel is
+  // right for any number.  Tiles of 16 rows read the codes again for each 16, from
+  // L2 beyond the first, and multiply twice; tiles of 128 are mostly empty with few
+  // rows and start slowly.  (90 fp32 rows: 17 us against 46; 80 bf16 rows over 9000
+  // tokens: 37 against 50; 32 sequences of 100 rows over 4000 tokens: 266 against
+  // 184; 2 sequences of 100 rows over 200 tokens: 9 against 17.)
+  const uint64_t packed = (max_rows ? umin(max_rows, rows) : (rows + seqs - 1) / seqs) * group;
+  const bool small = (rows * group / 16 + seqs) * columns <= 512 && width * c->page <= 1024;
+  p.few = packed <= 96 || small;
   p.bm = p.few ? 16 : 128;
   p.tiles = (uint32_t)item_count(rows, seqs, group, p.bm, 1);
   // Tiles that may be real: a sequence's last one is counted twice above.

@@ -236,9 +236,13 @@ def test_rows_out_of_order_stay_inside(first):
     out = torch.full((24, 1, 64), 9.0, device="cuda")
     out2 = torch.full((24, 1, 64), 9.0, device="cuda")
     ar.cache_read(cache, table, ints(first), at, [out[8:16]], [out2[8:16]])
-    for most in (1, 8, 0):
-        ar.cache_attention(k, cache, table, ints(first), at, out=[out[8:16]], max_rows=most)
+    ar.cache_attention(k, cache, table, ints(first), at, out=[out[8:16]], max_rows=1)
+    # the kernel of many rows: 16 heads to a key, a table with room for more tokens
+    table = torch.cat([table, torch.full((2, 70), 5, dtype=torch.int32, device="cuda")], 1)
+    q, wide = torch.ones(8, 16, 64, device="cuda"), torch.full((24, 16, 64), 9.0, device="cuda")
+    ar.cache_attention([q], cache, table, ints(first), at, out=[wide[8:16]], max_rows=8)
     torch.cuda.synchronize()
+    assert (wide[:8] == 9).all() and (wide[16:] == 9).all()
     for t in (out, out2):
         assert (t[:8] == 9).all() and (t[16:] == 9).all()
 
@@ -265,11 +269,23 @@ ATT = [  # ranks, heads, kv_heads, dim, page, cached tokens, query rows, causal,
     (1, 2, 2, 128, 64, [2000], [1], False, 0, "f32", 1),
     (1, 64, 1, 128, 64, [300], [1], True, 0, "bf16", 1),          # 64 heads to one key
     (8, 3, 1, 128, 64, [700, 1, 640, 90, 513, 1100, 2, 64, 800], [1] * 9, True, 0, "bf16", 1),  # eight waves a tile
+    (2, 5, 1, 128, 64, [150, 64, 33], [150, 64, 20], True, 0, "bf16", 150),   # from here on: many rows
+    (1, 4, 4, 64, 16, [200, 17], [130, 17], True, 50, "bf16", 130),
+    (1, 2, 1, 256, 64, [140, 80], [70, 80], True, 0, "bf16", 80),
+    (1, 3, 1, 128, 32, [300, 40], [50, 1], False, 0, "bf16", 50),
+    (3, 2, 1, 64, 128, [1, 500], [1, 99], True, 120, "bf16", 99),
+    (1, 6, 6, 64, 32, [130, 70], [129, 33], True, 0, "f32", 129),
+    (1, 8, 2, 128, 16, [50, 199], [50, 3], True, 0, "f32", 50),
+    (1, 3, 1, 256, 128, [60], [40], False, 0, "f32", 40),
+    (2, 3, 1, 128, 64, [1500], [40], True, 0, "bf16", 40),
+    (1, 7, 1, 64, 64, [700, 5], [20, 5], True, 0, "f32", 20),
     (4, 4, 4, 64, 16, [600, 70, 515, 540, 580], [1, 2, 1, 1, 1], True, 0, "f32", 2),
 ]
 
 
-def att_case(n, h, kv, dim, page, length, count, dt, seed=0):
+def att_case(n, h, kv, dim, page, length, count, dt, seed=0, wide=False):
+    """wide: a table with room for more tokens than the kernel of few rows takes
+    whatever the rows (97 packed rows and more then go to the kernel of many)."""
     rng = np.random.default_rng(seed)
     seqs, width = len(length), max(1, -(-max(length) // page)) + 1
     pages = seqs * width + 1
@@ -284,6 +300,8 @@ def att_case(n, h, kv, dim, page, length, count, dt, seed=0):
                 for t in range(length[s]):
                     x = c.codes[i][table[s, t // page], :, t % page]
                     x[(x & 0x7f) == 0x7f] = 0x30
+    if wide:
+        table = np.concatenate([table, np.full((seqs, 1100 // page), -1)], 1)
     first = np.concatenate([[0], np.cumsum(count)]) + 1
     rows = int(first[-1]) + 2
     q = [dev(rng.normal(size=(rows, h + 1, dim)) * 0.4, dt)[:, 1:] for _ in range(n)]
@@ -292,14 +310,15 @@ def att_case(n, h, kv, dim, page, length, count, dt, seed=0):
 
 @pytest.mark.parametrize("n,h,kv,dim,page,length,count,causal,window,dt,most", ATT)
 def test_attention(n, h, kv, dim, page, length, count, causal, window, dt, most):
-    ref, cache, table, first, q = att_case(n, h, kv, dim, page, length, count, dt)
+    wide = max(count) * h // kv > 96
+    ref, cache, table, first, q = att_case(n, h, kv, dim, page, length, count, dt, wide=wide)
     out = [torch.full(q[0].shape, 5.0, dtype=T[dt], device="cuda") for _ in range(n)]
     lse = [torch.full(q[0].shape[:2], 5.0, device="cuda") for _ in range(n)]
     scale = dim ** -0.5
     got = ar.cache_attention(q, cache, ints(table), ints(first), ints(length), causal=causal, window=window, max_rows=most, out=out, lse=lse)
     plain = ar.cache_attention(q, cache, ints(table), ints(first), ints(length), causal=causal, window=window, max_rows=most)
     a, b = int(first[0]), int(first[-1])
-    few = (most or -(-q[0].shape[0] // len(length))) * (h // kv) <= 32
+    few = (most or -(-q[0].shape[0] // len(length))) * (h // kv) <= 96
     for r in range(n):
         (o, eo), (z, ez) = heads.attention(host(q[r]), ref[r], table, first, length, scale, causal, window, dt,
                                            3 if dt == "f32" else 2 if few else 1)
@@ -309,14 +328,14 @@ def test_attention(n, h, kv, dim, page, length, count, causal, window, dt, most)
         assert torch.equal(got[r][a:b], plain[r][a:b])  # twice the same bits, lse or not
 
 
-@pytest.mark.parametrize("most", [1, 40])
+@pytest.mark.parametrize("most,count", [(1, [2, 6, 2, 3]), (60, [50, 60, 40, 45])])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_attention_rows_that_see_nothing(most, dt):
+def test_attention_rows_that_see_nothing(most, count, dt):
     # no cached token, fewer cached tokens than rows, a page that is missing, a window on missing pages
-    length, count, page = [0, 3, 40, 60], [2, 6, 2, 3], 16
-    ref, cache, table, first, q = att_case(1, 4, 2, 64, page, length, count, dt)
+    length, page = [0, 3, 40, 60], 16
+    ref, cache, table, first, q = att_case(1, 4, 2, 64, page, length, count, dt, wide=most > 1)
     table[2, 0] = -1
-    table[3, 2:] = 1 << 20
+    table[3, 2:4] = 1 << 20
     for window in (0, 8):
         lse = [torch.empty(q[0].shape[:2], device="cuda")]
         got = ar.cache_attention(q, cache, ints(table), ints(first), ints(length), window=window, max_rows=most, lse=lse)
@@ -345,7 +364,7 @@ def test_attention_nan_reaches_only_who_sees_it(most, count, dt, dim):
     clean = [x.copy() for x in c.codes]
     for x in c.codes:
         x[(x & 0x7f) == 0x7f] = 0  # the oracle's copy: without NaN, which is put where it is seen
-    few = (most or count) * 2 <= 32
+    few = (most or count) * 2 <= 96
     (o, eo), (z, ez) = heads.attention(host(q[0]), c, table, first, length, dim ** -0.5, True, 0, dt, 3 if dt == "f32" else 2 if few else 1)
     c.codes = clean
     a, m, b = (int(x) for x in first)
@@ -359,8 +378,8 @@ def test_attention_nan_reaches_only_who_sees_it(most, count, dt, dim):
 @pytest.mark.parametrize("most", [1, 100])
 def test_attention_nan_queries(most):
     """A row of NaN, and one that holds an infinity: NaN themselves, and no other row."""
-    length, count = [90, 700], [4, 40]
-    ref, cache, table, first, q = att_case(1, 2, 1, 128, 16, length, count, "bf16")
+    length, count = [90, 700], [4, 60]
+    ref, cache, table, first, q = att_case(1, 2, 1, 128, 16, length, count, "bf16", wide=most > 1)
     q = [q[0].clone()]
     a, b = int(first[0]), int(first[-1])
     clean = [q[0].clone()]
@@ -377,7 +396,7 @@ def test_attention_nan_queries(most):
 @pytest.mark.parametrize("scale", [-0.2, 0.0, 1.0])
 def test_attention_scales(most, scale):
     length, count = [90, 41], [4, 33]
-    ref, cache, table, first, q = att_case(1, 3, 1, 128, 16, length, count, "bf16")
+    ref, cache, table, first, q = att_case(1, 3, 1, 128, 16, length, count, "bf16", wide=most > 1)
     lse = [torch.empty(q[0].shape[:2], device="cuda")]
     got = ar.cache_attention(q, cache, ints(table), ints(first), ints(length), scale=scale, max_rows=most, lse=lse)
     (o, eo), (z, ez) = heads.attention(host(q[0]), ref[0], table, first, length, scale, True, 0, "bf16", 1)
@@ -389,7 +408,7 @@ def test_attention_scales(most, scale):
 def test_attention_queries_of_all_sizes():
     """Rows of bf16 queries whose elements span many binades, beside tiny and huge rows."""
     length, count = [130], [60]
-    ref, cache, table, first, q = att_case(1, 2, 1, 128, 64, length, count, "bf16")
+    ref, cache, table, first, q = att_case(1, 2, 1, 128, 64, length, count, "bf16", wide=True)
     rng = np.random.default_rng(3)
     spread = 2.0 ** rng.integers(-30, 1, q[0].shape)
     rows = 2.0 ** rng.integers(-40, 3, (q[0].shape[0], 1, 1))

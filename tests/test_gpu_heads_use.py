@@ -159,7 +159,7 @@ def test_two_streams_at_once():
             assert all(torch.equal(a[f[0]:f[-1]], b[f[0]:f[-1]]) for a, b in zip(o, want[i]))
 
 
-@pytest.mark.parametrize("most", [1, 64])
+@pytest.mark.parametrize("most", [1, 128])
 def test_cache_past_4_gib(most):
     kv, dim, page = 8, 256, 128
     pages = (5 << 30) // (kv * page * dim)
@@ -179,6 +179,8 @@ def test_cache_past_4_gib(most):
         assert ((a[0].double() - b[0].double()).abs() <= bound).all()
     n = most
     q = [torch.randn(2 * n, kv, dim, generator=gen, device="cuda").bfloat16()]
+    if n > 1:  # room for more tokens: the kernel of many rows
+        table = torch.cat([table, torch.full((2, 8), -1, dtype=torch.int32, device="cuda")], 1)
     out = ar.cache_attention(q, cache, table, ints([0, n, 2 * n]), length, causal=False, max_rows=n)
     z = torch.einsum("snhd,sjhd->shnj", q[0].view(2, n, kv, dim).double().cpu(), kb[0].view(2, 200, kv, dim).double().cpu()) / 16
     want = torch.einsum("shnj,sjhd->snhd", torch.softmax(z, -1), vb[0].view(2, 200, kv, dim).double().cpu()).reshape(2 * n, kv, dim)
@@ -204,8 +206,9 @@ def test_many_sequences():
     ref[0].write([host(k), host(v)], table, first, past)
     ar.cache_write(cache, [k], [v], ints(table), ints(first), ints(past))
     same_cache(ref, cache)
-    for most in (3, 40):
-        out = ar.cache_attention([q], cache, ints(table), ints(first), ints(past + count), max_rows=most)
+    wide = np.concatenate([table, np.full((seqs, 80), -1)], 1)
+    for most, pages in ((3, table), (100, wide)):
+        out = ar.cache_attention([q], cache, ints(pages), ints(first), ints(past + count), max_rows=most)
         (o, eo), _ = heads.attention(host(q), ref[0], table, first, past + count, 0.125, True, 0, "bf16", 1)
         check(host(out[0]), o, eo, "out")
 
