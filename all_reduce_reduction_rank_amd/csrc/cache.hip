@@ -150,15 +150,10 @@ __global__ __launch_bounds__(THREADS) void write_kernel(CacheArgs a) {
   __shared__ float maxima[THREADS / 64 + 1];
   const uint32_t kind = blockIdx.y & 1, r = blockIdx.z, head = blockIdx.y >> 1;
   Piece pc;
-  if (!piece_of(a.p, blockIdx.x, &pc) || pc.id >= a.p.pages) return;
+  if (!piece_of(a.p, blockIdx.x, &pc)) return;
   const uint32_t page = 1u << a.p.page_shift, count = pc.hi - pc.lo;
   const uint32_t lane = threadIdx.x % LANES, row = threadIdx.x / LANES;
   const char* x = a.x[kind][r] + (uint64_t)pc.row * a.pitch[kind] + (uint64_t)head * (DIM * ES) + lane * 8 * ES;
-  uint8_t* codes = a.codes[kind][r] + page_at(pc.id, a.kv_heads, head, page * DIM);
-  uint8_t* scale = a.scale[kind][r] + (uint64_t)pc.id * a.kv_heads + head;
-  // one thread reads the byte and writes it, in that order
-  uint32_t held = threadIdx.x == 0 ? *scale : 0;
-
   Eight<DT> v[BATCH];
   auto load = [&](uint32_t i0) {
 #pragma unroll
@@ -167,7 +162,12 @@ __global__ __launch_bounds__(THREADS) void write_kernel(CacheArgs a) {
       if (i < count) v[j] = load8<DT>(x + (uint64_t)i * a.pitch[kind]);
     }
   };
-  load(0);
+  load(0);  // (does not wait for the page's number)
+  if (pc.id >= a.p.pages) return;
+  uint8_t* codes = a.codes[kind][r] + page_at(pc.id, a.kv_heads, head, page * DIM);
+  uint8_t* scale = a.scale[kind][r] + (uint64_t)pc.id * a.kv_heads + head;
+  // one thread reads the byte and writes it, in that order
+  uint32_t held = threadIdx.x == 0 ? *scale : 0;
   // Values: words q0 .. of every dimension change.  A thread's first ones are asked
   // for here where some of their bytes stay.
   const uint32_t q1 = (pc.hi + 3) / 4, q0 = pc.lo / 4;
