@@ -230,12 +230,14 @@ __device__ __forceinline__ void plain_rows(const AttnArgs& a, const Tile& t, uin
   }
 }
 
-// ---- few rows: 16 rows per workgroup, its four waves share the tokens ----
+// ---- few rows: 16 rows per workgroup, its four or eight waves share the tokens ----
 //
-// Each wave takes every fourth step of 64 tokens straight from memory to
-// registers, with a softmax of its own, joined at the end; a long cache is
+// The waves take the steps of 64 tokens in turn, straight from memory to
+// registers, each with a softmax of its own, joined at the end; a long cache is
 // shared among workgroups and joined by a second kernel.  Bound by memory: a
-// step is 64 x 2 x dim bytes of codes, loaded 16 bytes per lane one step ahead.
+// step is 64 x 2 x dim bytes of codes, loaded 16 bytes per lane one step ahead
+// (64 sequences of 8192 tokens, 8 key heads of 128: 198 us, 5.4 TB/s; with
+// entries and scales waited for as they were loaded 271).
 //
 // Matrix instructions 16x16x32, keys as the first operand: S^T[token][row].
 // The order of k is free as long as both operands share it, and so is the
@@ -250,8 +252,9 @@ __device__ __forceinline__ void plain_rows(const AttnArgs& a, const Tile& t, uin
 //   O^T    lane (g, c) holds dimensions 16 t + 4 g + i of row c
 //
 // What a row does not see must not reach it: its weight is 0, but 0 times a NaN
-// is not.  A workgroup that ends with a NaN in a row whose sum of weights is none
-// (there the whole row is NaN by itself) does its rows again, by plain_rows.
+// is not.  A workgroup that ends with a NaN in a row whose sum of weights is a
+// number (where it is not, the whole row is NaN by itself) does its rows again, by
+// plain_rows.
 template <int DT, int DIM, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, WAVES == 8 || DT == DT_BF16 && DIM <= 128 || DIM == 64 ? 2 : 1) void few_rows_kernel(AttnArgs a) {
   constexpr int BM = 16;
@@ -524,8 +527,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 || DT == DT_BF16 && DIM <= 1
 // Bound by the vector units and the matrix cores in turn: the softmax, and the
 // waits of two waves per SIMD that share both.  The codes are widened once, on
 // their way into LDS; widened by every wave from codes in LDS they cost more
-// than the larger LDS reads (prompt of 8192 tokens, 40 heads of 128: 941 us, 830
-// now).  The e4m3 instructions with block scales would take the keys' codes
+// than the larger LDS reads (prompt of 8192 tokens, 40 heads of 128: 941 us, 815
+// now, 0.84 PFLOP/s).  The e4m3 instructions with block scales would take the keys' codes
 // as they are, but their sums over 64 products keep fewer than fp32's bits
 // (scores off by 2^-18 of their terms' size, measured).  A step of 64 tokens is
 // loaded to registers one step ahead and stored to the other of two LDS buffers.
