@@ -142,6 +142,43 @@ __device__ __forceinline__ uint4 flipped(const uint4& w, uint32_t f) { return ma
 __device__ __forceinline__ uint32_t clamp_byte(uint32_t b) { return b < SCALE_MIN ? SCALE_MIN : b > SCALE_MAX ? SCALE_MAX : b; }
 __device__ __forceinline__ float byte_scale(uint32_t b) { return scale_of(clamp_byte(b)); }
 
+// ---- what a row does not see ----
+//
+// Its weight is 0, but 0 times a NaN or an infinity is NaN. Codes of tokens that no
+// row of a tile sees are cleared in the steps where a mask runs through the tile.
+// Codes that stand for no number are cleared there too where some rows see the token
+// and others do not; the rows that do get their NaN at the end, from another look at
+// those steps. (In all other steps every row sees every token.) With a NaN that rows
+// see in the first and the last 64 tokens: a prompt of 1500 tokens takes the time it
+// takes without; with rows done again in plain loops it took 135 times as long.
+
+// The tokens [all0, all1) that every row of a tile sees.
+struct Mask {
+  int32_t all0, all1;
+  __device__ __forceinline__ Mask(const Tile& t, const AttnArgs& a) {
+    all0 = 0, all1 = t.length;
+    if (a.causal) {
+      const int32_t end = t.length - (int32_t)t.n + 1;
+      const int32_t e = end + (int32_t)(t.r0 / a.group), f = end + (int32_t)((t.r0 + t.rows - 1) / a.group);
+      all1 = e < 0 ? 0 : e;
+      if (a.window && f > a.window) all0 = f - a.window;
+    }
+  }
+  __device__ __forceinline__ bool step(int32_t base) const { return base < all0 || base > all1 - (int32_t)TOKENS; }
+  __device__ __forceinline__ bool token(int32_t at) const { return at < all0 || at >= all1; }
+};
+
+// The smallest magnitude of a code that stands for no finite number: NaN, or with
+// scales of 2^120 and more 2^128 and above.
+__device__ __forceinline__ uint32_t not_finite_from(uint32_t byte) {
+  return byte < 247 ? 0x7fu : 0x78u - 8 * (byte - 247);
+}
+
+// The high bit of every byte whose code is one of those.
+__device__ __forceinline__ uint32_t not_finite(uint32_t codes, uint32_t from) {
+  return ((codes & 0x7f7f7f7fu) + (0x80u - from) * 0x01010101u) & 0x80808080u;
+}
+
 // Bytes of a 16-token block of codes that lie outside tokens [lo, hi) become 0;
 // `at` is the block's first token.
 __device__ __forceinline__ uint4 clear_outside(uint4 w, int32_t at, int32_t lo, int32_t hi) {
@@ -154,81 +191,38 @@ __device__ __forceinline__ uint4 clear_outside(uint4 w, int32_t at, int32_t lo, 
   return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
-// A tile's rows over tokens [t0, t1), a row per wave, in plain loops: what a row
-// does not see is not touched.  For tiles that hold a NaN.
-template <int DT, int DIM, int WAVES>
-__device__ __forceinline__ void plain_rows(const AttnArgs& a, const Tile& t, uint32_t h, uint32_t r, uint32_t t0,
-                                           uint32_t t1, bool shared, uint64_t slot) {
-  constexpr int PER = DIM / 64;  // dimensions of a lane
-  const uint32_t lane = threadIdx.x & 63, in_page = (1u << a.p.page_shift) - 1, page_bytes = DIM << a.p.page_shift;
-#pragma nounroll
-  for (uint32_t row = threadIdx.x >> 6; row < t.rows; row += WAVES) {
-    const uint32_t packed = t.r0 + row, qr = packed / a.group, head = h * a.group + packed % a.group;
-    int32_t see0 = 0, see1 = t.length;
-    if (a.causal) {
-      const int32_t e = t.length - (int32_t)t.n + (int32_t)qr + 1;
-      see1 = e < 0 ? 0 : e;
-      if (a.window && e > a.window) see0 = e - a.window;
-    }
-    const char* q = a.q[r] + (uint64_t)(t.row0 + qr) * a.q_pitch + (uint64_t)head * DIM * Elem<DT>::size;
-    float m = -INFINITY, l = 0.f, o[PER] = {};
-#pragma nounroll
-    for (uint32_t base = t0; base < t1; base += 64) {
-      const uint32_t tok = base + lane, id = page_id(a.p, t.s, tok >> a.p.page_shift);
-      const bool seen = (int32_t)tok >= see0 && (int32_t)tok < see1 && id < a.p.pages;
-      float z = -INFINITY, vs = 0.f;
-      if (seen) {
-        const uint8_t* k = a.k[r] + page_at(id, a.kv_heads, h, page_bytes) + (tok & in_page) * DIM;
-        const float ks = byte_scale(a.k_scale[r][(uint64_t)id * a.kv_heads + h]);
-        vs = byte_scale(a.v_scale[r][(uint64_t)id * a.kv_heads + h]);
-        z = 0.f;
-#pragma nounroll
-        for (int d = 0; d < DIM; d += 4) {
-          float x[4];
-          values_of(*(const uint32_t*)(k + d), ks, x);
+// Clears those of a block that some rows do not see; *taken becomes 1 if there are any.
+__device__ __forceinline__ uint4 clear_unseen(uint4 w, uint32_t from, int32_t at, const Mask& m, uint32_t* taken) {
+  uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) z += Elem<DT>::ldf(q + (d + e) * Elem<DT>::size) * x[e];
-        }
-        if (a.flip) z = -z;
-      }
-      float top = z;
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t bad = not_finite(x[i], from);
 #pragma unroll
-      for (int s = 32; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
-      const float next = fmaxf(m, top), shift = next == -INFINITY ? 0.f : next * a.factor;
-      const float f = next == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - next) * a.factor);
-      m = next;
-      const float p = seen ? __builtin_amdgcn_exp2f(__builtin_fmaf(z, a.factor, -shift)) : 0.f;
-      l = l * f + p;
-#pragma unroll
-      for (int x = 0; x < PER; ++x) o[x] *= f;
-      const uint64_t who = __ballot(seen);
-#pragma nounroll
-      for (int j = 0; j < 64; ++j) {
-        if (!(who >> j & 1)) continue;
-        const float pj = __shfl(p, j), sj = __shfl(vs, j);
-        const uint8_t* v = a.v[r] + page_at(__shfl((int)id, j), a.kv_heads, h, page_bytes) + ((base + j) & in_page);
-#pragma unroll
-        for (int x = 0; x < PER; ++x) {
-          float y[4];
-          values_of(v[(lane + 64 * x) << a.p.page_shift], sj, y);
-          o[x] += pj * y[0];
-        }
-      }
-    }
-#pragma unroll
-    for (int s = 32; s > 0; s >>= 1) l += __shfl_xor(l, s);
-    const float inv = shared ? 1.f : l == 0.f ? 0.f : 1.f / l;
-    const uint64_t at = ((uint64_t)(t.row0 + qr) * a.heads + head);
-#pragma unroll
-    for (int x = 0; x < PER; ++x) {
-      if (shared) a.part[(slot + row) * DIM + lane + 64 * x] = o[x];
-      else Elem<DT>::stf(a.out[r] + (at * DIM + lane + 64 * x) * Elem<DT>::size, o[x] * inv);
-    }
-    if (lane) continue;
-    if (shared) a.stat[slot + row] = make_float2(m * a.factor, l);
-    else if (a.lse[r]) a.lse[r][at] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m * a.factor) + log2f(l)) * LN2;
+    for (int e = 0; e < 4; ++e)
+      if ((bad >> (8 * e + 7) & 1) && m.token(at + 4 * i + e)) x[i] &= ~(0xffu << (8 * e)), *taken = 1;
   }
+  return make_uint4(x[0], x[1], x[2], x[3]);
 }
+
+// A bit for each token of a block that some rows do not see and that holds no number.
+__device__ __forceinline__ uint16_t hidden_bits(uint4 w, uint32_t from, int32_t at, const Mask& m) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if ((not_finite(x[i / 4], from) >> (8 * (i % 4) + 7) & 1) && m.token(at + i)) bits |= 1u << i;
+  return (uint16_t)bits;
+}
+
+// Bits of the tokens [from, to) of a step.
+__device__ __forceinline__ uint64_t token_bits(int32_t from, int32_t to) {
+  const uint64_t below = to >= 64 ? ~0ull : to > 0 ? (1ull << to) - 1 : 0;
+  return from >= 64 ? 0 : from > 0 ? below & (~0ull << from) : below;
+}
+
+// A dimension's tokens of a step, 16 bits of each block, written by four lanes and read as one.
+typedef uint16_t __attribute__((may_alias)) bits16;
+typedef uint64_t __attribute__((may_alias)) bits64;
 
 // ---- few rows: 16 rows per workgroup, its four or eight waves share the tokens ----
 //
@@ -251,10 +245,6 @@ __device__ __forceinline__ void plain_rows(const AttnArgs& a, const Tile& t, uin
 //          16 g + 15, which are one 16-byte load (a page is whole blocks of 16)
 //   O^T    lane (g, c) holds dimensions 16 t + 4 g + i of row c
 //
-// What a row does not see must not reach it: its weight is 0, but 0 times a NaN
-// is not.  A workgroup that ends with a NaN in a row whose sum of weights is a
-// number (where it is not, the whole row is NaN by itself) does its rows again, by
-// plain_rows.
 template <int DT, int DIM, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, WAVES == 8 || DT == DT_BF16 && DIM <= 128 || DIM == 64 ? 2 : 1) void few_rows_kernel(AttnArgs a) {
   constexpr int BM = 16;
@@ -318,14 +308,9 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 || DT == DT_BF16 && DIM <= 1
       __syncthreads();
     }
   }
-  // Tokens that every row sees: no mask within [all0, all1).
-  int32_t all0 = 0, all1 = t.length;
-  if (a.causal) {
-    const int32_t end = t.length - (int32_t)t.n + 1;
-    const int32_t e = end + (int32_t)(t.r0 / a.group), f = end + (int32_t)((t.r0 + t.rows - 1) / a.group);
-    all1 = e < 0 ? 0 : e;
-    if (a.window && f > a.window) all0 = f - a.window;
-  }
+  const Mask seen(t, a);
+  const bool differ = seen.all0 > t.lo || seen.all1 < t.hi;  // some rows do not see tokens that others see
+  uint32_t taken = 0;
 
   v4f o[DT_TILES];
   float m, l;
@@ -412,7 +397,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 || DT == DT_BF16 && DIM <= 1
         }
       }
       if (more) load_k(step + WAVES);
-      const bool mask = base < all0 || base > all1 - (int32_t)TOKENS || __any(!there);
+      const bool mask = seen.step(base) || __any(!there);
       const int32_t first = base + 16 * (int32_t)g;
       float p[16];
 #pragma unroll
@@ -455,6 +440,18 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 || DT == DT_BF16 && DIM <= 1
 #pragma unroll
         for (int i = 0; i < DT_TILES; ++i) vw[i] = clear_outside(vw[i], first, t.lo, t.hi);
       }
+      // (looked for first: taking them out costs 4 us of a decode step)
+      if (differ && seen.step(base)) {
+        const uint32_t from = not_finite_from(clamp_byte(vbyte));
+        uint32_t bad = 0;
+#pragma unroll
+        for (int i = 0; i < DT_TILES; ++i)
+          bad |= not_finite(vw[i].x, from) | not_finite(vw[i].y, from) | not_finite(vw[i].z, from) | not_finite(vw[i].w, from);
+        if (__any(bad != 0)) {
+#pragma unroll
+          for (int i = 0; i < DT_TILES; ++i) vw[i] = clear_unseen(vw[i], from, first, seen, &taken);
+        }
+      }
       const float vs = byte_scale(vbyte);
 #pragma unroll
       for (int i = 0; i < DT_TILES; ++i) {
@@ -476,16 +473,33 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 || DT == DT_BF16 && DIM <= 1
     }
   }
 
+  if (__any(taken)) {
+    static_assert(DIM * 8 <= BM * PITCH * 4, "a wave's part of o_s, free until the waves are joined, holds a step's bits");
+    bits16* hidden = (bits16*)o_s[wave];  // [DIM][4]
+#pragma nounroll
+    for (uint32_t step = step0 + wave; step < step1; step += WAVES) {
+      const int32_t base = (int32_t)(t.begin + step * TOKENS);
+      if (!seen.step(base)) continue;
+      ids(step);
+      load_v(step);
+#pragma unroll
+      for (int i = 0; i < DT_TILES; ++i) hidden[(16 * i + c) * 4 + g] = hidden_bits(vw[i], not_finite_from(clamp_byte(vbyte)), base + 16 * (int32_t)g, seen);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      const uint64_t own = token_bits(see0 - base, see1 - base);
+#pragma unroll
+      for (int i = 0; i < DT_TILES; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (((const bits64*)hidden)[16 * i + 4 * g + e] & own) o[i][e] = __builtin_nanf("");
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+
   const uint64_t slot = (((uint64_t)r * a.kv_heads + h) * a.tiles + tile) * a.splits + split;
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
-  float worst = 0.f;
-#pragma unroll
-  for (int i = 0; i < DT_TILES * 4; ++i) worst += o[i / 4][i % 4] * 0.f;
-  if (__syncthreads_or(!(worst == 0.f) && l == l)) {
-    plain_rows<DT, DIM, WAVES>(a, t, h, r, t.begin + step0 * TOKENS, t.begin + step1 * TOKENS, shared, slot * BM);
-    return;
-  }
 
   // Join the waves.
   if (g == 0) m_s[wave][c] = m * a.factor, l_s[wave][c] = l;
@@ -550,7 +564,7 @@ __device__ __forceinline__ uint32_t key_turn(uint32_t key, uint32_t row_chunks) 
 }
 
 template <int DT, int DIM>
-__global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 ? 2 : 1) void many_rows_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, (DT == DT_BF16 && DIM <= 128) || DIM == 64 ? 2 : 1) void many_rows_kernel(AttnArgs a) {
   constexpr int WAVES = 4, THREADS = 64 * WAVES, BM = 32 * WAVES;
   constexpr int KSTEPS = DIM / 16, DT_TILES = DIM / 32;
   constexpr int KCHUNKS = DIM / 16;               // 16-byte chunks of a key
@@ -593,6 +607,8 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 ? 2 : 1) void many
       all0 = e1 > a.window ? e1 - a.window : 0;
     }
   }
+  const Mask seen(t, a);
+  uint32_t taken = 0;
   v8bf q[KSTEPS][QT];
   {
     const char* at = a.q[r] + (uint64_t)(t.row0 + qrow) * a.q_pitch + (uint64_t)qhead * (DIM * ES) + hf * 8 * ES;
@@ -687,7 +703,13 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 ? 2 : 1) void many
       kt[(ch % KCHUNKS * 2) ^ key_turn(kr, KROW)] = __builtin_bit_cast(uint4, widen8(kx[i].x, kx[i].y, ks));
       kt[(ch % KCHUNKS * 2 + 1) ^ key_turn(kr, KROW)] = __builtin_bit_cast(uint4, widen8(kx[i].z, kx[i].w, ks));
       uint4 w = vx[i];
-      if (base < t.lo || base > t.hi - (int32_t)TOKENS) w = clear_outside(w, base + 16 * (int32_t)(tid & 3), t.lo, t.hi);
+      if (seen.step(base)) {
+        const int32_t first = base + 16 * (int32_t)(tid & 3);
+        const uint32_t from = not_finite_from(clamp_byte(vbyte));
+        w = clear_outside(w, first, t.lo, t.hi);
+        if (not_finite(w.x, from) | not_finite(w.y, from) | not_finite(w.z, from) | not_finite(w.w, from))
+          w = clear_unseen(w, from, first, seen, &taken);
+      }
       uint4* vt = v_s[buf] + vr * 8;
       vt[(2 * (tid & 3)) ^ ((vr >> 1) & 7)] = __builtin_bit_cast(uint4, widen8(w.x, w.y, vs));
       vt[(2 * (tid & 3) + 1) ^ ((vr >> 1) & 7)] = __builtin_bit_cast(uint4, widen8(w.z, w.w, vs));
@@ -810,16 +832,30 @@ __global__ __launch_bounds__(256, DT == DT_BF16 && DIM <= 128 ? 2 : 1) void many
     }
   }
 
-  const uint64_t slot = ((((uint64_t)r * a.kv_heads + h) * a.tiles + tile) * a.splits + split) * BM;
-  l += __shfl_xor(l, 32);
-  float worst = 0.f;
+  if (__syncthreads_or(taken)) {
+    bits16* hidden = (bits16*)v_s;  // [DIM][4]
+#pragma nounroll
+    for (uint32_t step = step0; step < step1; ++step) {
+      const int32_t base = (int32_t)(t.begin + step * TOKENS);
+      if (!seen.step(base)) continue;
+      ids(step);
+      load(step);
+      __syncthreads();
 #pragma unroll
-  for (int i = 0; i < DT_TILES * 16; ++i) worst += o[i / 16][i % 16] * 0.f;
-  if (__syncthreads_or(!(worst == 0.f) && l == l)) {
-    plain_rows<DT, DIM, WAVES>(a, t, h, r, t.begin + step0 * TOKENS, t.begin + step1 * TOKENS, shared, slot);
-    return;
+      for (int i = 0; i < NC; ++i)
+        hidden[tid + i * THREADS] = hidden_bits(vx[i], not_finite_from(clamp_byte(vbyte)), base + 16 * (int32_t)(tid & 3), seen);
+      __syncthreads();
+      const uint64_t own = token_bits(see0 - base, see1 - base);
+#pragma unroll
+      for (int i = 0; i < DT_TILES; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (((const bits64*)hidden)[32 * i + 8 * (e / 4) + 4 * hf + e % 4] & own) o[i][e] = __builtin_nanf("");
+    }
   }
 
+  const uint64_t slot = ((((uint64_t)r * a.kv_heads + h) * a.tiles + tile) * a.splits + split) * BM;
+  l += __shfl_xor(l, 32);
   if (PT == 1) lr += __shfl_xor(lr, 32);
   else lr = l;
   if (!real) return;
