@@ -24,7 +24,9 @@ if that fails every call raises -- there is no CPU fallback.
 
 import ctypes
 import functools
+import importlib
 import os
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 # AR_LIBRARY points at another build of the same library (measurements only).
@@ -169,15 +171,29 @@ _MARSHAL = None  # the checks of the attention operators' tensors in C++ (csrc/m
 _DT_NAMES = None  # torch dtype -> "f32" / "bf16" / "i32"
 
 
+def _compiled_checks():
+    """csrc/marshal.cpp's module, or None: the same checks run in Python."""
+    from .build import checks_built_for
+    try:
+        found = importlib.import_module("._marshal", __package__)
+    except ModuleNotFoundError:
+        return None
+    except ImportError as e:
+        warnings.warn(f"_marshal.so does not load, the checks run in Python: {e}", RuntimeWarning, stacklevel=4)
+        return None
+    mark = getattr(found, "BUILT_FOR", "something else")
+    if mark != checks_built_for():
+        warnings.warn(f"_marshal.so was built for {mark}, the checks run in Python", RuntimeWarning, stacklevel=4)
+        return None
+    return found
+
+
 def _torch():
     global _TORCH, _DT_NAMES, _MARSHAL
     if _TORCH is None:
         import torch
 
-        try:
-            from . import _marshal as _MARSHAL  # noqa: N812
-        except ImportError:
-            pass  # the same checks in Python
+        _MARSHAL = _compiled_checks()
         _DT_NAMES = {torch.float32: "f32", torch.bfloat16: "bf16", torch.int32: "i32"}
         _TORCH = torch
     return _TORCH

@@ -32,14 +32,21 @@ def _hipcc():
     return path if os.path.exists(path) else "hipcc"
 
 
+def checks_built_for():
+    """What the compiled checks (_marshal.so) depend on, as they are marked."""
+    import torch
+    return f"torch {torch.__version__}, python {sys.version_info[0]}.{sys.version_info[1]}"
+
+
 def build_marshal(out: str = MARSHAL) -> str:
-    """Compile the binding's argument checks (host code against torch's headers)."""
+    """Compile the binding's argument checks (host code against torch's headers),
+    marked with the torch and Python they are for."""
     import torch
     root = os.path.dirname(torch.__file__)
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"]]
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           *[f"-I{i}" for i in inc], os.path.join(CSRC, "marshal.cpp"), "-L" + os.path.join(root, "lib"), "-ltorch_python",
+           f'-DBUILT_FOR="{checks_built_for()}"', *[f"-I{i}" for i in inc], os.path.join(CSRC, "marshal.cpp"), "-L" + os.path.join(root, "lib"), "-ltorch_python",
            "-ltorch_cpu", "-lc10", "-o", out + ".tmp"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
@@ -50,8 +57,9 @@ def build_marshal(out: str = MARSHAL) -> str:
 
 def build(verbose: bool = False, out: str = LIB, defines=()) -> str:
     """Compile every source and link the library (libar.so next to this file
-    unless `out` says otherwise); `defines` are extra -D options.  With the
-    library goes the binding's compiled half (_marshal.so)."""
+    unless `out` says otherwise); `defines` are extra -D options.  Beside it goes
+    the binding's compiled half (_marshal.so), which the binding does without
+    where it does not build (no g++, Python headers or torch)."""
     hipcc = _hipcc()
     with tempfile.TemporaryDirectory(prefix="ar_build_") as tmp:
         def compile_one(src):
@@ -67,14 +75,16 @@ def build(verbose: bool = False, out: str = LIB, defines=()) -> str:
         with ThreadPoolExecutor(len(SOURCES) + 1) as pool:
             checks = pool.submit(build_marshal) if out == LIB else None
             objs = list(pool.map(compile_one, SOURCES))
-            if checks:
-                checks.result()
         tmp_lib = out + ".tmp"
         cmd = [hipcc, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp_lib]
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stderr}")
         os.replace(tmp_lib, out)
+    if checks and checks.exception():
+        if os.path.exists(MARSHAL):  # of an earlier build
+            os.remove(MARSHAL)
+        sys.stderr.write(f"the binding's checks are not compiled, and run in Python: {checks.exception()}\n")
     return out
 
 

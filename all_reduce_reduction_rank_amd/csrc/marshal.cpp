@@ -139,4 +139,9 @@ PyModuleDef MODULE = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, METHODS, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal() { return PyModule_Create(&MODULE); }
+// BUILT_FOR: the torch and Python this was compiled against; the binding uses no other's.
+PyMODINIT_FUNC PyInit__marshal() {
+  PyObject* m = PyModule_Create(&MODULE);
+  if (m && PyModule_AddStringConstant(m, "BUILT_FOR", BUILT_FOR) != 0) Py_CLEAR(m);
+  return m;
+}
