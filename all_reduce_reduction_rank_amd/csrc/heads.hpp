@@ -82,8 +82,10 @@ __device__ __forceinline__ uint32_t first_row(const Paged& p, uint32_t s) {
 // items from base(s) = floor(first[s] * mul / div) + extra * s on, which leaves
 // it room for the ceil(n mul / div) + extra - 1 it may need.  The sequence of
 // an item is found by every wave on its own: its lanes look at 64 sequences at
-// a time and count those that start at or before the item, one memory latency
-// in all.  Returns seqs if no sequence owns the item; n = its rows, at = its entry
+// a time, first at every 64th part of those in question, and count the ones that
+// start at or before the item: one memory latency up to 64 sequences, two up to
+// 4096, four at most (65536 sequences of one token stored: 0.42 ms; with all of them
+// looked at in turn 22 ms).  Returns seqs if no sequence owns the item; n = its rows, at = its entry
 // of p.at, local = the item's number within the sequence.  (Where `first`
 // decreases the count names some sequence, whose rows are checked as any.)
 __device__ __forceinline__ uint64_t item_base(uint64_t first, uint32_t s, uint32_t mul, uint32_t div, uint32_t extra) {
@@ -93,31 +95,34 @@ __device__ __forceinline__ uint64_t item_base(uint64_t first, uint32_t s, uint32
 __device__ __forceinline__ uint32_t find_sequence(const Paged& p, uint64_t item, uint32_t mul, uint32_t div,
                                                   uint32_t extra, uint32_t* row0, uint32_t* n, uint64_t* local,
                                                   int32_t* at) {
-  uint32_t count = 0;
   const uint32_t lane = threadIdx.x & 63;
-  for (uint32_t s0 = 0; s0 < p.seqs; s0 += 64) {
-    const uint32_t s = s0 + lane;
-    // what the owner will need is loaded along, for the same latency
-    uint32_t a = 0, b = 0;
-    int32_t x = 0;
-    if (s < p.seqs) a = first_row(p, s), b = first_row(p, s + 1), x = p.at[s];
-    const uint64_t who = __ballot(s < p.seqs && item_base(a, s, mul, div, extra) <= item);
+  uint32_t s0 = 0, span = p.seqs;  // the owner is one of [s0, s0 + span)
+  while (span > 64) {
+    const uint32_t part = (span + 63) / 64, s = s0 + lane * part;
+    const uint64_t who = __ballot(lane * part < span && item_base(first_row(p, s), s, mul, div, extra) <= item);
     const uint32_t c = __popcll(who);
-    if (c) {
-      *row0 = __builtin_amdgcn_readlane(a, c - 1);
-      *n = __builtin_amdgcn_readlane(b, c - 1);
-      *at = __builtin_amdgcn_readlane(x, c - 1);
-    }
-    count += c;
-    if (c < 64) break;  // bases do not decrease
+    if (!c) return p.seqs;
+    s0 += (c - 1) * part;
+    span -= (c - 1) * part;
+    if (span > part) span = part;
   }
-  if (!count || *n <= *row0) return p.seqs;
-  const uint32_t s = count - 1;
+  const uint32_t s = s0 + lane;
+  // what the owner will need is loaded along, for the same latency
+  uint32_t a = 0, b = 0;
+  int32_t x = 0;
+  if (lane < span) a = first_row(p, s), b = first_row(p, s + 1), x = p.at[s];
+  const uint32_t c = __popcll(__ballot(lane < span && item_base(a, s, mul, div, extra) <= item));
+  if (!c) return p.seqs;
+  *row0 = __builtin_amdgcn_readlane(a, c - 1);
+  *n = __builtin_amdgcn_readlane(b, c - 1);
+  *at = __builtin_amdgcn_readlane(x, c - 1);
+  if (*n <= *row0) return p.seqs;
+  const uint32_t owner = s0 + c - 1;
   *n -= *row0;
-  const uint64_t base = item_base(*row0, s, mul, div, extra);
+  const uint64_t base = item_base(*row0, owner, mul, div, extra);
   if (item < base) return p.seqs;
   *local = item - base;
-  return s;
+  return owner;
 }
 
 inline uint64_t item_count(uint64_t rows, uint64_t seqs, uint64_t mul, uint64_t div, uint64_t extra) {
