@@ -42,7 +42,7 @@ struct AttnArgs {
   const uint8_t* v_scale[MAX_RANKS];
   uint64_t q_pitch;  // bytes
   Paged p;
-  uint32_t kv_heads, heads, group;
+  uint32_t kv_heads, heads, group, nranks;
   uint32_t splits, min_steps;  // shares of a tile's tokens: at most `splits`, of at least `min_steps` steps
   uint32_t tiles;              // row tiles of a head (bound)
   // z in units of log2: factor * (q . k), factor > 0; a negative scale turns the
@@ -260,8 +260,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 || DT == DT_BF16 && DIM <= 1
   constexpr bool Q_LDS = QT > 1;
   __shared__ uint4 q_s[Q_LDS ? KSTEPS * QT * 64 : 1];
 
-  const uint32_t split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits;
-  const uint32_t h = blockIdx.y, r = blockIdx.z;
+  uint32_t r;
+  const uint32_t item = item_of(a.nranks, &r), split = item % a.splits, tile = item / a.splits, h = blockIdx.y;
   Tile t;
   if (!tile_of(a, tile, BM, &t)) return;
   const uint32_t per = share_steps(a, t.steps), step0 = split * per;
@@ -575,8 +575,11 @@ __global__ __launch_bounds__(256, (DT == DT_BF16 && DIM <= 128) || DIM == 64 ? 2
   __shared__ uint4 k_s[2][8 * DIM], v_s[2][8 * DIM];  // bf16
   __shared__ uint32_t there_s[2][4];                  // the 16-token blocks: on a page
 
-  const uint32_t columns = a.kv_heads * gridDim.y;  // (gridDim.y: ranks)
-  const uint32_t b = blockIdx.x + gridDim.x * blockIdx.y, column = b % columns, item = b / columns;
+  const uint32_t columns = a.kv_heads * a.nranks;
+  uint32_t b = blockIdx.x;
+  if (blockIdx.z) b += blockIdx.z * gridDim.x;  // (below 2^32: the host checks)
+  const uint32_t column = b % columns, item = b / columns;
+  if (item >= a.tiles * a.splits) return;
   const uint32_t h = column % a.kv_heads, r = column / a.kv_heads;
   const uint32_t split = item % a.splits, tile = a.tiles - 1 - item / a.splits;
   Tile t;
@@ -988,11 +991,13 @@ AttnPlan plan_of(const ar_kv_cache* c, uint64_t seqs, uint64_t rows, uint64_t wi
   return p;
 }
 
-ar_status check_heads(const ar_kv_cache* c, size_t rows, size_t heads, int dtype) {
+ar_status check_heads(const ar_kv_cache* c, size_t rows, size_t seqs, size_t heads, int dtype) {
   if (dtype < 0 || dtype > 2) return AR_ERR_INVALID;
   if (dtype == DT_I32) return AR_ERR_UNSUPPORTED;
   if (heads < 1 || heads % c->kv_heads) return AR_ERR_INVALID;
   if (heads > MAX_HEADS || rows * heads > LAYER_MAX_ROWS) return AR_ERR_TOO_LARGE;
+  // Tiles of every key head and rank are numbered in 32 bits.
+  if (seqs * c->kv_heads * c->nranks > (1ull << 31)) return AR_ERR_TOO_LARGE;
   return AR_OK;
 }
 
@@ -1003,7 +1008,7 @@ extern "C" {
 size_t ar_cache_attention_workspace(const ar_kv_cache* cache, size_t seqs, size_t rows, size_t width, size_t heads,
                                     size_t window, size_t max_rows, ar_dtype dtype) {
   if (check_cache(cache) != AR_OK || rows > LAYER_MAX_ROWS || seqs > (1ull << 20) || width > (1ull << 31) ||
-      width * cache->page >= (1ull << 31) || check_heads(cache, rows, heads, (int)dtype) != AR_OK || !rows || !seqs)
+      width * cache->page >= (1ull << 31) || check_heads(cache, rows, seqs, heads, (int)dtype) != AR_OK || !rows || !seqs)
     return 0;
   return (size_t)plan_of(cache, seqs, rows, width, heads, window, max_rows, (int)dtype).bytes();
 }
@@ -1014,7 +1019,7 @@ ar_status ar_cache_attention(const ar_kv_cache* cache, const void* const* q, siz
                              void* workspace, size_t workspace_bytes, ar_stream_t stream) {
   ar_status st = check_cache(cache);
   if (st == AR_OK) st = check_rows(cache, rows);
-  if (st == AR_OK) st = check_heads(cache, rows->rows, heads, (int)dtype);
+  if (st == AR_OK) st = check_heads(cache, rows->rows, rows->seqs, heads, (int)dtype);
   if (st != AR_OK) return st;
   if (!q || !out || causal < 0 || causal > 1 || (window && !causal) || !(fabsf(scale) < 1e38f)) return AR_ERR_INVALID;
   if (rows->rows == 0 || rows->seqs == 0) return AR_OK;
@@ -1045,6 +1050,7 @@ ar_status ar_cache_attention(const ar_kv_cache* cache, const void* const* q, siz
   a.p = paged_of(cache, rows);
   a.kv_heads = (uint32_t)cache->kv_heads;
   a.heads = (uint32_t)heads;
+  a.nranks = (uint32_t)n;
   a.group = (uint32_t)(heads / cache->kv_heads);
   a.splits = plan.splits;
   a.min_steps = plan.min_steps;
@@ -1056,8 +1062,9 @@ ar_status ar_cache_attention(const ar_kv_cache* cache, const void* const* q, siz
   a.window = (int32_t)umin(window, 0x7fffffff);
   a.part = (float*)workspace;
   a.stat = (float2*)((char*)workspace + plan.part_bytes);
-  const dim3 grid(plan.tiles * plan.splits, a.kv_heads, n), joins(plan.tiles * (plan.bm / JOIN_ROWS), a.kv_heads, n);
-  const dim3 wide(plan.tiles * plan.splits * a.kv_heads, n);
+  const Fold fold = fold_items((uint64_t)plan.tiles * plan.splits * (plan.few ? 1 : a.kv_heads * n), 64 * plan.waves);
+  const dim3 grid(fold.x, plan.few ? a.kv_heads : 1, plan.few ? fold.folds * n : fold.folds);
+  const dim3 joins(plan.tiles * (plan.bm / JOIN_ROWS), a.kv_heads, n);  // (few tiles, where they are shared)
   by_head_dim((int)dtype, cache->head_dim, [&](auto dt, auto dim) {
     constexpr int DT = decltype(dt)::value, DIM = decltype(dim)::value;
     if (plan.few) {
@@ -1067,7 +1074,7 @@ ar_status ar_cache_attention(const ar_kv_cache* cache, const void* const* q, siz
       } else {
         few_rows_kernel<DT, DIM, 4><<<grid, 256, 0, (hipStream_t)stream>>>(a);
       }
-    } else many_rows_kernel<DT, DIM><<<wide, 256, 0, (hipStream_t)stream>>>(a);
+    } else many_rows_kernel<DT, DIM><<<grid, 256, 0, (hipStream_t)stream>>>(a);
     if (plan.splits > 1) join_kernel<DT, DIM><<<joins, 256, 0, (hipStream_t)stream>>>(a, plan.bm);
   });
   return hipGetLastError() == hipSuccess ? AR_OK : AR_ERR_HIP;

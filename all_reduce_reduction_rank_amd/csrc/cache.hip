@@ -32,7 +32,7 @@ struct CacheArgs {
   uint8_t* scale[2][MAX_RANKS];
   uint64_t pitch[2];  // bytes from row to row
   Paged p;
-  uint32_t kv_heads;
+  uint32_t kv_heads, nranks;
 };
 
 // A workgroup's page: rows row .. row + (hi - lo) of the call are the page's
@@ -148,9 +148,10 @@ __global__ __launch_bounds__(THREADS) void write_kernel(CacheArgs a) {
   constexpr uint32_t PITCH = DIM + 4;                                                      // of a token's codes in LDS
   extern __shared__ uint8_t tile[];                                                        // values: [page][PITCH]
   __shared__ float maxima[THREADS / 64 + 1];
-  const uint32_t kind = blockIdx.y & 1, r = blockIdx.z, head = blockIdx.y >> 1;
+  const uint32_t kind = blockIdx.y & 1, head = blockIdx.y >> 1;
+  uint32_t r;
   Piece pc;
-  if (!piece_of(a.p, blockIdx.x, &pc)) return;
+  if (!piece_of(a.p, item_of(a.nranks, &r), &pc)) return;
   const uint32_t page = 1u << a.p.page_shift, count = pc.hi - pc.lo;
   const uint32_t lane = threadIdx.x % LANES, row = threadIdx.x / LANES;
   const char* x = a.x[kind][r] + (uint64_t)pc.row * a.pitch[kind] + (uint64_t)head * (DIM * ES) + lane * 8 * ES;
@@ -265,9 +266,10 @@ template <int DT, int DIM>
 __global__ __launch_bounds__(THREADS) void read_kernel(CacheArgs a) {
   constexpr uint32_t ES = DT == DT_BF16 ? 2 : 4, LANES = DIM / 8, ROWS = THREADS / LANES, PITCH = DIM + 4;
   extern __shared__ uint8_t tile[];
-  const uint32_t kind = blockIdx.y & 1, r = blockIdx.z, head = blockIdx.y >> 1;
+  const uint32_t kind = blockIdx.y & 1, head = blockIdx.y >> 1;
+  uint32_t r;
   Piece pc;
-  if (!piece_of(a.p, blockIdx.x, &pc)) return;
+  if (!piece_of(a.p, item_of(a.nranks, &r), &pc)) return;
   const uint32_t page = 1u << a.p.page_shift, count = pc.hi - pc.lo;
   const bool there = pc.id < a.p.pages;
   const uint32_t lane = threadIdx.x % LANES, row = threadIdx.x / LANES;
@@ -417,7 +419,9 @@ ar_status cache_call(const ar_kv_cache* c, const void* const* k, size_t k_stride
   a.pitch[1] = v_stride * es;
   a.p = paged_of(c, p);
   a.kv_heads = (uint32_t)c->kv_heads;
-  const dim3 grid((uint32_t)item_count(p->rows, p->seqs, 1, c->page, 2), 2 * (uint32_t)c->kv_heads, (uint32_t)c->nranks);
+  a.nranks = (uint32_t)c->nranks;
+  const Fold fold = fold_items(item_count(p->rows, p->seqs, 1, c->page, 2), THREADS);
+  const dim3 grid(fold.x, 2 * a.kv_heads, a.nranks * fold.folds);
   const uint32_t lds = (uint32_t)(c->page * (c->head_dim + 4));
   by_head_dim(dtype, c->head_dim, [&](auto dt, auto dim) {
     if (write) write_kernel<decltype(dt)::value, decltype(dim)::value><<<grid, THREADS, lds, stream>>>(a);

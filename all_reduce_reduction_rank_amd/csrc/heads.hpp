@@ -39,6 +39,27 @@ void by_head_dim(int dtype, uint64_t dim, F f) {
   else with(std::integral_constant<int, DT_F32>{});
 }
 
+// A launch may have fewer than 2^32 threads along x.  Work items beyond that go
+// along z, in `folds` layers of as many as x holds (the last one partly empty:
+// kernels check their items).
+struct Fold {
+  uint32_t x, folds;
+};
+
+inline Fold fold_items(uint64_t items, uint32_t threads) {
+  const uint64_t most = (1ull << 32) / threads - 1;
+  const uint64_t x = items < most ? items : most;
+  return {(uint32_t)x, (uint32_t)(x ? (items + x - 1) / x : 1)};
+}
+
+// z holds the ranks and the layers: a workgroup's item, and its rank in *r.
+__device__ __forceinline__ uint32_t item_of(uint32_t nranks, uint32_t* r) {
+  uint32_t item = blockIdx.x, z = blockIdx.z;
+  while (z >= nranks) z -= nranks, item += gridDim.x;
+  *r = z;
+  return item;
+}
+
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
 // Two floats to bf16, nearest even, NaN kept (one instruction).

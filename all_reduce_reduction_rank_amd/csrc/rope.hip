@@ -161,7 +161,10 @@ template <int DT, int DIM, bool PAIRS>
 __global__ __launch_bounds__(THREADS) void rope_kernel(RopeArgs a) {
   constexpr int L = DIM / E, ES = DT == DT_BF16 ? 2 : 4;
   extern __shared__ float2 table[];
-  const uint32_t t0 = blockIdx.x * a.tokens, half = a.rot / 2;
+  uint32_t group = blockIdx.x;
+  if (blockIdx.z) group += blockIdx.z * gridDim.x;
+  const uint32_t t0 = group * a.tokens, half = a.rot / 2;
+  if (t0 >= a.rows) return;
   const uint32_t n = min(a.tokens, a.rows - t0);
   const uint32_t heads = a.heads[0] + a.heads[1];
   const Share sh = share_of(threadIdx.x % L, a.rot, PAIRS);
@@ -413,7 +416,8 @@ ar_status ar_qk_norm_rope(int nranks, const void* const* q, size_t q_stride, con
   const uint32_t groups = (uint32_t)((rows + a.tokens - 1) / a.tokens);
   const uint64_t passes = (a.tokens * per_token + THREADS - 1) / THREADS;
   const uint32_t split = (uint32_t)umax(1, umin(passes, 512 / groups));
-  const dim3 grid(groups, split);
+  const Fold fold = fold_items(groups, THREADS);
+  const dim3 grid(fold.x, split, fold.folds);
   const uint32_t lds = a.tokens * (uint32_t)rot / 2 * 8;
   by_head_dim((int)dtype, head_dim, [&](auto dt, auto dim) {
     launch_forward<decltype(dt)::value, decltype(dim)::value>(a, grid, lds, (hipStream_t)stream);

@@ -573,7 +573,8 @@ size_t ar_cache_attention_workspace(const ar_kv_cache* cache, size_t seqs, size_
  * a row does not see hold, NaN among it, does not reach the row.
  * q[r] [rows, heads, head_dim] with q_stride; out[r] [rows, heads, head_dim];
  * lse NULL, or N fp32 buffers [rows, heads].  out[r] is what rank r multiplies
- * by its columns of the output projection.  window needs causal.  max_rows: no
+ * by its columns of the output projection.  window needs causal.  seqs *
+ * kv_heads * N at most 2^31 (AR_ERR_TOO_LARGE).  max_rows: no
  * sequence has more rows than this (0: unknown); it chooses kernels and changes
  * no result beyond the order of sums.  Sums, maxima and products with q are fp32
  * or better; with AR_BF16 the weights exp(z - m) are rounded to bf16 before they
