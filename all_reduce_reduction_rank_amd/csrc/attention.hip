@@ -110,15 +110,19 @@ __device__ __forceinline__ v8bf widen8(uint32_t lo, uint32_t hi, float scale) {
 __device__ __forceinline__ float low_of(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// x in TERMS bf16 terms: each holds what the ones before it left.
-template <int TERMS>
+// x in TERMS bf16 terms: each holds what the ones before it left.  WIDE: x may be any
+// fp32 number; those beyond bf16's largest would round to infinity and leave NaN, so
+// the first term stops there.
+template <int TERMS, bool WIDE = false>
 __device__ __forceinline__ void split8(float* x, v8bf* out) {
+  constexpr float MOST = 0x1.fep+127f;
 #pragma unroll
   for (int t = 0; t < TERMS; ++t) {
     v4u w;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+      if (WIDE && t == 0) w[i] = pack_bf16(__builtin_amdgcn_fmed3f(x[2 * i], -MOST, MOST), __builtin_amdgcn_fmed3f(x[2 * i + 1], -MOST, MOST));
+      else w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
       if (t + 1 < TERMS) x[2 * i] -= low_of(w[i]), x[2 * i + 1] -= high_of(w[i]);
     }
     out[t] = __builtin_bit_cast(v8bf, w);
@@ -301,7 +305,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 || DT == DT_BF16 && DIM <= 1
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] = -x[e];
         v8bf terms[QT];
-        split8<QT>(x, terms);
+        split8<QT, true>(x, terms);
 #pragma unroll
         for (int y = 0; y < QT; ++y) q_s[(s * QT + y) * 64 + lane] = __builtin_bit_cast(uint4, terms[y]);
       }
@@ -626,7 +630,7 @@ __global__ __launch_bounds__(256, (DT == DT_BF16 && DIM <= 128) || DIM == 64 ? 2
         if (a.flip)
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] = -x[e];
-        split8<QT>(x, q[s]);
+        split8<QT, true>(x, q[s]);
       }
     }
   }
