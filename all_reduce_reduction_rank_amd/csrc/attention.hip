@@ -583,8 +583,8 @@ __global__ __launch_bounds__(256, (DT == DT_BF16 && DIM <= 128) || DIM == 64 ? 2
   uint32_t b = blockIdx.x;
   if (blockIdx.z) b += blockIdx.z * gridDim.x;  // (below 2^32: the host checks)
   const uint32_t column = b % columns, item = b / columns;
-  if (item >= a.tiles * a.splits) return;
   const uint32_t h = column % a.kv_heads, r = column / a.kv_heads;
+  // (past the last item `tile` is beyond every sequence's)
   const uint32_t split = item % a.splits, tile = a.tiles - 1 - item / a.splits;
   Tile t;
   if (!tile_of(a, tile, BM, &t)) return;
@@ -640,22 +640,27 @@ __global__ __launch_bounds__(256, (DT == DT_BF16 && DIM <= 128) || DIM == 64 ? 2
   // term is off by up to 2^-9 of it; over lr a row that one token dominates has
   // that error in both and loses it.  lse goes by l.
   float m, l, lr;
-  uint32_t kid[NC], vid;  // pages of the step to load next
+  // Of the blocks of 16 tokens, lane by lane block tid % 4: the page of the step to
+  // load next, the scales of the one that is loaded (as the entries, not touched
+  // before their step).  A wave's chunk i of keys lies in one block and takes both
+  // from a lane that has them: held by every lane for its own chunks they were
+  // short of registers with heads of 256, and waited for where they moved.
+  uint32_t vid, kbyte, vbyte;
   uint4 kx[NC], vx[NC];
-  uint32_t kbyte[NC], vbyte;  // their scales; as the entries, not touched before their step
-  bool there;                 // block tid % 4 is on a page
+  bool there;  // block tid % 4 is on a page
+  const uint32_t wave64 = __builtin_amdgcn_readfirstlane(tid & ~63u);
+  auto key_block = [&](int i) { return (wave64 + i * THREADS) / DIM; };
   // A page of 64 tokens or more holds a whole step: one page, the same for
   // every thread, whose address scalar registers keep.
   const bool whole = a.p.page_shift >= 6;
   auto ids = [&](uint32_t step) {
     const uint64_t base = (uint64_t)t.begin + (uint64_t)step * TOKENS;
     vid = page_id(a.p, t.s, (whole ? base : base + 16 * (tid & 3)) >> a.p.page_shift);
-    if (whole) return;
-#pragma unroll
-    for (int i = 0; i < NC; ++i) kid[i] = page_id(a.p, t.s, (base + (tid + i * THREADS) / KCHUNKS) >> a.p.page_shift);
   };
   auto load = [&](uint32_t step) {
     const uint32_t base = t.begin + step * TOKENS, in_page = (1u << a.p.page_shift) - 1;
+    there = vid < a.p.pages;
+    kbyte = vbyte = 127;
     if (whole) {
       const uint32_t id = __builtin_amdgcn_readfirstlane(vid);
       if (id < a.p.pages) {
@@ -667,45 +672,39 @@ __global__ __launch_bounds__(256, (DT == DT_BF16 && DIM <= 128) || DIM == 64 ? 2
           kx[i] = ld16((const char*)kp + (tid + i * THREADS) * 16);
           vx[i] = ld16((const char*)vp + (((tid + i * THREADS) / 4) << a.p.page_shift) + 16 * (tid & 3));
         }
-        kbyte[0] = a.k_scale[r][(uint64_t)id * a.kv_heads + h];
+        kbyte = a.k_scale[r][(uint64_t)id * a.kv_heads + h];
         vbyte = a.v_scale[r][(uint64_t)id * a.kv_heads + h];
       } else {
 #pragma unroll
         for (int i = 0; i < NC; ++i) kx[i] = vx[i] = make_uint4(0, 0, 0, 0);
-        kbyte[0] = vbyte = 127;
       }
-#pragma unroll
-      for (int i = 1; i < NC; ++i) kbyte[i] = kbyte[0];
-      there = id < a.p.pages;
       return;
     }
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const uint32_t ch = tid + i * THREADS;
+      const uint32_t ch = tid + i * THREADS, id = __builtin_amdgcn_readlane(vid, key_block(i));
       kx[i] = make_uint4(0, 0, 0, 0);
-      kbyte[i] = 127;
-      if (kid[i] < a.p.pages) {
-        kbyte[i] = a.k_scale[r][(uint64_t)kid[i] * a.kv_heads + h];
-        kx[i] = ld16((const char*)a.k[r] + page_at(kid[i], a.kv_heads, h, page_bytes) +
-                     ((base + ch / KCHUNKS) & in_page) * DIM + ch % KCHUNKS * 16);
-      }
+      if (id < a.p.pages)
+        kx[i] = ld16((const char*)a.k[r] + page_at(id, a.kv_heads, h, page_bytes) + ((base + ch / KCHUNKS) & in_page) * DIM +
+                     ch % KCHUNKS * 16);
     }
-    there = vid < a.p.pages;
     const uint8_t* at = a.v[r] + page_at(there ? vid : 0, a.kv_heads, h, page_bytes) + ((base + 16 * (tid & 3)) & in_page);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       vx[i] = make_uint4(0, 0, 0, 0);
       if (there) vx[i] = ld16((const char*)at + (((tid + i * THREADS) / 4) << a.p.page_shift));
     }
-    vbyte = 127;
-    if (there) vbyte = a.v_scale[r][(uint64_t)vid * a.kv_heads + h];
+    if (there) {
+      kbyte = a.k_scale[r][(uint64_t)vid * a.kv_heads + h];
+      vbyte = a.v_scale[r][(uint64_t)vid * a.kv_heads + h];
+    }
   };
   auto store = [&](uint32_t step, uint32_t buf) {
     const int32_t base = (int32_t)(t.begin + step * TOKENS);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const uint32_t ch = tid + i * THREADS, kr = ch / KCHUNKS, vr = ch / 4;
-      const float ks = byte_scale(kbyte[i]), vs = byte_scale(vbyte);
+      const float ks = byte_scale(__builtin_amdgcn_readlane(kbyte, key_block(i))), vs = byte_scale(vbyte);
       uint4* kt = k_s[buf] + kr * KROW;
       kt[(ch % KCHUNKS * 2) ^ key_turn(kr, KROW)] = __builtin_bit_cast(uint4, widen8(kx[i].x, kx[i].y, ks));
       kt[(ch % KCHUNKS * 2 + 1) ^ key_turn(kr, KROW)] = __builtin_bit_cast(uint4, widen8(kx[i].z, kx[i].w, ks));

@@ -138,7 +138,7 @@ __device__ __forceinline__ uint32_t find_sequence(const Paged& p, uint64_t item,
   *n = __builtin_amdgcn_readlane(b, c - 1);
   *at = __builtin_amdgcn_readlane(x, c - 1);
   if (*n <= *row0) return p.seqs;
-  const uint32_t owner = s0 + c - 1;
+  const uint32_t owner = __builtin_amdgcn_readfirstlane(s0 + c - 1);
   *n -= *row0;
   const uint64_t base = item_base(*row0, owner, mul, div, extra);
   if (item < base) return p.seqs;
