@@ -1058,8 +1058,9 @@ ar_status ar_cache_attention(const ar_kv_cache* cache, const void* const* q, siz
   a.splits = plan.splits;
   a.min_steps = plan.min_steps;
   a.tiles = plan.tiles;
-  // (a factor of 0 would make NaN of what is masked; the smallest does the same to the rest)
-  a.factor = fmaxf(fabsf(scale * LOG2E), 1.17549435e-38f);
+  // (a factor of 0 would make NaN of what is masked; the smallest number there is makes
+  // scores of less than 1e-6, whatever the products)
+  a.factor = fmaxf(fabsf(scale * LOG2E), 0x1p-149f);
   a.flip = scale < 0.f ? 0x80008000u : 0u;
   a.causal = causal;
   a.window = (int32_t)umin(window, 0x7fffffff);
