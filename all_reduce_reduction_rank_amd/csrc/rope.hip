@@ -306,24 +306,25 @@ struct SumArgs {
   uint32_t blocks, dim;
 };
 
-// 32 values of one rank's and kind's dw: the workgroups' shares added in a fixed
-// order, 32 slices of them side by side, eight loads of a slice in flight.
+// 32 values of one rank's and kind's dw: the workgroups' shares, up to a thousand,
+// added in fp64 and in a fixed order, 32 slices of them side by side, eight loads of
+// a slice in flight.
 constexpr uint32_t SUM_DIMS = 32, SUM_SLICES = 32;
 
 template <int DT>
 __global__ __launch_bounds__(SUM_DIMS * SUM_SLICES) void rope_weight_kernel(SumArgs a) {
-  __shared__ float s[SUM_SLICES][SUM_DIMS];
+  __shared__ double s[SUM_SLICES][SUM_DIMS];
   const uint32_t kind = blockIdx.x, r = blockIdx.y, lane = threadIdx.x % SUM_DIMS, slice = threadIdx.x / SUM_DIMS;
   const uint32_t d = blockIdx.z * SUM_DIMS + lane;
   const float* p = a.part + ((uint64_t)r * 2 + kind) * a.blocks * a.dim + d;
-  float v = 0.f;
+  double v = 0.;
 #pragma unroll 8
   for (uint32_t b = slice; b < a.blocks; b += SUM_SLICES) v += p[(uint64_t)b * a.dim];
   s[slice][lane] = v;
   __syncthreads();
   if (slice == 0) {
     for (uint32_t i = 1; i < SUM_SLICES; ++i) v += s[i][lane];
-    Elem<DT>::stf(a.out[kind][r] + (uint64_t)d * Elem<DT>::size, v);
+    Elem<DT>::stf(a.out[kind][r] + (uint64_t)d * Elem<DT>::size, (float)v);
   }
 }
 
