@@ -787,8 +787,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, pos, freq, eps=1e-6, pairs=False, q_o
 
     q[r]: [rows, heads, head_dim], k[r]: [rows, kv_heads, head_dim], each row's
     heads side by side (views of one projection's result are fine);
-    q_weight, k_weight: [head_dim]; pos: int64 [rows]; freq: fp32 [rot / 2] (None:
-    no rotation).  k and k_weight None: queries alone, k_out is None.  q_out,
+    q_weight, k_weight: [head_dim], aligned to 16 bytes; pos: int64 [rows]; freq: fp32
+    [rot / 2] (None: no rotation).  k and k_weight None: queries alone, k_out is None.  q_out,
     k_out: contiguous, allocated when None.  head_dim 64, 128 or 256; fp32 and bf16."""
     n, device, dtype, dt, (rows, heads, kv, dim, rot), x, shared = _rope_inputs(q, k, q_weight, k_weight, pos, freq)
     qo = _rank_list(q_out, n, (rows, heads, dim), dtype, device, "q_out") if q_out is not None else None
@@ -945,8 +945,8 @@ def _cache_ranks(cache, n, device, what):
 def cache_read(cache, table, first, start, k, v, stream=None):
     """ar_cache_read: (k, v) filled with tokens read back from the cache.
 
-    k[r], v[r]: contiguous [rows, kv_heads, head_dim], fp32 or bf16 (exact in
-    both); rows first[s] .. first[s + 1] - 1 receive the tokens of sequence s from
+    k[r], v[r]: contiguous [rows, kv_heads, head_dim], fp32 or bf16 (exact but at
+    the ends of the range, ar.h); rows first[s] .. first[s + 1] - 1 receive the tokens of sequence s from
     position start[s] on, zeros where the table names no page."""
     n, device, dt = _layer_ranks(k, "k")
     _cache_ranks(cache, n, device, "k")
@@ -980,8 +980,10 @@ def cache_attention(q, cache, table, first, length, scale=None, causal=True, win
     among them: the last row stands at position length - 1.  causal False:
     every row sees all of them (an encoder's states).  window: with causal, a row
     sees the last `window` positions up to its own (0: all).  scale: 1 /
-    sqrt(head_dim) when None.  max_rows: the most rows a sequence has, where
-    the caller knows (it spares a launch).  lse: None, or N fp32 tensors
+    sqrt(head_dim) when None.  max_rows: the rows the longest sequence is expected to
+    have (0: the mean of the call counts); it chooses the kernel, and with bf16 whether the
+    softmax weights enter the product with v in two bf16 terms (up to 96 rows of a key
+    head) or in one.  lse: None, or N fp32 tensors
     [rows, heads] that receive the log of the softmax denominators.  Rows that
     see nothing have out 0 and lse minus infinity."""
     n, device, dt = _layer_ranks(q, "q")

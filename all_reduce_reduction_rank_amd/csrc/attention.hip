@@ -546,7 +546,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 || DT == DT_BF16 && DIM <= 1
 // waits of two waves per SIMD that share both.  The codes are widened once, on
 // their way into LDS; widened by every wave from codes in LDS they cost more
 // than the larger LDS reads (prompt of 8192 tokens, 40 heads of 128: 941 us, 815
-// now, 0.84 PFLOP/s).  The e4m3 instructions with block scales would take the keys' codes
+// so; 795 to 830 by the machine's clock now, 0.83 to 0.87 PFLOP/s).  The e4m3 instructions with block scales would take the keys' codes
 // as they are, but their sums over 64 products keep fewer than fp32's bits
 // (scores off by 2^-18 of their terms' size, measured).  A step of 64 tokens is
 // loaded to registers one step ahead and stored to the other of two LDS buffers.
@@ -637,7 +637,8 @@ __global__ __launch_bounds__(256, (DT == DT_BF16 && DIM <= 128) || DIM == 64 ? 2
 
   v16f o[DT_TILES];
   // l: sum of the weights; lr: of the weights as they are multiplied.  One bf16
-  // term is off by up to 2^-9 of it; over lr a row that one token dominates has
+  // term is off by up to 2^-8 of it (a second one costs a quarter of the kernel's time:
+  // prompt of 8192 tokens 829 -> 1065 us); over lr a row that one token dominates has
   // that error in both and loses it.  lse goes by l.
   float m, l, lr;
   // Of the blocks of 16 tokens, lane by lane block tid % 4: the page of the step to
@@ -945,9 +946,10 @@ AttnPlan plan_of(const ar_kv_cache* c, uint64_t seqs, uint64_t rows, uint64_t wi
   // Packed rows of a sequence: by the caller's word, or the mean.  Either kernel is
   // right for any number.  Tiles of 16 rows read the codes again for each 16, from
   // L2 beyond the first, and multiply twice; tiles of 128 are mostly empty with few
-  // rows and start slowly.  (90 fp32 rows: 17 us against 46; 80 bf16 rows over 9000
-  // tokens: 37 against 50; 32 sequences of 100 rows over 4000 tokens: 266 against
-  // 184; 2 sequences of 100 rows over 200 tokens: 9 against 17.)
+  // rows and start slowly.  (90 fp32 rows: 18 us against 45; 80 bf16 rows over 9000
+  // tokens: 38 against 50; 32 sequences of 100 rows over 4000 tokens: 271 against
+  // 159; 2 sequences of 100 rows over 200 tokens: 10 against 17.)  The table's width
+  // stands for the lengths, which only the device knows.
   const uint64_t packed = (max_rows ? umin(max_rows, rows) : (rows + seqs - 1) / seqs) * group;
   const bool small = (rows * group / 16 + seqs) * columns <= 512 && width * c->page <= 1024;
   p.few = packed <= 96 || small;
@@ -971,9 +973,12 @@ AttnPlan plan_of(const ar_kv_cache* c, uint64_t seqs, uint64_t rows, uint64_t wi
     const uint64_t want = real < round / 2 ? round : 2 * round;
     p.splits = (uint32_t)umin(most_splits, (want + real - 1) / real);
     // Half a GPU's worth of tiles over not many tokens: eight waves of one workgroup
-    // instead of a few workgroups and a second kernel to join them (16 sequences of
-    // up to 2000 tokens, 8 key heads of 128: 25 us shared, 20 so; with 8 tiles the
-    // CUs' own bandwidth is short: 15 us shared, 19 so).
+    // instead of a few workgroups and a second kernel to join them.  (Measured with 8 to
+    // 480 tiles of heads of 64 and 128 over 2000 tokens: 128 tiles of 128 27 us shared, 21
+    // so, 192 tiles 35 and 23, of 64 17 and 16, 21 and 17; equal within 4 % with 64
+    // and 96 tiles; with 8 and 32, where the CUs' own bandwidth is short, 15 shared, 19 so;
+    // with 480 tiles 49 and 59.  `real` counts a sequence's last tile up to twice: 176
+    // tiles of 64 count as 344, and are better shared, 18 us and 22.)
     // Not where eight waves would be short of registers.
     const bool fits = eight_waves_fit(dtype, c->head_dim);
     if (p.splits > 1 && fits && real > 64 && real <= 256 && steps <= 48) p.waves = 8, p.splits = 1;

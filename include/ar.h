@@ -462,7 +462,8 @@ ar_status ar_linear_cross_entropy_backward(int nranks, const float* grad_loss, c
  * from one row to the next (at least heads * head_dim, a multiple of 16
  * bytes, below 2^31), so queries, keys and values may stay where one
  * projection left them; the others are contiguous.  Vectors shared by all
- * ranks are DEVICE pointers, aligned to their elements.  head_dim is 64, 128 or
+ * ranks are DEVICE pointers, the norms' weights aligned to 16 bytes, the others to
+ * their elements.  head_dim is 64, 128 or
  * 256 (AR_ERR_UNSUPPORTED otherwise); heads is a multiple of kv_heads, at most
  * 1024; query head h reads key/value head h / (heads / kv_heads).  rows *
  * heads at most 2^30. */
@@ -474,8 +475,9 @@ ar_status ar_linear_cross_entropy_backward(int nranks, const float* grad_loss, c
  *   `rot` values turned by a(j): (y_j cos a - y_j' sin a, y_j' cos a + y_j sin a)
  * pairs 0: j' = j + rot / 2, j < rot / 2;  pairs 1: neighbours 2 j, 2 j + 1.
  * weight: head_dim elements, one vector for queries and one for keys.
- * pos: `rows` int64; freq: rot / 2 floats; the angle is computed in fp64, the
- * rest in fp32, rounded once.  rot: a multiple of 16, 0 to head_dim (0: norms
+ * pos: `rows` int64; freq: rot / 2 floats; pos * freq is formed in fp64, what it
+ * has beyond whole turns is rounded to fp32 (an angle is off by at most 1e-7), and
+ * the rest is fp32, rounded once.  rot: a multiple of 16, 0 to head_dim (0: norms
  * alone; freq and pos may be NULL).  kv_heads may be 0 here (queries alone;
  * k, k_weight and k_out may be NULL), and heads need not be a multiple of it. */
 ar_status ar_qk_norm_rope(int nranks, const void* const* q, size_t q_stride, const void* const* k, size_t k_stride,
@@ -493,7 +495,8 @@ size_t ar_qk_norm_rope_workspace(int nranks, size_t rows, size_t heads, size_t k
  *   dweight[r] = sum over rows and heads of g * n
  * dq, dk have strides as q and k do, and may be the columns of one matrix.
  * dq_weight[r], dk_weight[r] are rank r's partial sums (an all-reduce
- * completes them), summed in fp32 in a fixed order and rounded once.  rows 0:
+ * completes them), summed in a fixed order, in fp32 within a workgroup and in fp64
+ * over them, and rounded once.  rows 0:
  * the weight gradients become zeros. */
 ar_status ar_qk_norm_rope_backward(int nranks, const void* const* dq_out, const void* const* dk_out,
                                    const void* const* q, size_t q_stride, const void* const* k, size_t k_stride,
@@ -510,8 +513,10 @@ ar_status ar_qk_norm_rope_backward(int nranks, const void* const* dq_out, const 
  *            7, 3 mantissa bits, largest value 448, 0x7f and 0xff: NaN)
  *   v        [pages, kv_heads, head_dim, page]  e4m3 codes, tokens fastest
  *   k_scale, v_scale  [pages, kv_heads]  one byte b for each page and head
- * A code c stands for value(c) * 2^(b - 127).  Scales are powers of two, so a
- * page whose scale grows keeps the bits of all but its smallest values.  pages at
+ * A code c stands for value(c) * 2^(b - 127), with b 1 to 254 (a byte of 0 counts
+ * as 1, 255 as 254).  Scales are powers of two, so a page whose scale grows keeps
+ * the bits of all but its smallest values.  (Magnitudes of 2^128 and more, beyond
+ * fp32, need a byte of 247 or more: fp32's very largest are rounded up to it.)  pages at
  * most 2^31 - 1, pages * kv_heads * page * head_dim below 2^47. */
 typedef struct {
   void* const* k;
@@ -553,8 +558,10 @@ ar_status ar_cache_write(const ar_kv_cache* cache, const void* const* k, size_t 
                          size_t v_stride, const ar_paged_rows* rows, ar_dtype dtype, ar_stream_t stream);
 
 /* Reads tokens back: row first[s] + i of k[r] and v[r] ([rows, kv_heads,
- * head_dim], contiguous) receives token at[s] + i of sequence s, exact in either
- * dtype; zeros for tokens beyond width * page or on no page. */
+ * head_dim], contiguous) receives token at[s] + i of sequence s: exact where the
+ * dtype has the number, which leaves out 2^128 and above (infinity) and, in AR_BF16,
+ * what scale bytes 1 and 2 hold below 2^-126 (the nearest); zeros for tokens beyond
+ * width * page or on no page. */
 ar_status ar_cache_read(const ar_kv_cache* cache, void* const* k, void* const* v, const ar_paged_rows* rows,
                         ar_dtype dtype, ar_stream_t stream);
 
@@ -570,15 +577,20 @@ size_t ar_cache_attention_workspace(const ar_kv_cache* cache, size_t seqs, size_
  *          causal 0: all;  causal 1: j <= P and, with window > 0, j > P - window
  *   lse = log sum_j exp(z[j]);  out = sum_j exp(z[j] - lse) v[j]
  * A row that sees no token has out 0 and lse minus infinity.  What tokens that
- * a row does not see hold, NaN among it, does not reach the row.
+ * a row does not see hold, NaN among it, does not reach the row; where one that it
+ * sees holds NaN or a magnitude of 2^128 or more, out is no finite number.
  * q[r] [rows, heads, head_dim] with q_stride; out[r] [rows, heads, head_dim];
  * lse NULL, or N fp32 buffers [rows, heads].  out[r] is what rank r multiplies
  * by its columns of the output projection.  window needs causal.  seqs *
- * kv_heads * N at most 2^31 (AR_ERR_TOO_LARGE).  max_rows: no
- * sequence has more rows than this (0: unknown); it chooses kernels and changes
- * no result beyond the order of sums.  Sums, maxima and products with q are fp32
- * or better; with AR_BF16 the weights exp(z - m) are rounded to bf16 before they
- * are multiplied by v (a second term holds the rest where rows are few). */
+ * kv_heads * N at most 2^31 (AR_ERR_TOO_LARGE).  max_rows: the
+ * rows that the longest sequence is expected to have (0: unknown, and the mean of the
+ * call counts).  It chooses between two kernels, of which either is right for any
+ * number: one for up to 96 rows of a key head (max_rows * heads / kv_heads), or for small
+ * calls, and one for more.  Sums, maxima and products with q are fp32 or better in
+ * both.  With AR_BF16 the weights exp(z - m) are multiplied by v in two bf16 terms
+ * (2^-16 of a weight) by the first kernel and in one (2^-8) by the second, so max_rows, or
+ * else the mean of what is in the call, decides that too; max_rows 1 keeps every call
+ * at two terms (prompts at 1.7 to 2.7 times the time). */
 ar_status ar_cache_attention(const ar_kv_cache* cache, const void* const* q, size_t q_stride,
                              const ar_paged_rows* rows, void* const* out, float* const* lse, size_t heads,
                              float scale, int causal, size_t window, size_t max_rows, ar_dtype dtype,
