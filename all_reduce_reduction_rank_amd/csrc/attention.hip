@@ -964,6 +964,7 @@ AttnPlan plan_of(const ar_kv_cache* c, uint64_t seqs, uint64_t rows, uint64_t wi
   p.waves = 4;
   const uint64_t most_splits = umax(1, (steps + p.min_steps - 1) / p.min_steps);
   // Workgroups that are resident together: two per CU, one where registers are short.
+  // (Of 64 bf16 values a head three may be; shares for two were measured.)
   const uint64_t round = eight_waves_fit(dtype, c->head_dim) ? 512 : 256;
   if (p.few) {
     // One round of them if the tiles are few, else two: shares that fill a round

@@ -566,7 +566,8 @@ ar_status ar_cache_read(const ar_kv_cache* cache, void* const* k, void* const* v
                         ar_dtype dtype, ar_stream_t stream);
 
 /* Workspace bytes of ar_cache_attention; 0 for arguments it refuses, and where
- * it needs none. */
+ * it needs none.  It goes by width * page, which stands for the lengths here: a
+ * table cut to what its longest sequence needs takes less and is shared better. */
 size_t ar_cache_attention_workspace(const ar_kv_cache* cache, size_t seqs, size_t rows, size_t width, size_t heads,
                                     size_t window, size_t max_rows, ar_dtype dtype);
 
